@@ -1,0 +1,168 @@
+/*
+ * gemm_moe.h -- C ABI of the mixture-of-experts operators: tokens sorted by
+ * expert and back, with weights applied, and one product per expert.
+ *
+ * A layer of E experts gives each of T tokens to k of them.  The T * k
+ * (token, choice) pairs are its slots, slot t * k + j for choice j of token t.
+ * In expert order the slots of expert 0 come first, then those of expert 1,
+ * and so on, in slot order within an expert; row r of that order belongs to
+ * expert e when offsets[e] <= r < offsets[e + 1].  A layer is
+ *
+ *   gemm_moe_sort      choices -> offsets, rows (slot -> row), slots (row -> slot)
+ *   gemm_moe_dispatch  token rows -> expert rows
+ *   gemm_grouped_run   one product per expert (GEMM_GROUPED_ROWS), as often as
+ *                      the experts have layers
+ *   gemm_moe_combine   expert rows -> token rows, weighted
+ *
+ * and its gradient gemm_moe_combine_grad, gemm_grouped_run (ROWS with the
+ * other layout of B for the rows, INNER for the experts' matrices) and
+ * gemm_moe_dispatch_grad.  Group sizes stay on the device: no call reads them
+ * back, so a layer can be captured into a CUDA graph.
+ *
+ * Conventions, beyond those of gemm.h (status codes, stream semantics and
+ * dependent launches are the same):
+ *  - A slot whose choice is outside [0, E) is dropped: its rows entry is -1,
+ *    it takes no row, and it contributes nothing (its weight and whatever an
+ *    unused row holds are not read).  Rows from offsets[E] on are unused; an
+ *    operator that writes rows writes them as +0.
+ *  - Row matrices have a leading dimension in elements (ldx and so on), at
+ *    least the row length.  Any alignment of the 16-bit element is accepted;
+ *    16-byte aligned rows are faster.  Offsets, rows, slots and the weights are
+ *    contiguous.
+ *  - Sums are in fp32, in ascending choice order, rounded once; results do
+ *    not depend on timing (no floating-point atomics).
+ *  - The functions without a plan run on the current CUDA device, which must
+ *    be the one that holds their operands.
+ *  - Inputs and outputs must not overlap.
+ */
+#ifndef PSM_GEMM_MOE_H
+#define PSM_GEMM_MOE_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { GEMM_INDEX_I32 = 0, GEMM_INDEX_I64 = 1 } gemm_index_t;
+
+/* The most experts (groups) any call takes. */
+#define GEMM_MOE_MAX_EXPERTS 1024
+
+/*
+ * Bytes of device workspace gemm_moe_sort needs for these sizes (may be 0).
+ * Its contents need no initialisation.  Errors: as gemm_moe_sort for the
+ * sizes, INVALID_ARG for a NULL bytes.
+ */
+gemm_status_t gemm_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts,
+                                           size_t *bytes);
+
+/*
+ * Sort the slots by expert, stably.  ids: tokens x topk choices of type
+ * id_type, token t at ids + t * ld_ids.  Writes offsets (experts + 1), rows
+ * (tokens * topk: the row of each slot, -1 when dropped) and slots (tokens *
+ * topk: the slot of each row, -1 for unused rows), each in full.
+ * tokens == 0: only offsets is written, as zeros.
+ * Errors: INVALID_ARG (NULL operand, negative size, topk < 1, experts < 1,
+ * ld_ids < topk, bad id_type), UNSUPPORTED (experts > GEMM_MOE_MAX_EXPERTS,
+ * tokens * topk > 2^31 - 1024, an operand not aligned to its element),
+ * WORKSPACE (NULL or not 16-byte aligned while one is needed), LAUNCH.
+ */
+gemm_status_t gemm_moe_sort(const void *ids, gemm_index_t id_type, int64_t ld_ids, int64_t tokens,
+                            int64_t topk, int64_t experts, int32_t *offsets, int32_t *rows,
+                            int32_t *slots, void *workspace, gemm_stream_t stream);
+
+/*
+ * xs[rows[t * topk + j]] = x[t] for every slot that is kept, and +0 in the
+ * unused rows.  x: tokens x hidden; xs: (tokens * topk) x hidden; rows and
+ * slots as gemm_moe_sort wrote them.
+ * Errors (this and the next three): INVALID_ARG (NULL operand, negative size,
+ * topk < 1, a leading dimension below hidden, bad dtype), UNSUPPORTED (tokens *
+ * topk > 2^31 - 1024, hidden > 2^31 - 1024, an operand not aligned to its
+ * element), LAUNCH.  tokens == 0 or hidden == 0: an empty output is left
+ * alone.
+ */
+gemm_status_t gemm_moe_dispatch(const void *x, int64_t ldx, const int32_t *rows,
+                                const int32_t *slots, int64_t tokens, int64_t topk, int64_t hidden,
+                                gemm_dtype_t dtype, void *xs, int64_t ldxs, gemm_stream_t stream);
+
+/* Gradient of gemm_moe_dispatch: dx[t] = the sum over j of
+ * dxs[rows[t * topk + j]]; +0 for a token whose slots are all dropped. */
+gemm_status_t gemm_moe_dispatch_grad(const void *dxs, int64_t lddxs, const int32_t *rows,
+                                     int64_t tokens, int64_t topk, int64_t hidden,
+                                     gemm_dtype_t dtype, void *dx, int64_t lddx,
+                                     gemm_stream_t stream);
+
+/* y[t] = the sum over j of weights[t * topk + j] * ys[rows[t * topk + j]];
+ * weights: tokens x topk fp32. */
+gemm_status_t gemm_moe_combine(const void *ys, int64_t ldys, const int32_t *rows,
+                               const float *weights, int64_t tokens, int64_t topk, int64_t hidden,
+                               gemm_dtype_t dtype, void *y, int64_t ldy, gemm_stream_t stream);
+
+/* Gradients of gemm_moe_combine for dy (tokens x hidden): dys[r] = weights[s]
+ * * dy[s / topk] for the slot s of each row, +0 in the unused rows; dweights[s]
+ * = dy[s / topk] . ys[rows[s]] in fp32, +0 for a dropped slot. */
+gemm_status_t gemm_moe_combine_grad(const void *dy, int64_t lddy, const void *ys, int64_t ldys,
+                                    const int32_t *rows, const int32_t *slots,
+                                    const float *weights, int64_t tokens, int64_t topk,
+                                    int64_t hidden, gemm_dtype_t dtype, void *dys, int64_t lddys,
+                                    float *dweights, gemm_stream_t stream);
+
+/* ------------------------------------------------------------ grouped products */
+
+typedef enum {
+    /* C[r] = A[r] * B_g for the rows r of each group g; +0 in the unused rows. */
+    GEMM_GROUPED_ROWS = 0,
+    /* C_g = the sum over the rows r of group g of A[r]^T * B[r], the gradient
+     * of ROWS to its B for A and the gradient of its C; +0 for an empty group. */
+    GEMM_GROUPED_INNER = 1
+} gemm_grouped_kind_t;
+
+typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
+
+/*
+ * Create a plan for `groups` products over `rows` rows in all, on the current
+ * device.  In both kinds A is rows x K row-major.
+ *   ROWS   B: groups matrices of K x N in layout_b, one after another;
+ *          C: rows x N row-major.
+ *   INNER  B: rows x N row-major; C: groups matrices of K x N in layout_b.
+ * A, B and C have one 16-bit type; accumulation is fp32, rounded once.  The
+ * sizes of the groups are given to each run, on the device.
+ * K and N must be multiples of 8 and the operands 16-byte aligned, as for
+ * gemm_run.  A plan is not thread-safe.
+ * Errors: INVALID_ARG (NULL out, groups < 1, another negative size, bad enum),
+ * UNSUPPORTED (groups > GEMM_MOE_MAX_EXPERTS, rows, N or K > 2^31 - 1024, K or
+ * N not a multiple of 8), NO_DEVICE, CUDA.
+ */
+gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, gemm_grouped_kind_t kind,
+                                       int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                       gemm_dtype_t dtype, gemm_layout_t layout_b);
+
+/* Bytes of device workspace gemm_grouped_run needs (may be 0).  Its contents
+ * need no initialisation; two runs that share it must not overlap in time.
+ * Errors: INVALID_ARG. */
+gemm_status_t gemm_grouped_workspace_size(gemm_grouped_plan_t plan, size_t *bytes);
+
+/*
+ * Run the products on `stream`, asynchronously.  offsets: groups + 1 device
+ * int32, ascending, at most `rows` (gemm_moe_sort writes such); a value out of
+ * order or range is taken as the nearest one in order and range, so no
+ * access leaves the operands.  C is written in full.
+ * Errors: INVALID_ARG (NULL plan, or a NULL operand that is not empty),
+ * UNSUPPORTED (alignment), WORKSPACE (NULL or not 16-byte aligned while one is
+ * needed), CUDA, LAUNCH.
+ */
+gemm_status_t gemm_grouped_run(gemm_grouped_plan_t plan, const void *A, const void *B, void *C,
+                               const int32_t *offsets, void *workspace, gemm_stream_t stream);
+
+/* As gemm_last_status, for a grouped plan. */
+gemm_status_t gemm_grouped_last_status(gemm_grouped_plan_t plan, gemm_stream_t stream);
+
+/* Free the plan.  NULL is accepted.  Always returns GEMM_OK. */
+gemm_status_t gemm_grouped_plan_destroy(gemm_grouped_plan_t plan);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PSM_GEMM_MOE_H */

@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/gemm.h.
+"""ctypes binding of the C ABI in include/gemm.h and include/gemm_moe.h.
 
 Argument marshalling only: every step of the product runs in the CUDA
 library.  The functions keep the C names; a non-OK status raises GemmError.
@@ -49,10 +49,14 @@ INFO = {
     "l2_prefetch": 20, "pair_mma": 21, "schedule": 22, "sk_mode": 23, "raster": 24, "host_chunks": 25, "host_col_chunks": 26,
     "split_k_cluster": 27, "clusters_resident": 28, "early_prefetch": 29,
 }
+GEMM_INDEX_I32, GEMM_INDEX_I64 = 0, 1
+GEMM_GROUPED_ROWS, GEMM_GROUPED_INNER = 0, 1
+GEMM_MOE_MAX_EXPERTS = 1024
+
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3
 TRACE_STAMPS = 6   # uint64 per CTA written by gemm_plan_set_trace: 4 timer + 2 clock stamps
 
-# every entry point of include/gemm.h: name -> (restype, argtypes)
+# every entry point of the headers: name -> (restype, argtypes)
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
 _pp = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = {
@@ -71,6 +75,18 @@ SIGNATURES = {
     "gemm_plan_set_trace": (_i32, [_vp, _vp, ctypes.c_size_t]),
     "gemm_plan_destroy": (_i32, [_vp]),
     "gemm_status_string": (ctypes.c_char_p, [_i32]),
+    "gemm_moe_sort_workspace_size": (_i32, [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "gemm_moe_sort": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "gemm_moe_dispatch": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp]),
+    "gemm_moe_dispatch_grad": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp]),
+    "gemm_moe_combine": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp]),
+    "gemm_moe_combine_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
+                                     _vp, _i64, _vp, _vp]),
+    "gemm_grouped_plan_create": (_i32, [_pp, _i32, _i64, _i64, _i64, _i64, _i32, _i32]),
+    "gemm_grouped_workspace_size": (_i32, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
+    "gemm_grouped_run": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gemm_grouped_last_status": (_i32, [_vp, _vp]),
+    "gemm_grouped_plan_destroy": (_i32, [_vp]),
 }
 
 _lib = None
@@ -263,6 +279,105 @@ class Plan:
     def close(self):
         if getattr(self, "handle", None):
             gemm_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def gemm_moe_sort_workspace_size(tokens, topk, experts) -> int:
+    v = ctypes.c_size_t()
+    _check(load().gemm_moe_sort_workspace_size(tokens, topk, experts, ctypes.byref(v)),
+           "gemm_moe_sort_workspace_size")
+    return v.value
+
+
+def gemm_moe_sort(ids, id_type, ld_ids, tokens, topk, experts, offsets, rows, slots, workspace=None,
+                  stream=None):
+    _check(load().gemm_moe_sort(_addr(ids), id_type, ld_ids, tokens, topk, experts, _addr(offsets),
+                                _addr(rows), _addr(slots), _addr(workspace), _stream(stream)),
+           "gemm_moe_sort")
+
+
+def gemm_moe_dispatch(x, ldx, rows, slots, tokens, topk, hidden, dtype, xs, ldxs, stream=None):
+    _check(load().gemm_moe_dispatch(_addr(x), ldx, _addr(rows), _addr(slots), tokens, topk, hidden,
+                                    dtype, _addr(xs), ldxs, _stream(stream)), "gemm_moe_dispatch")
+
+
+def gemm_moe_dispatch_grad(dxs, lddxs, rows, tokens, topk, hidden, dtype, dx, lddx, stream=None):
+    _check(load().gemm_moe_dispatch_grad(_addr(dxs), lddxs, _addr(rows), tokens, topk, hidden, dtype,
+                                         _addr(dx), lddx, _stream(stream)), "gemm_moe_dispatch_grad")
+
+
+def gemm_moe_combine(ys, ldys, rows, weights, tokens, topk, hidden, dtype, y, ldy, stream=None):
+    _check(load().gemm_moe_combine(_addr(ys), ldys, _addr(rows), _addr(weights), tokens, topk, hidden,
+                                   dtype, _addr(y), ldy, _stream(stream)), "gemm_moe_combine")
+
+
+def gemm_moe_combine_grad(dy, lddy, ys, ldys, rows, slots, weights, tokens, topk, hidden, dtype, dys,
+                          lddys, dweights, stream=None):
+    _check(load().gemm_moe_combine_grad(_addr(dy), lddy, _addr(ys), ldys, _addr(rows), _addr(slots),
+                                        _addr(weights), tokens, topk, hidden, dtype, _addr(dys), lddys,
+                                        _addr(dweights), _stream(stream)), "gemm_moe_combine_grad")
+
+
+def gemm_grouped_plan_create(kind, groups, rows, N, K, dtype, layout_b) -> int:
+    h = ctypes.c_void_p()
+    _check(load().gemm_grouped_plan_create(ctypes.byref(h), kind, groups, rows, N, K, dtype, layout_b),
+           "gemm_grouped_plan_create")
+    return h.value
+
+
+def gemm_grouped_workspace_size(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(load().gemm_grouped_workspace_size(plan, ctypes.byref(v)), "gemm_grouped_workspace_size")
+    return v.value
+
+
+def gemm_grouped_run(plan, A, B, C, offsets, workspace=None, stream=None):
+    _check(load().gemm_grouped_run(plan, _addr(A), _addr(B), _addr(C), _addr(offsets),
+                                   _addr(workspace), _stream(stream)), "gemm_grouped_run")
+
+
+def gemm_grouped_last_status(plan, stream=None) -> int:
+    """Returns the status code (GEMM_OK or GEMM_ERR_TIMEOUT ...); does not raise."""
+    return int(load().gemm_grouped_last_status(plan, _stream(stream)))
+
+
+def gemm_grouped_plan_destroy(plan):
+    _check(load().gemm_grouped_plan_destroy(plan), "gemm_grouped_plan_destroy")
+
+
+class GroupedPlan:
+    """Owning wrapper around a grouped plan handle (marshalling only)."""
+
+    def __init__(self, kind, groups, rows, N, K, dtype, layout_b):
+        self.kind, self.groups, self.rows, self.N, self.K = kind, groups, rows, N, K
+        self.dtype, self.layout_b = dtype, layout_b
+        self.handle = gemm_grouped_plan_create(kind, groups, rows, N, K, dtype, layout_b)
+
+    @property
+    def workspace_size(self) -> int:
+        return gemm_grouped_workspace_size(self.handle)
+
+    def run(self, A, B, C, offsets, workspace=None, stream=None):
+        gemm_grouped_run(self.handle, A, B, C, offsets, workspace, stream)
+
+    def last_status(self, stream=None) -> int:
+        return gemm_grouped_last_status(self.handle, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            gemm_grouped_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -10,10 +10,13 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpsm_gemm.so")
-SOURCES = [os.path.join(CSRC, "gemm.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "ptx.cuh", "sched.cuh")] + [
-    os.path.join(INCLUDE, "gemm.h")
-]
+# each translation unit and the headers it includes
+UNITS = {
+    "gemm.cu": ("gemm_kernel.cuh", "ptx.cuh", "sched.cuh", "gemm.h"),
+    "moe.cu": ("ptx.cuh", "gemm.h", "gemm_moe.h"),
+    "grouped.cu": ("ptx.cuh", "gemm.h", "gemm_moe.h"),
+}
+SOURCES = [os.path.join(CSRC, f) for f in UNITS]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -24,24 +27,40 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _header(name: str) -> str:
+    return os.path.join(CSRC if name.endswith(".cuh") else INCLUDE, name)
+
+
+def _stale(target: str, inputs) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in DEPENDS)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(f) > t for f in inputs)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if it is missing or older than its sources."""
-    if not force and not _stale():
-        return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-I" + INCLUDE, "-o", tmp, *SOURCES]
+    """Compile what is missing or older than its sources, the units in
+    parallel, and link the library."""
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+        flags.insert(0, "-Xptxas=-v")
+    suffix = ".tmp%d" % os.getpid()
+    objects, jobs = [], []
+    for source, headers in UNITS.items():
+        src = os.path.join(CSRC, source)
+        obj = src[:-3] + ".o"
+        objects.append(obj)
+        if force or _stale(obj, [src, *map(_header, headers)]):
+            cmd = [nvcc(), *flags, "-c", "-o", obj + suffix, src]
+            jobs.append((subprocess.Popen(cmd), cmd, obj))
+    failed = [cmd for job, cmd, _ in jobs if job.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    for _, _, obj in jobs:
+        os.replace(obj + suffix, obj)
+    if jobs or _stale(LIB, objects):
+        subprocess.check_call([nvcc(), *ARCH, "-shared", "-o", LIB + suffix, *objects])
+        os.replace(LIB + suffix, LIB)
     return LIB
 
 
