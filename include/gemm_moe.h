@@ -120,6 +120,23 @@ typedef enum {
 
 typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
 
+/* Options for gemm_grouped_plan_set_option (key, value). */
+enum {
+    /* CTAs of a scheduling unit: 1 (tiles of 128 x up to 128), or 2, a cluster
+     * that runs pair MMAs (256 x up to 256); 0 (default) lets the plan choose. */
+    GEMM_GROUPED_OPT_CTAS = 1
+};
+
+/* Keys for gemm_grouped_plan_get_info. */
+enum {
+    GEMM_GROUPED_INFO_CTAS = 1,    /* CTAs of a scheduling unit (1 or 2) */
+    GEMM_GROUPED_INFO_UNITS = 2,   /* scheduling units of a launch */
+    GEMM_GROUPED_INFO_TILE_M = 3,  /* tile extent along C's contiguous dimension */
+    GEMM_GROUPED_INFO_TILE_N = 4,  /* the largest extent along the other one */
+    GEMM_GROUPED_INFO_STAGES = 5,  /* depth of the shared-memory ring */
+    GEMM_GROUPED_INFO_SMEM_BYTES = 6
+};
+
 /*
  * Create a plan for `groups` products over `rows` rows in all, on the current
  * device.  In both kinds A is rows x K row-major.
@@ -132,11 +149,38 @@ typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
  * gemm_run.  A plan is not thread-safe.
  * Errors: INVALID_ARG (NULL out, groups < 1, another negative size, bad enum),
  * UNSUPPORTED (groups > GEMM_MOE_MAX_EXPERTS, rows, N or K > 2^31 - 1024, K or
- * N not a multiple of 8), NO_DEVICE, CUDA.
+ * N not a multiple of 8, 2^31 tiles or more), NO_DEVICE, CUDA.
  */
 gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, gemm_grouped_kind_t kind,
                                        int64_t groups, int64_t rows, int64_t N, int64_t K,
                                        gemm_dtype_t dtype, gemm_layout_t layout_b);
+
+/* Same, but touches no device: for inspection only, as if the device had
+ * num_sms SMs; gemm_grouped_run returns GEMM_ERR_NO_DEVICE.  Errors: as above,
+ * INVALID_ARG for num_sms < 2. */
+gemm_status_t gemm_grouped_plan_create_offline(gemm_grouped_plan_t *out, gemm_grouped_kind_t kind,
+                                               int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                               gemm_dtype_t dtype, gemm_layout_t layout_b,
+                                               int num_sms);
+
+/* Set one GEMM_GROUPED_OPT_* option.  On error the plan keeps its options.
+ * Errors: INVALID_ARG (NULL plan, unknown key), UNSUPPORTED (value). */
+gemm_status_t gemm_grouped_plan_set_option(gemm_grouped_plan_t plan, int key, int64_t value);
+
+/* Read one GEMM_GROUPED_INFO_* value.  Errors: INVALID_ARG. */
+gemm_status_t gemm_grouped_plan_get_info(gemm_grouped_plan_t plan, int key, int64_t *value);
+
+/*
+ * Host twin of the device scheduler: the work of scheduling unit `unit` for
+ * the HOST offsets given (groups + 1, ascending, at most rows), in order, 9
+ * int32 each: tile, group, tile along C's contiguous dimension, first row of
+ * the tile (of C for ROWS, of the group's matrix along its other dimension
+ * for INNER), rows stored, accumulator width, first and end k-block of 64,
+ * and the tile's k-blocks.  Writes at most max_units and the full count to
+ * *n_units.  Errors: INVALID_ARG.
+ */
+gemm_status_t gemm_grouped_plan_units(gemm_grouped_plan_t plan, const int32_t *offsets, int64_t unit,
+                                      int32_t *units, int64_t max_units, int64_t *n_units);
 
 /* Bytes of device workspace gemm_grouped_run needs (may be 0).  Its contents
  * need no initialisation; two runs that share it must not overlap in time.
@@ -150,7 +194,7 @@ gemm_status_t gemm_grouped_workspace_size(gemm_grouped_plan_t plan, size_t *byte
  * access leaves the operands.  C is written in full.
  * Errors: INVALID_ARG (NULL plan, or a NULL operand that is not empty),
  * UNSUPPORTED (alignment), WORKSPACE (NULL or not 16-byte aligned while one is
- * needed), CUDA, LAUNCH.
+ * needed), NO_DEVICE (offline plan), CUDA, LAUNCH.
  */
 gemm_status_t gemm_grouped_run(gemm_grouped_plan_t plan, const void *A, const void *B, void *C,
                                const int32_t *offsets, void *workspace, gemm_stream_t stream);

@@ -7,10 +7,12 @@ generator.  Loading the binding's functions fails loudly if the library is
 not built: there is no CPU fallback.
 """
 from ._binding import (  # noqa: F401
-    GEMM_BF16, GEMM_COL_MAJOR, GEMM_GROUPED_INNER, GEMM_GROUPED_ROWS, GEMM_INDEX_I32, GEMM_INDEX_I64,
+    GEMM_BF16, GEMM_COL_MAJOR, GEMM_GROUPED_INNER, GEMM_GROUPED_OPT_CTAS, GEMM_GROUPED_ROWS, GEMM_INDEX_I32, GEMM_INDEX_I64,
     GEMM_MOE_MAX_EXPERTS, GEMM_SCHED_AUTO, GEMM_F16, GEMM_ROW_MAJOR, GEMM_SCHED_DATA_PARALLEL,
     GEMM_SCHED_PERSISTENT, GEMM_SCHED_SPLITK, GEMM_SCHED_STREAMK, GemmError, GroupedPlan, Plan, SCHEDULES,
-    gemm_grouped_last_status, gemm_grouped_plan_create, gemm_grouped_plan_destroy, gemm_grouped_run,
+    gemm_grouped_last_status, gemm_grouped_plan_create, gemm_grouped_plan_create_offline,
+    gemm_grouped_plan_destroy, gemm_grouped_plan_get_info, gemm_grouped_plan_set_option,
+    gemm_grouped_plan_units, gemm_grouped_run,
     gemm_grouped_workspace_size, gemm_last_status, gemm_moe_combine, gemm_moe_combine_grad,
     gemm_moe_dispatch, gemm_moe_dispatch_grad, gemm_moe_sort, gemm_moe_sort_workspace_size,
     gemm_plan_create, gemm_plan_create_offline, gemm_plan_destroy, gemm_plan_get_info,

@@ -52,6 +52,8 @@ INFO = {
 GEMM_INDEX_I32, GEMM_INDEX_I64 = 0, 1
 GEMM_GROUPED_ROWS, GEMM_GROUPED_INNER = 0, 1
 GEMM_MOE_MAX_EXPERTS = 1024
+GEMM_GROUPED_OPT_CTAS = 1
+GROUPED_INFO = {"ctas": 1, "units": 2, "tile_m": 3, "tile_n": 4, "stages": 5, "smem_bytes": 6}
 
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3
 TRACE_STAMPS = 6   # uint64 per CTA written by gemm_plan_set_trace: 4 timer + 2 clock stamps
@@ -83,6 +85,11 @@ SIGNATURES = {
     "gemm_moe_combine_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
                                      _vp, _i64, _vp, _vp]),
     "gemm_grouped_plan_create": (_i32, [_pp, _i32, _i64, _i64, _i64, _i64, _i32, _i32]),
+    "gemm_grouped_plan_create_offline": (_i32, [_pp, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _i32]),
+    "gemm_grouped_plan_set_option": (_i32, [_vp, _i32, _i64]),
+    "gemm_grouped_plan_get_info": (_i32, [_vp, _i32, ctypes.POINTER(_i64)]),
+    "gemm_grouped_plan_units": (_i32, [_vp, ctypes.POINTER(ctypes.c_int32), _i64,
+                                       ctypes.POINTER(ctypes.c_int32), _i64, ctypes.POINTER(_i64)]),
     "gemm_grouped_workspace_size": (_i32, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
     "gemm_grouped_run": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "gemm_grouped_last_status": (_i32, [_vp, _vp]),
@@ -337,6 +344,38 @@ def gemm_grouped_plan_create(kind, groups, rows, N, K, dtype, layout_b) -> int:
     return h.value
 
 
+def gemm_grouped_plan_create_offline(kind, groups, rows, N, K, dtype, layout_b, num_sms) -> int:
+    h = ctypes.c_void_p()
+    _check(load().gemm_grouped_plan_create_offline(ctypes.byref(h), kind, groups, rows, N, K, dtype,
+                                                   layout_b, num_sms),
+           "gemm_grouped_plan_create_offline")
+    return h.value
+
+
+def gemm_grouped_plan_set_option(plan, key, value):
+    _check(load().gemm_grouped_plan_set_option(plan, key, value), "gemm_grouped_plan_set_option")
+
+
+def gemm_grouped_plan_get_info(plan, key) -> int:
+    v = ctypes.c_int64()
+    key = GROUPED_INFO[key] if isinstance(key, str) else key
+    _check(load().gemm_grouped_plan_get_info(plan, key, ctypes.byref(v)), "gemm_grouped_plan_get_info")
+    return v.value
+
+
+def gemm_grouped_plan_units(plan, offsets, unit: int):
+    """[(tile, group, tile along C's rows, first row, rows, width, k0, k1, k-blocks), ...] of
+    scheduling unit ``unit`` for host offsets."""
+    off = (ctypes.c_int32 * len(offsets))(*[int(x) for x in offsets])
+    n = ctypes.c_int64()
+    _check(load().gemm_grouped_plan_units(plan, off, unit, None, 0, ctypes.byref(n)),
+           "gemm_grouped_plan_units")
+    buf = (ctypes.c_int32 * (9 * max(n.value, 1)))()
+    _check(load().gemm_grouped_plan_units(plan, off, unit, buf, n.value, ctypes.byref(n)),
+           "gemm_grouped_plan_units")
+    return [tuple(buf[9 * i:9 * i + 9]) for i in range(n.value)]
+
+
 def gemm_grouped_workspace_size(plan) -> int:
     v = ctypes.c_size_t()
     _check(load().gemm_grouped_workspace_size(plan, ctypes.byref(v)), "gemm_grouped_workspace_size")
@@ -360,10 +399,25 @@ def gemm_grouped_plan_destroy(plan):
 class GroupedPlan:
     """Owning wrapper around a grouped plan handle (marshalling only)."""
 
-    def __init__(self, kind, groups, rows, N, K, dtype, layout_b):
+    def __init__(self, kind, groups, rows, N, K, dtype, layout_b, offline_sms=None, ctas=None):
         self.kind, self.groups, self.rows, self.N, self.K = kind, groups, rows, N, K
         self.dtype, self.layout_b = dtype, layout_b
-        self.handle = gemm_grouped_plan_create(kind, groups, rows, N, K, dtype, layout_b)
+        if offline_sms is None:
+            self.handle = gemm_grouped_plan_create(kind, groups, rows, N, K, dtype, layout_b)
+        else:
+            self.handle = gemm_grouped_plan_create_offline(kind, groups, rows, N, K, dtype, layout_b,
+                                                           offline_sms)
+        if ctas is not None:
+            self.set_option(GEMM_GROUPED_OPT_CTAS, int(ctas))
+
+    def info(self, key):
+        return gemm_grouped_plan_get_info(self.handle, key)
+
+    def set_option(self, key, value):
+        gemm_grouped_plan_set_option(self.handle, key, value)
+
+    def units(self, offsets, unit):
+        return gemm_grouped_plan_units(self.handle, offsets, unit)
 
     @property
     def workspace_size(self) -> int:

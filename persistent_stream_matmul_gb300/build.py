@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libpsm_gemm.so")
 UNITS = {
     "gemm.cu": ("gemm_kernel.cuh", "ptx.cuh", "sched.cuh", "gemm.h"),
     "moe.cu": ("ptx.cuh", "gemm.h", "gemm_moe.h"),
-    "grouped.cu": ("ptx.cuh", "gemm.h", "gemm_moe.h"),
+    "grouped.cu": ("grouped_kernel.cuh", "grouped_sched.cuh", "ptx.cuh", "gemm.h", "gemm_moe.h"),
 }
 SOURCES = [os.path.join(CSRC, f) for f in UNITS]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

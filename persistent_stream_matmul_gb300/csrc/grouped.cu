@@ -1,97 +1,67 @@
-// Grouped products of include/gemm_moe.h: plans, launches and the C entry points.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+// Grouped products of include/gemm_moe.h: plans, tensor maps, launches and the
+// C entry points.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+#include <chrono>
+#include <mutex>
 #include <new>
 
 #include "gemm_moe.h"
-#include "ptx.cuh"
+#include "grouped_kernel.cuh"
 
 using namespace psm;
+
+static_assert(G_MAX_GROUPS == GEMM_MOE_MAX_EXPERTS, "the kernel's tables hold every group");
+
+struct gemm_grouped_plan {
+    int64_t groups, rows, N, K;
+    int kind, dtype, layout_b, device, num_sms;
+    bool offline;
+    int opt_ctas;
+    // derived
+    int ctas;             // CTAs of a scheduling unit
+    int64_t m_total;      // C's contiguous extent (the lanes side)
+    GroupedShape shape;
+    size_t counter_bytes, ws_bytes;
+    int* d_status;
+};
 
 namespace {
 
 constexpr int64_t MAX_INDEX = (1ll << 31) - 1024;
 
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Offset g made monotone and in range: the largest of offsets[0 .. g], within [0, rows].
-__device__ int bounded_offset(const int32_t* offsets, int g, int rows) {
-    int v = 0;
-    for (int i = 0; i <= g; ++i) v = max(v, offsets[i]);
-    return min(v, rows);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
 }
 
-constexpr int TILE = 64, KT = 16;
-
-// One 64 x 64 tile of out = P^T-like products at a time, 256 threads of 4 x 4
-// outputs.  pe(i, k) and qe(j, k) give the operands' elements, st(i, j, v) stores.
-template <typename PE, typename QE, typename ST>
-__device__ void tile_product(float (*sp)[TILE], float (*sq)[TILE], int64_t klen, PE pe, QE qe, ST st) {
-    float acc[4][4] = {};
-    const int ti = (threadIdx.x / 16) * 4, tj = (threadIdx.x % 16) * 4;
-    for (int64_t k0 = 0; k0 < klen; k0 += KT) {
-        __syncthreads();
-        for (int x = threadIdx.x; x < TILE * KT; x += 256) {
-            const int i = x % TILE, k = x / TILE;
-            sp[k][i] = k0 + k < klen ? pe(i, k0 + k) : 0.f;
-            sq[k][i] = k0 + k < klen ? qe(i, k0 + k) : 0.f;
-        }
-        __syncthreads();
-        for (int k = 0; k < KT; ++k)
-            for (int a = 0; a < 4; ++a)
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(sp[k][ti + a], sq[k][tj + b], acc[a][b]);
-    }
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) st(ti + a, tj + b, acc[a][b]);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-    rows_kernel(const T* A, const T* B, T* C, const int32_t* offsets, int groups, int rows, int N, int K,
-                bool b_col) {
-    __shared__ float sp[KT][TILE], sq[KT][TILE];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int g = blockIdx.y, n0 = blockIdx.x * TILE;
-    const int r_begin = bounded_offset(offsets, g, rows);
-    const bool tail = g == groups;  // the unused rows
-    const int r_end = tail ? rows : bounded_offset(offsets, g + 1, rows);
-    const T* Bg = B + (int64_t)g * N * K;
-    for (int64_t r0 = r_begin; r0 < r_end; r0 += TILE)
-        tile_product(
-            sp, sq, tail ? 0 : K,
-            [&](int i, int64_t k) { return r0 + i < r_end ? to_f(A[(r0 + i) * K + k]) : 0.f; },
-            [&](int j, int64_t k) {
-                return n0 + j < N ? to_f(b_col ? Bg[(int64_t)(n0 + j) * K + k] : Bg[k * N + n0 + j]) : 0.f;
-            },
-            [&](int i, int j, float v) {
-                if (r0 + i < r_end && n0 + j < N) C[(r0 + i) * N + n0 + j] = from_f<T>(v);
-            });
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-    inner_kernel(const T* A, const T* B, T* C, const int32_t* offsets, int groups, int rows, int N, int K,
-                 bool c_col) {
-    __shared__ float sp[KT][TILE], sq[KT][TILE];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int n0 = blockIdx.x * TILE, k0 = blockIdx.y * TILE, g = blockIdx.z;
-    const int64_t r0 = bounded_offset(offsets, g, rows), r1 = bounded_offset(offsets, g + 1, rows);
-    T* Cg = C + (int64_t)g * N * K;
-    tile_product(
-        sp, sq, r1 - r0, [&](int i, int64_t r) { return k0 + i < K ? to_f(A[(r0 + r) * K + k0 + i]) : 0.f; },
-        [&](int j, int64_t r) { return n0 + j < N ? to_f(B[(r0 + r) * N + n0 + j]) : 0.f; },
-        [&](int i, int j, float v) {
-            if (k0 + i < K && n0 + j < N)
-                Cg[c_col ? (int64_t)(n0 + j) * K + k0 + i : (int64_t)(k0 + i) * N + n0 + j] = from_f<T>(v);
-        });
+// Run numbers tagged into the split tiles' counters, 48 bits, unique in the
+// process and started from the clock, so that what another run or program left
+// in a workspace is not taken for this run's.
+uint64_t next_epoch() {
+    static std::atomic<uint64_t> epoch{
+        (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() << 8};
+    uint64_t e;
+    do e = ++epoch & 0xffffffffffffull;
+    while (e == 0);
+    return e;
 }
 
 struct DeviceGuard {
@@ -107,37 +77,133 @@ struct DeviceGuard {
     }
 };
 
-}  // namespace
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-struct gemm_grouped_plan {
-    int64_t groups, rows, N, K;
-    int kind, dtype, layout_b, device, num_sms;
-    int* d_status;
-};
+// Kernels, by [pair][ROWS K-major, ROWS MN-major, INNER][bf16].
+template <bool PAIR>
+void* kernel_of(int form, bool bf16) {
+    switch (form) {
+        case 0: return bf16 ? (void*)&grouped_kernel<PAIR, false, false, true> : (void*)&grouped_kernel<PAIR, false, false, false>;
+        case 1: return bf16 ? (void*)&grouped_kernel<PAIR, false, true, true> : (void*)&grouped_kernel<PAIR, false, true, false>;
+        default: return bf16 ? (void*)&grouped_kernel<PAIR, true, true, true> : (void*)&grouped_kernel<PAIR, true, true, false>;
+    }
+}
 
-extern "C" {
+int smem_of(int ctas) { return ctas == 2 ? GroupedCfg<true>::SMEM_BYTES : GroupedCfg<false>::SMEM_BYTES; }
 
-gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t* out, gemm_grouped_kind_t kind,
-                                       int64_t groups, int64_t rows, int64_t N, int64_t K,
-                                       gemm_dtype_t dtype, gemm_layout_t layout_b) {
+// The kernel of a plan with its shared memory allowed on the current device;
+// null when that fails.
+void* prepared_kernel(int ctas, int form, bool bf16, int dev) {
+    static std::mutex mu;
+    static bool ready[64][2][3][2];
+    void* fn = ctas == 2 ? kernel_of<true>(form, bf16) : kernel_of<false>(form, bf16);
+    if (dev < 0 || dev >= 64) return nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& r = ready[dev][ctas - 1][form][bf16];
+    if (!r) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(ctas)) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        r = true;
+    }
+    return fn;
+}
+
+// Pairs of CTAs that can be resident at once: a cluster lives inside one GPC,
+// so this can be below #SMs / 2.  0 when unknown.
+int resident_pairs(int dev) {
+    static std::mutex mu;
+    static int cache[64];
+    void* fn = prepared_kernel(2, 0, true, dev);
+    if (!fn) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[dev]) return cache[dev];
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(G_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem_of(2);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return cache[dev] = n;
+}
+
+gemm_status_t derive(gemm_grouped_plan* p) {
+    const bool inner = p->kind == GEMM_GROUPED_INNER;
+    const bool col = p->layout_b == GEMM_COL_MAJOR;
+    // the lanes side is C's contiguous dimension
+    p->m_total = inner && col ? p->K : p->N;
+    const int64_t n_total = inner ? (col ? p->N : p->K) : 0;
+    int ctas = p->opt_ctas;
+    if (ctas == 0) {
+        if (inner) ctas = p->m_total > 128 && n_total > 128 ? 2 : 1;
+        else ctas = p->rows > 128 * p->groups && p->m_total > 128 ? 2 : 1;
+    }
+    const int tile = 128 * ctas;
+    GroupedShape s{};
+    s.groups = (int32_t)p->groups;
+    s.rows = (int32_t)p->rows;
+    s.inner = inner;
+    s.tiles_m = (int32_t)cdiv(p->m_total, tile);
+    s.tiles_n = (int32_t)cdiv(n_total, tile);
+    s.n_total = (int32_t)n_total;
+    s.kb = inner ? 0 : (int32_t)cdiv(p->K, G_BK);
+    s.tile_n = tile;
+    s.step = 16 * ctas;
+    s.band = 8;
+    s.min_iters = 4;
+    s.units = p->num_sms / ctas;
+    if (ctas == 2 && !p->offline) {
+        const int n = resident_pairs(p->device);
+        if (n > 0) s.units = std::min(s.units, n);
+    }
+    const int64_t tiles_n = inner ? p->groups * s.tiles_n : p->rows / tile + std::min(p->groups, p->rows);
+    if (s.tiles_m > 0 && tiles_n > MAX_INDEX / s.tiles_m) return GEMM_ERR_UNSUPPORTED;
+    p->ctas = ctas;
+    p->shape = s;
+    p->counter_bytes = p->ws_bytes = 0;
+    if (!inner && p->rows > 0 && p->K > 0 && p->N > 0) {
+        // fewer tiles than units are split: a counter a tile and CTA, two partial slots a CTA
+        const size_t slot = 128 * (size_t)tile * sizeof(float), grid = (size_t)s.units * ctas;
+        p->counter_bytes = (grid * 8 + 255) / 256 * 256;
+        p->ws_bytes = p->counter_bytes + 2 * grid * slot;
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t make_plan(gemm_grouped_plan_t* out, int kind, int64_t groups, int64_t rows, int64_t N,
+                        int64_t K, int dtype, int layout_b, bool offline, int num_sms) {
     if (!out || groups < 1 || rows < 0 || N < 0 || K < 0 ||
         (kind != GEMM_GROUPED_ROWS && kind != GEMM_GROUPED_INNER) ||
         (dtype != GEMM_F16 && dtype != GEMM_BF16) ||
-        (layout_b != GEMM_ROW_MAJOR && layout_b != GEMM_COL_MAJOR))
+        (layout_b != GEMM_ROW_MAJOR && layout_b != GEMM_COL_MAJOR) || (offline && num_sms < 2))
         return GEMM_ERR_INVALID_ARG;
     if (groups > GEMM_MOE_MAX_EXPERTS || rows > MAX_INDEX || N > MAX_INDEX || K > MAX_INDEX || N % 8 || K % 8)
         return GEMM_ERR_UNSUPPORTED;
-    int dev = 0, count = 0, major = 0, minor = 0, sms = 0;
-    if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
-        cudaGetLastError();
-        return GEMM_ERR_NO_DEVICE;
+    int dev = -1;
+    if (!offline) {
+        int count = 0, major = 0, minor = 0;
+        if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
+            cudaGetLastError();
+            return GEMM_ERR_NO_DEVICE;
+        }
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        if (major != 10 || minor != 3) return GEMM_ERR_NO_DEVICE;
     }
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    if (major != 10 || minor != 3) return GEMM_ERR_NO_DEVICE;
     gemm_grouped_plan* p = new (std::nothrow) gemm_grouped_plan();
     if (!p) return GEMM_ERR_CUDA;
     p->groups = groups;
@@ -148,9 +214,15 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t* out, gemm_grouped_ki
     p->dtype = dtype;
     p->layout_b = layout_b;
     p->device = dev;
-    p->num_sms = sms;
-    if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess ||
-        cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
+    p->num_sms = num_sms;
+    p->offline = offline;
+    const gemm_status_t st = derive(p);
+    if (st != GEMM_OK) {
+        delete p;
+        return st;
+    }
+    if (!offline && (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess ||
+                     cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess)) {
         cudaGetLastError();
         if (p->d_status) cudaFree(p->d_status);
         delete p;
@@ -160,49 +232,189 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t* out, gemm_grouped_ki
     return GEMM_OK;
 }
 
+// 128-byte-swizzled map of a matrix stack: dims {x, y, z}, rows of ld elements.
+bool encode(CUtensorMap* m, int dtype, const void* base, int rank, int64_t x, int64_t y, int64_t z,
+            uint32_t box_x, uint32_t box_y) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
+    const cuuint64_t strides[2] = {(cuuint64_t)x * 2, (cuuint64_t)x * (cuuint64_t)y * 2};
+    const cuuint32_t box[3] = {box_x, box_y, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, dtype == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t* out, gemm_grouped_kind_t kind,
+                                       int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                       gemm_dtype_t dtype, gemm_layout_t layout_b) {
+    return make_plan(out, kind, groups, rows, N, K, dtype, layout_b, false, 0);
+}
+
+gemm_status_t gemm_grouped_plan_create_offline(gemm_grouped_plan_t* out, gemm_grouped_kind_t kind,
+                                               int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                               gemm_dtype_t dtype, gemm_layout_t layout_b,
+                                               int num_sms) {
+    return make_plan(out, kind, groups, rows, N, K, dtype, layout_b, true, num_sms);
+}
+
+gemm_status_t gemm_grouped_plan_set_option(gemm_grouped_plan_t p, int key, int64_t value) {
+    if (!p || key != GEMM_GROUPED_OPT_CTAS) return GEMM_ERR_INVALID_ARG;
+    if (value < 0 || value > 2) return GEMM_ERR_UNSUPPORTED;
+    const int saved = p->opt_ctas;
+    p->opt_ctas = (int)value;
+    const gemm_status_t st = derive(p);
+    if (st != GEMM_OK) {
+        p->opt_ctas = saved;
+        derive(p);
+    }
+    return st;
+}
+
+gemm_status_t gemm_grouped_plan_get_info(gemm_grouped_plan_t p, int key, int64_t* value) {
+    if (!p || !value) return GEMM_ERR_INVALID_ARG;
+    switch (key) {
+        case GEMM_GROUPED_INFO_CTAS: *value = p->ctas; break;
+        case GEMM_GROUPED_INFO_UNITS: *value = p->shape.units; break;
+        case GEMM_GROUPED_INFO_TILE_M: *value = 128 * p->ctas; break;
+        case GEMM_GROUPED_INFO_TILE_N: *value = p->shape.tile_n; break;
+        case GEMM_GROUPED_INFO_STAGES: *value = GroupedCfg<true>::STAGES; break;
+        case GEMM_GROUPED_INFO_SMEM_BYTES: *value = smem_of(p->ctas); break;
+        default: return GEMM_ERR_INVALID_ARG;
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_grouped_plan_units(gemm_grouped_plan_t p, const int32_t* offsets, int64_t unit,
+                                      int32_t* units, int64_t max_units, int64_t* n_units) {
+    if (!p || !offsets || !n_units || unit < 0 || unit >= p->shape.units || max_units < 0 ||
+        (max_units > 0 && !units))
+        return GEMM_ERR_INVALID_ARG;
+    const GroupedShape& s = p->shape;
+    int32_t first[G_MAX_GROUPS + 1];
+    if (offsets[0] < 0 || offsets[s.groups] > s.rows) return GEMM_ERR_INVALID_ARG;
+    first[0] = 0;
+    for (int g = 0; g < s.groups; ++g) {
+        if (offsets[g + 1] < offsets[g]) return GEMM_ERR_INVALID_ARG;
+        first[g + 1] = first[g] + grouped_tiles_of(s, offsets[g + 1] - offsets[g]);
+    }
+    const GroupedTables tab{offsets, first};
+    GroupedCursor cur;
+    grouped_cursor_init(s, tab, (int32_t)unit, cur);
+    GroupedWork w;
+    int64_t n = 0;
+    while (grouped_cursor_next(s, tab, cur, w)) {
+        if (n < max_units) {
+            const int32_t v[9] = {w.tile, w.group, w.tm, w.n0, w.valid, w.width, w.k0, w.k1, w.kb};
+            std::copy(v, v + 9, units + 9 * n);
+        }
+        ++n;
+    }
+    *n_units = n;
+    return GEMM_OK;
+}
+
 gemm_status_t gemm_grouped_workspace_size(gemm_grouped_plan_t p, size_t* bytes) {
     if (!p || !bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = 0;
+    *bytes = p->ws_bytes;
     return GEMM_OK;
 }
 
 gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void* B, void* C,
                                const int32_t* offsets, void* workspace, gemm_stream_t stream) {
     if (!p) return GEMM_ERR_INVALID_ARG;
+    if (p->offline) return GEMM_ERR_NO_DEVICE;
     const bool inner = p->kind == GEMM_GROUPED_INNER;
     if (p->N == 0 || (inner ? p->K : p->rows) == 0) return GEMM_OK;  // C is empty
     const bool sums = inner ? p->rows > 0 : p->K > 0;                // something to sum
     if (!C || !offsets || (sums && (!A || !B))) return GEMM_ERR_INVALID_ARG;
     if (((uintptr_t)A & 15u) || ((uintptr_t)B & 15u) || ((uintptr_t)C & 15u) || ((uintptr_t)offsets & 3u))
         return GEMM_ERR_UNSUPPORTED;
-    (void)workspace;
+    if (p->ws_bytes > 0 && (!workspace || ((uintptr_t)workspace & 15u))) return GEMM_ERR_WORKSPACE;
     DeviceGuard guard(p->device);
     if (!guard.ok) return GEMM_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!sums) {
+    if (!sums) {  // empty sums: +0
         const size_t bytes = 2 * (size_t)p->N * (size_t)(inner ? p->groups * p->K : p->rows);
         return cudaMemsetAsync(C, 0, bytes, st) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
     }
-    const unsigned nt = (unsigned)((p->N + TILE - 1) / TILE), kt = (unsigned)((p->K + TILE - 1) / TILE);
-    const bool col = p->layout_b == GEMM_COL_MAJOR, bf = p->dtype == GEMM_BF16;
-    const int G = (int)p->groups, R = (int)p->rows, N = (int)p->N, K = (int)p->K;
-    using BF = __nv_bfloat16;
-    using HF = __half;
+    const bool bf16 = p->dtype == GEMM_BF16, col = p->layout_b == GEMM_COL_MAJOR;
+    const int form = inner ? 2 : (col ? 0 : 1);
+    void* fn = prepared_kernel(p->ctas, form, bf16, p->device);
+    if (!fn) return GEMM_ERR_CUDA;
+
+    // The maps are encoded for every run: they cost well under a microsecond
+    // of host time, and nothing is kept by an operand's address.
+    CUtensorMap tmP;
+    GroupedQMaps tmQ;
+    bool ok;
     if (inner) {
-        const dim3 grid(nt, kt, G);
-        if (bf) inner_kernel<BF><<<grid, 256, 0, st>>>((const BF*)A, (const BF*)B, (BF*)C, offsets, G, R, N, K, col);
-        else inner_kernel<HF><<<grid, 256, 0, st>>>((const HF*)A, (const HF*)B, (HF*)C, offsets, G, R, N, K, col);
+        const void* P = col ? A : B;  // C's contiguous dimension
+        const void* Q = col ? B : A;
+        ok = encode(&tmP, p->dtype, P, 3, p->m_total, p->rows, 1, 64, G_BK) &&
+             encode(&tmQ.m[0], p->dtype, Q, 2, p->shape.n_total, p->rows, 1, 64, G_BK);
+        tmQ.m[1] = tmQ.m[2] = tmQ.m[3] = tmQ.m[0];
     } else {
-        const dim3 grid(nt, G + 1, 1);
-        if (bf) rows_kernel<BF><<<grid, 256, 0, st>>>((const BF*)A, (const BF*)B, (BF*)C, offsets, G, R, N, K, col);
-        else rows_kernel<HF><<<grid, 256, 0, st>>>((const HF*)A, (const HF*)B, (HF*)C, offsets, G, R, N, K, col);
+        ok = col ? encode(&tmP, p->dtype, B, 3, p->K, p->N, p->groups, G_BK, 128)
+                 : encode(&tmP, p->dtype, B, 3, p->N, p->K, p->groups, 64, G_BK);
+        for (int i = 0; i < 4; ++i)
+            ok = ok && encode(&tmQ.m[i], p->dtype, A, 2, p->K, p->rows, 1, G_BK, 16u << i);
     }
-    if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+    if (!ok) return GEMM_ERR_UNSUPPORTED;
+
+    GroupedParams kp{};
+    kp.s = p->shape;
+    kp.K = (int32_t)p->K;
+    kp.m_total = (int32_t)p->m_total;
+    kp.out_group = p->N * p->K;
+    kp.out = C;
+    kp.offsets = offsets;
+    if (p->ws_bytes > 0) {
+        kp.counters = reinterpret_cast<unsigned long long*>(workspace);
+        kp.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + p->counter_bytes);
+    }
+    kp.epoch = next_epoch();
+    kp.status = p->d_status;
+    kp.idesc = idesc_f16(bf16, inner || !col, inner, 128 * p->ctas, 0);
+    // a wait may last as long as the longest tile's k-loop
+    kp.pipe_limit_ns = 4000000000ull + 2000ull * (uint64_t)cdiv(inner ? p->rows : p->K, G_BK);
+
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p->shape.units * p->ctas), 1, 1);
+    cfg.blockDim = dim3(G_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem_of(p->ctas);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    if (p->ctas == 2) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = 2;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    void* args[3] = {&tmP, &tmQ, &kp};
+    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
     return GEMM_OK;
 }
 
 gemm_status_t gemm_grouped_last_status(gemm_grouped_plan_t p, gemm_stream_t stream) {
     if (!p) return GEMM_ERR_INVALID_ARG;
+    if (p->offline) return GEMM_ERR_NO_DEVICE;
     DeviceGuard guard(p->device);
     if (!guard.ok) return GEMM_ERR_CUDA;
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;

@@ -1,0 +1,566 @@
+// Grouped products on the tensor cores: fp16/bf16 in, fp32 accumulation in
+// tensor memory, fp16/bf16 out.
+//
+// Orientation.  Both kinds compute out[j][m] = sum_k P[m, k] * Q[j, k], with m
+// the contiguous dimension of the output, along the tensor memory's lanes, and
+// j along its columns:
+//   ROWS   P = a group's matrix (m = columns of C), Q = the group's rows of A;
+//   INNER  P and Q = the columns of the two row operands, k = the group's rows.
+// So the ragged dimension of ROWS is the instruction's N, which takes any
+// multiple of 16 (32 for a pair): a group of 300 rows runs as two tiles of 160
+// and 140 rows, not as three of 128, and eight rows cost 16.  Rows past a
+// group's end that a tile loads (its neighbour's) only reach accumulator
+// columns that are not stored.
+//
+// PAIR: the two CTAs of a cluster run one tcgen05.mma.cta_group::2 of 256 x up
+// to 256; each CTA keeps its 128 lanes' P and half of Q.  Without it, 128 x up
+// to 128 a CTA.
+//
+// Warp roles (256 threads, one CTA per SM):
+//   warp 0     TMA producer, a ring of STAGES stages of 16 KB of P and up to
+//              16 KB of Q (128-byte swizzle), as many rows of Q as the tile has.
+//   warp 1     one lane issues the MMAs (pair: the first CTA's, for both).
+//   warp 2     allocates tensor memory.  INNER: relays every stage from its
+//              copies to the MMA, and writes zeros over the rows of a group's
+//              last k-block past its end, up to the next multiple of 16, where
+//              the MMA stops: zeros in both operands, so that whatever a
+//              neighbour's rows hold (NaN, infinity) adds nothing.
+//   warps 4-7  epilogue: accumulator fragments, packed to 16 bits, transposed
+//              through shared memory into rows, stored 16 bytes a lane.
+//
+// Split tiles (fewer tiles than units): every contributor writes its fp32
+// partial to its workspace slot and counts itself in; the one that comes last
+// adds all partials in ascending k and stores.  Nothing waits, and the sum
+// does not depend on who comes last.
+//
+// Waits inside the CTA are bounded, as in gemm_kernel.cuh.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "grouped_sched.cuh"
+#include "ptx.cuh"
+
+namespace psm {
+
+constexpr int G_THREADS = 256;
+constexpr int G_BK = 64;
+constexpr int G_EPI_WARP0 = 4;
+constexpr int G_EPI_THREADS = 128;
+constexpr int G_MAX_GROUPS = 1024;
+constexpr uint32_t G_CHUNK = 64 * 128;  // one 64 x 64 MN-major box
+enum : uint32_t { G_BAR_EPI = 1 };
+enum : int { G_STATUS_PIPE_TIMEOUT = 2 };
+
+template <bool PAIR>
+struct GroupedCfg {
+    static constexpr int CM = PAIR ? 2 : 1;
+    static constexpr int TILE_M = 128 * CM;
+    static constexpr int TILE_N = 128 * CM;
+    static constexpr int STEP = 16 * CM;          // granularity of the instruction's N
+    static constexpr int P_BYTES = 128 * G_BK * 2;
+    static constexpr int Q_BYTES = 128 * G_BK * 2;  // this CTA's rows of Q
+    static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+    static constexpr int STAGES = 6;
+    static constexpr int OUT_BYTES = 32 * 256;    // one staged chunk: 32 rows x 128 columns
+    static constexpr int TABLE_BYTES = 2 * (G_MAX_GROUPS + 4) * 4;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int TMEM_COLS = 2 * TILE_N;  // two accumulators
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * OUT_BYTES + TABLE_BYTES + BAR_BYTES + 1024;
+    static constexpr int SLOT_FLOATS = 128 * TILE_N;  // a CTA's partial tile
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert((3 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
+};
+
+struct GroupedParams {
+    GroupedShape s;
+    int32_t K;                    // ROWS: summed extent
+    int32_t m_total;              // extent of the output's contiguous dimension
+    int64_t out_group;            // INNER: elements of one output matrix
+    void* out;
+    const int32_t* offsets;
+    float* partials;              // two slots a CTA
+    unsigned long long* counters; // one a split tile and CTA of the pair
+    uint64_t epoch;               // run number tagged into the counters, 48 bits
+    int* status;
+    uint32_t idesc;               // without N
+    uint64_t pipe_limit_ns;
+};
+
+// Count one contribution to a split tile in; true when it was the last of n.
+// The word holds (epoch << 16) | count; a word of another run counts as 0, so
+// the workspace needs no clearing, and the last arrival leaves 0, so that a
+// replay of the same launch starts afresh.
+__device__ __forceinline__ bool grouped_count_in(unsigned long long* f, uint64_t epoch, uint32_t n) {
+    uint64_t cur = *reinterpret_cast<volatile unsigned long long*>(f);
+#pragma unroll 1
+    for (int tries = 0; tries < (1 << 20); ++tries) {
+        const uint64_t have = (cur >> 16) == epoch ? (cur & 0xffffu) : 0;
+        const bool last = have + 1 == n;
+        const uint64_t want = last ? 0 : ((epoch << 16) | (have + 1));
+        const uint64_t prev = atom_cas_acq_rel_u64(f, cur, want);
+        if (prev == cur) return last;
+        cur = prev;
+    }
+    return false;
+}
+
+template <bool OUT_BF16>
+__device__ __forceinline__ uint32_t grouped_pack2(float a, float b) {
+    if constexpr (OUT_BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+}
+
+// One warp: bounded offsets and the tiles before each group, from the device
+// offsets (a value out of order or range becomes the nearest one in order and
+// range).
+__device__ __forceinline__ void grouped_tables(const GroupedShape& s, const int32_t* offsets, int32_t* off,
+                                               int32_t* first) {
+    const int lane = threadIdx.x & 31;
+    int32_t carry = 0;
+    for (int b = 0; b <= s.groups; b += 32) {
+        const int i = b + lane;
+        int32_t v = i <= s.groups ? min(offsets[i], s.rows) : 0;
+        v = max(v, carry);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = max(v, u);
+        }
+        if (i <= s.groups) off[i] = v;
+        carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+    __syncwarp();
+    carry = 0;
+    for (int b = 0; b < s.groups; b += 32) {
+        const int i = b + lane;
+        const int32_t mine = i < s.groups ? grouped_tiles_of(s, off[i + 1] - off[i]) : 0;
+        int32_t v = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (i < s.groups) first[i] = carry + v - mine;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) first[s.groups] = carry;
+}
+
+struct GroupedQMaps {
+    CUtensorMap m[4];  // ROWS: boxes of 16, 32, 64 and 128 rows; INNER: m[0], 64 x 64
+};
+
+// P_MN: P is MN-major (INNER: both operands are).
+template <bool PAIR, bool INNER, bool P_MN, bool OUT_BF16>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ GroupedQMaps tmQ,
+                   const __grid_constant__ GroupedParams p) {
+    using Cf = GroupedCfg<PAIR>;
+    static_assert(!INNER || P_MN, "INNER reads both operands MN-major");
+    constexpr int STAGES = Cf::STAGES;
+    constexpr uint16_t PAIR_MASK = 0x3;
+    extern __shared__ uint8_t smem_raw[];
+
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    const uint32_t ring = raw + pad;
+    const uint32_t out_stage = ring + STAGES * Cf::STAGE_BYTES;
+    uint8_t* tables = smem_raw + pad + STAGES * Cf::STAGE_BYTES + 2 * Cf::OUT_BYTES;
+    int32_t* off = reinterpret_cast<int32_t*>(tables);
+    int32_t* first = off + G_MAX_GROUPS + 4;
+    uint8_t* bar_area = tables + Cf::TABLE_BYTES;
+    const uint32_t bar_base = smem_addr(bar_area);
+    auto full_bar = [&](int s) { return bar_base + 8u * s; };
+    auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+    auto ready_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };  // INNER
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (3 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (3 * STAGES + 2 + b); };
+    const uint32_t done_bar = bar_base + 8u * (3 * STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * (3 * STAGES + 5));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 8 * (3 * STAGES + 5) + 4);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(bar_area + 8 * (3 * STAGES + 5) + 8);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int unit = blockIdx.x / Cf::CM;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+            mbar_init(ready_bar(s), Cf::CM);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), Cf::CM * G_EPI_THREADS / 32);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmP);
+        tma_prefetch_desc(&tmQ.m[0]);
+    }
+    if (warp == 2) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(smem_addr(tmem_slot), Cf::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_addr(tmem_slot), Cf::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    // everything above may overlap the previous kernel in the stream
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_launch_dependents();
+    if (warp == 3) grouped_tables(p.s, p.offsets, off, first);
+    tc_fence_before_sync();
+    if constexpr (PAIR) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const GroupedTables tab{off, first};
+    GroupedCursor cur;
+    grouped_cursor_init(p.s, tab, unit, cur);
+    GroupedWork w;
+
+    auto fail_pipe = [&]() {
+        *abort_flag = 1;
+        atomicCAS(p.status, 0, G_STATUS_PIPE_TIMEOUT);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t filled = 0, fill_parity = 0;
+        bool ok = true;
+        const uint32_t full0_c = PAIR ? mapa_shared(full_bar(0), 0) : 0u;
+        while (ok && grouped_cursor_next(p.s, tab, cur, w)) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const int m0 = (w.tm * Cf::CM + rank) * 128;
+            const int rows_q = w.width / Cf::CM;  // this CTA's rows of Q
+            const int q0 = w.n0 + rank * rows_q;
+            // ROWS: the smallest box that holds them
+            const int box = rows_q <= 16 ? 0 : rows_q <= 32 ? 1 : rows_q <= 64 ? 2 : 3;
+            const uint32_t q_bytes = INNER ? (uint32_t)Cf::Q_BYTES : (16u << box) * 128u;
+            for (int kb = w.k0; kb < w.k1; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.pipe_limit_ns))) {
+                    if (lane == 0) fail_pipe();
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t sp = ring + stage * Cf::STAGE_BYTES;
+                    const uint32_t sq = sp + Cf::P_BYTES;
+                    if constexpr (INNER) {
+                        // each CTA's copies complete on its own barrier (warp 2 relays)
+                        const uint32_t fb = full_bar(stage);
+                        const int k = w.r0 + kb * G_BK;
+                        mbar_arrive_expect_tx(fb, Cf::STAGE_BYTES);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            tma_load_3d(sp + c * G_CHUNK, &tmP, fb, m0 + 64 * c, k, 0);
+                            tma_load_2d(sq + c * G_CHUNK, &tmQ.m[0], fb, q0 + 64 * c, k, false, 0);
+                        }
+                    } else {
+                        const int k = kb * G_BK;
+                        if constexpr (PAIR) {
+                            const uint32_t fbc = full0_c + 8u * (uint32_t)stage;
+                            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * (Cf::P_BYTES + q_bytes));
+                            if constexpr (P_MN) {
+                                tma_load_3d_pair(sp, &tmP, fbc, m0, k, w.group);
+                                tma_load_3d_pair(sp + G_CHUNK, &tmP, fbc, m0 + 64, k, w.group);
+                            } else {
+                                tma_load_3d_pair(sp, &tmP, fbc, k, m0, w.group);
+                            }
+                            tma_load_2d_pair(sq, &tmQ.m[box], fbc, k, q0, false, 0);
+                        } else {
+                            const uint32_t fb = full_bar(stage);
+                            mbar_arrive_expect_tx(fb, Cf::P_BYTES + q_bytes);
+                            if constexpr (P_MN) {
+                                tma_load_3d(sp, &tmP, fb, m0, k, w.group);
+                                tma_load_3d(sp + G_CHUNK, &tmP, fb, m0 + 64, k, w.group);
+                            } else {
+                                tma_load_3d(sp, &tmP, fb, k, m0, w.group);
+                            }
+                            tma_load_2d(sq, &tmQ.m[box], fb, k, q0, false, 0);
+                        }
+                    }
+                }
+                __syncwarp();
+                filled |= 1u << stage;
+                fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // before the CTA (or its peer) exits: every copy has landed, and every
+        // MMA that reads this ring has released it
+        for (int s = 0; s < STAGES; ++s)
+            if (filled & (1u << s)) {
+                if (INNER || !PAIR || rank == 0) mbar_wait(full_bar(s), (fill_parity >> s) & 1u, p.pipe_limit_ns);
+                mbar_wait(empty_bar(s), (fill_parity >> s) & 1u, p.pipe_limit_ns);
+            }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (!PAIR || rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0, iter = 0;
+            bool ok = true;
+            const uint64_t p_desc0 = smem_desc_sw128(ring, P_MN ? G_CHUNK : 16, 1024);
+            const uint64_t q_desc0 = smem_desc_sw128(ring + Cf::P_BYTES, INNER ? G_CHUNK : 16, 1024);
+            constexpr uint64_t p_step = P_MN ? (16 * 128) >> 4 : 32 >> 4;
+            constexpr uint64_t q_step = INNER ? (16 * 128) >> 4 : 32 >> 4;
+            while (ok && grouped_cursor_next(p.s, tab, cur, w)) {
+                if (w.k1 <= w.k0) continue;  // an empty group: the epilogue writes zeros
+                const int buf = iter & 1;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(tempty_bar(buf), ((iter >> 1) & 1u) ^ 1u, p.pipe_limit_ns))) {
+                    if (lane == 0) fail_pipe();
+                    break;
+                }
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(buf * Cf::TILE_N);
+                const uint32_t idesc = p.idesc | ((uint32_t)(w.width >> 3) << 17);
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    bool got;
+                    if constexpr (INNER) got = mbar_wait_acq_cluster(ready_bar(stage), phase, p.pipe_limit_ns);
+                    else got = mbar_wait(full_bar(stage), phase, p.pipe_limit_ns);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        if (lane == 0) fail_pipe();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const bool leader = elect_one();
+                    const uint64_t at = (uint64_t)((uint32_t)(stage * Cf::STAGE_BYTES) >> 4);
+                    // k-steps of 16 with rows in them (INNER: a group's last block may have fewer)
+                    const int steps = INNER ? min(4, (w.r1 - w.r0 - kb * G_BK + 15) / 16) : 4;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t pd = p_desc0 + at + (uint64_t)kk * p_step;
+                        const uint64_t qd = q_desc0 + at + (uint64_t)kk * q_step;
+                        const uint32_t acc = (kb > w.k0 || kk > 0) ? 1u : 0u;
+                        if (leader && kk < steps) {
+                            if constexpr (PAIR) mma_f16_ss_pair(d_tmem, pd, qd, idesc, acc);
+                            else mma_f16_ss(d_tmem, pd, qd, idesc, acc);
+                        }
+                    }
+                    if (leader) {
+                        if constexpr (PAIR) mma_commit_pair_multicast(empty_bar(stage), PAIR_MASK);
+                        else mma_commit(empty_bar(stage));
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if constexpr (PAIR) mma_commit_pair_multicast(tfull_bar(buf), PAIR_MASK);
+                    else mma_commit(tfull_bar(buf));
+                }
+                __syncwarp();
+                ++iter;
+            }
+            // all MMAs are complete before tensor memory is freed
+            __syncwarp();
+            if (elect_one()) {
+                if constexpr (PAIR) mma_commit_pair_multicast(done_bar, 0x1);
+                else mma_commit(done_bar);
+            }
+            __syncwarp();
+            mbar_wait(done_bar, 0, p.pipe_limit_ns);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ INNER relay
+        if constexpr (INNER) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint32_t ready0 = mapa_shared(ready_bar(0), 0);  // the issuing CTA's
+            while (ok && grouped_cursor_next(p.s, tab, cur, w)) {
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.pipe_limit_ns))) {
+                        if (lane == 0) fail_pipe();
+                        ok = false;
+                        break;
+                    }
+                    const int rows = w.r1 - w.r0 - kb * G_BK;  // of the group, from this block on
+                    if (rows < G_BK && (rows & 15)) {
+                        // four boxes (two of P, two of Q) of 64 k-rows x 128 bytes
+                        const int z0 = rows, zn = 16 - (rows & 15);
+                        const uint32_t base = ring + stage * Cf::STAGE_BYTES;
+                        for (int i = lane; i < zn * 32; i += 32) {
+                            const int box = (i >> 3) & 3, r = z0 + (i >> 5);
+                            st_shared_u4(base + box * G_CHUNK + r * 128 + (i & 7) * 16, 0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp >= G_EPI_WARP0) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
+        const int et = threadIdx.x - G_EPI_WARP0 * 32;
+        uint32_t iter = 0, staged = 0;
+        auto barrier = [&]() { named_bar_sync(G_BAR_EPI, G_EPI_THREADS); };
+        // rows 32c .. 32c + 31 of the tile, from fragments, to the output
+        auto store_chunk = [&](const float (&v)[32], int c) {
+            const uint32_t base = out_stage + (staged & 1u) * Cf::OUT_BYTES;
+            ++staged;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = j * 8 + (lane & 7);
+                const int u = (q * 4 + (lane >> 3)) ^ (row & 7);
+                stmatrix_x4_trans(base + row * 256 + u * 16, grouped_pack2<OUT_BF16>(v[8 * j], v[8 * j + 1]),
+                                  grouped_pack2<OUT_BF16>(v[8 * j + 2], v[8 * j + 3]),
+                                  grouped_pack2<OUT_BF16>(v[8 * j + 4], v[8 * j + 5]),
+                                  grouped_pack2<OUT_BF16>(v[8 * j + 6], v[8 * j + 7]));
+            }
+            barrier();  // (the other buffer's readers are past the barrier before this one)
+            const int col0 = (w.tm * Cf::CM + rank) * 128;
+            uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) +
+                           2 * ((INNER ? (int64_t)w.group * p.out_group : 0) + (int64_t)w.n0 * p.m_total);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (et >> 4) + 8 * i, u = et & 15;
+                const uint4 x = ld_shared_u4(base + row * 256 + ((u ^ (row & 7)) * 16));
+                if (32 * c + row < w.valid && col0 + u * 8 < p.m_total)
+                    st_u4(dst + 2 * ((int64_t)(32 * c + row) * p.m_total + col0 + u * 8), x.x, x.y, x.z, x.w);
+            }
+        };
+        bool ok = true;
+        while (grouped_cursor_next(p.s, tab, cur, w)) {
+            const bool empty = w.k1 <= w.k0;
+            const bool split = w.k1 - w.k0 < w.kb;
+            const int buf = iter & 1;
+            const int chunks = (w.valid + 31) / 32;
+            if (!empty) {
+                const bool got = mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) && !*abort_flag;
+                // one vote for all four warps
+                if (et == 0) *last_flag = 1;
+                barrier();
+                if (!got) *last_flag = 0;
+                barrier();
+                ok = *last_flag != 0;
+                if (!ok) {
+                    if (et == 0) fail_pipe();
+                    break;
+                }
+                tc_fence_after_sync();
+            }
+            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * Cf::TILE_N);
+            float4* slot = nullptr;
+            if (split)  // a unit's first share may start inside a tile, its last may end inside one
+                slot = reinterpret_cast<float4*>(p.partials +
+                                                 (size_t)(2 * blockIdx.x + (w.k0 > 0 ? 0 : 1)) * Cf::SLOT_FLOATS);
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t r[32];
+                float v[32];
+                if (empty) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                } else {
+                    __syncwarp();
+                    tmem_ld_fragments_x4(tbase + c * 32, r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                }
+                if (split) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_f4(slot + (c * 8 + i) * G_EPI_THREADS + et,
+                              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                } else {
+                    store_chunk(v, c);
+                }
+            }
+            if (!empty) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
+                    else mbar_arrive(tempty_bar(buf));
+                }
+                ++iter;
+            }
+            if (split) {
+                const int64_t base_it = (int64_t)w.tile * w.kb;
+                const int u0 = grouped_split_unit(cur, base_it), u1 = grouped_split_unit(cur, base_it + w.kb - 1);
+                __threadfence();
+                barrier();
+                if (et == 0)
+                    *last_flag = grouped_count_in(p.counters + (size_t)w.tile * Cf::CM + rank, p.epoch,
+                                                  (uint32_t)(u1 - u0 + 1));
+                barrier();
+                const bool last = *last_flag != 0;
+                barrier();
+                if (last) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        float v[32];
+#pragma unroll 1
+                        for (int x = u0; x <= u1; ++x) {
+                            // the tile's first contributor holds k-block 0: its unit's last share
+                            const float4* from =
+                                reinterpret_cast<const float4*>(
+                                    p.partials + (size_t)(2 * (x * Cf::CM + rank) + (x > u0 ? 0 : 1)) * Cf::SLOT_FLOATS) +
+                                c * 8 * G_EPI_THREADS + et;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 y = ld_cg_f4(from + i * G_EPI_THREADS);
+                                v[4 * i] = x > u0 ? v[4 * i] + y.x : y.x;
+                                v[4 * i + 1] = x > u0 ? v[4 * i + 1] + y.y : y.y;
+                                v[4 * i + 2] = x > u0 ? v[4 * i + 2] + y.z : y.z;
+                                v[4 * i + 3] = x > u0 ? v[4 * i + 3] + y.w : y.w;
+                            }
+                        }
+                        store_chunk(v, c);
+                    }
+                }
+            }
+        }
+        if constexpr (!INNER) {
+            // the unused rows: +0, 16 bytes a thread
+            const int64_t begin = (int64_t)off[p.s.groups] * p.m_total / 8, end = (int64_t)p.s.rows * p.m_total / 8;
+            for (int64_t i = begin + (int64_t)blockIdx.x * G_EPI_THREADS + et; i < end;
+                 i += (int64_t)gridDim.x * G_EPI_THREADS)
+                st_u4(reinterpret_cast<uint8_t*>(p.out) + i * 16, 0, 0, 0, 0);
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncwarp();
+    if constexpr (PAIR) cluster_sync_all();
+    else __syncthreads();
+    if (warp == 2) {
+        __syncwarp();
+        tc_fence_after_sync();
+        if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Cf::TMEM_COLS);
+        else tmem_dealloc(tmem_base, Cf::TMEM_COLS);
+    }
+}
+
+}  // namespace psm

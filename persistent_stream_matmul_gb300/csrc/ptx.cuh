@@ -198,6 +198,25 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
             : "memory");
 }
 
+// 3-D forms of the two copies above, without an L2 policy.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                 int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // shared::cluster address of the same shared-memory offset in CTA `rank`
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -357,6 +376,38 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
+// 32 lanes x 32 columns of 32-bit as 8 x 8 matrix fragments: for columns 8j ..
+// 8j + 7, thread t receives r[8j], r[8j + 1] from lane t / 4 (columns 2 (t % 4)
+// and the next), r[8j + 2], r[8j + 3] from lane t / 4 + 8, and the other four
+// from the lanes 16 below.  `taddr` names the first of the 32 lanes.
+__device__ __forceinline__ void tmem_ld_fragments_x4(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %8, %9, %10, %11, %16, %17, %18, %19, %24, %25, %26, %27}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%4, %5, %6, %7, %12, %13, %14, %15, %20, %21, %22, %23, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]),
+          "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]),
+          "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]),
+          "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]), "=&r"(r[24]),
+          "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]),
+          "=&r"(r[31])
+        : "r"(taddr), "r"(taddr + (16u << 16))
+        : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: thread
+// t holds elements (t / 4, 2 (t % 4)) and the next of each matrix; element
+// (i, c) of matrix m goes to position i of the 16-byte row that lane 8m + c
+// addresses.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 // Shared-memory matrix descriptor (tcgen05 "matrix descriptor"): start
 // address, leading- and stride-dimension byte offsets (all >> 4), the fixed
 // version field 0b001 at bit 46, base offset 0 (tiles are 1024-byte aligned)
@@ -399,6 +450,16 @@ __device__ __forceinline__ uint64_t atom_cas_release_u64(unsigned long long* p, 
                                                          uint64_t val) {
     uint64_t old;
     asm volatile("atom.release.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                 : "=l"(old)
+                 : "l"(p), "l"(cmp), "l"(val)
+                 : "memory");
+    return old;
+}
+
+__device__ __forceinline__ uint64_t atom_cas_acq_rel_u64(unsigned long long* p, uint64_t cmp,
+                                                         uint64_t val) {
+    uint64_t old;
+    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
                  : "=l"(old)
                  : "l"(p), "l"(cmp), "l"(val)
                  : "memory");

@@ -22,21 +22,19 @@ def _sizes(counts, unused=0):
     return offsets, int(np.sum(counts)) + unused
 
 
-def _run(kind, counts, unused, N, K, dtype, layout, A, Bm, offsets=None, stream=None, plan=None):
+def _run(kind, counts, unused, N, K, dtype, layout, A, Bm, offsets=None, stream=None, ctas=None):
     """One run with guards around C; returns C in its natural shape."""
     code, dt = DTYPES[dtype]
     E = len(counts)
     offs, R = _sizes(counts, unused)
     offs = offsets if offsets is not None else offs
-    own = plan is None
-    plan = plan or B.GroupedPlan(kind, E, R, N, K, code, layout)
+    plan = B.GroupedPlan(kind, E, R, N, K, code, layout, ctas=ctas)
     C = Rows(1, (R if kind == B.GEMM_GROUPED_ROWS else E * K) * N, dt, offset=64)
     ws = torch.randint(0, 256, (max(1, plan.workspace_size),), dtype=torch.uint8, device="cuda")
     plan.run(A, Bm, C, offs, ws, stream)
     assert plan.last_status(stream) == B.GEMM_OK
     C.check_guards()
-    if own:
-        plan.close()
+    plan.close()
     flat = C.view[0]
     if kind == B.GEMM_GROUPED_ROWS:
         return flat.reshape(R, N)
@@ -93,46 +91,49 @@ SHAPES = [
 @pytest.mark.parametrize("layout", [COL, ROW])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("counts,unused,N,K", SHAPES)
-def test_products_of_groups(counts, unused, N, K, kind, dtype, layout):
+def test_products_of_groups(counts, unused, N, K, ctas, kind, dtype, layout):
     R = int(np.sum(counts)) + unused
     A, Bm = _operands(kind, counts, R, N, K, dtype, layout, 7)
     exact, absolute = _reference(kind, counts, R, N, K, layout, A, Bm)
-    got = _run(kind, counts, unused, N, K, dtype, layout, A, Bm)
+    got = _run(kind, counts, unused, N, K, dtype, layout, A, Bm, ctas=ctas)
     assert_rounded_sum(got, exact, absolute, K if kind == B.GEMM_GROUPED_ROWS else max(counts))
-    again = _run(kind, counts, unused, N, K, dtype, layout, A, Bm)
+    again = _run(kind, counts, unused, N, K, dtype, layout, A, Bm, ctas=ctas)
     assert torch.equal(got.view(torch.int16), again.view(torch.int16))
     # whole numbers: every partial sum is exact, so only the last rounding remains
     A, Bm = _operands(kind, counts, R, N, K, dtype, layout, 17, integers=True)
     exact, absolute = _reference(kind, counts, R, N, K, layout, A, Bm)
-    got = _run(kind, counts, unused, N, K, dtype, layout, A, Bm)
+    got = _run(kind, counts, unused, N, K, dtype, layout, A, Bm, ctas=ctas)
     assert torch.equal(got, exact.to(got.dtype))
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
-def test_many_groups(kind):
+def test_many_groups(kind, ctas):
     r = np.random.default_rng(3)
     counts = (r.integers(0, 9, 1024) * (r.random(1024) < 0.6)).tolist()
     R = int(np.sum(counts))
     A, Bm = _operands(kind, counts, R, 72, 136, "bf16", COL, 5)
     exact, absolute = _reference(kind, counts, R, 72, 136, COL, A, Bm)
-    assert_rounded_sum(_run(kind, counts, 0, 72, 136, "bf16", COL, A, Bm), exact, absolute, 136)
+    assert_rounded_sum(_run(kind, counts, 0, 72, 136, "bf16", COL, A, Bm, ctas=ctas), exact, absolute, 136)
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
-def test_neighbours_do_not_leak(kind):
+def test_neighbours_do_not_leak(kind, ctas):
     """A group whose rows and matrix are NaN and infinite changes nothing in
     the groups beside it, at boundaries inside a tile."""
     counts, N, K = [37, 21, 70], 136, 200
     R = sum(counts)
     A, Bm = _operands(kind, counts, R, N, K, "f16", ROW, 9)
-    clean = _run(kind, counts, 0, N, K, "f16", ROW, A, Bm)
+    clean = _run(kind, counts, 0, N, K, "f16", ROW, A, Bm, ctas=ctas)
     A[37:58] = float("nan")
     if kind == B.GEMM_GROUPED_ROWS:
         Bm[1] = float("inf")
     else:
         Bm[37:58] = float("inf")
-    dirty = _run(kind, counts, 0, N, K, "f16", ROW, A, Bm)
+    dirty = _run(kind, counts, 0, N, K, "f16", ROW, A, Bm, ctas=ctas)
     mine = slice(37, 58) if kind == B.GEMM_GROUPED_ROWS else slice(1, 2)
     assert bool(torch.isnan(dirty[mine]).all())
     clean[mine] = dirty[mine] = 0
@@ -242,3 +243,33 @@ def test_gradients_against_differences():
         bp[e, k, n] += 16
         bm[e, k, n] -= 16
         agree(dB[e, k, n].item(), loss(A, bp), loss(A, bm), (bp[e, k, n].double() - bm[e, k, n].double()).item())
+
+
+def test_empty_sizes_and_refusals():
+    dt = torch.bfloat16
+    offs = torch.zeros(4, dtype=torch.int32, device="cuda")
+    C = Rows(1, 3 * 64 * 72, dt)
+    with B.GroupedPlan(B.GEMM_GROUPED_ROWS, 3, 10, 64, 0, B.GEMM_BF16, COL) as p:  # nothing to sum: +0
+        p.run(None, None, C, offs)
+        assert bool((C.view[0, :640] == 0).all()) and bool((C.view[0, 640:] == 77).all())
+    with B.GroupedPlan(B.GEMM_GROUPED_INNER, 3, 0, 64, 72, B.GEMM_BF16, COL) as p:
+        p.run(None, None, C, offs)
+        assert bool((C.view[0] == 0).all())
+        C.check_guards()
+    for kind, rows, N, K in ((0, 0, 64, 72), (0, 5, 0, 72), (1, 5, 0, 72), (1, 5, 64, 0)):
+        with B.GroupedPlan(kind, 3, rows, N, K, B.GEMM_BF16, COL) as p:
+            p.run(None, None, None, None)  # C is empty
+    A, Bm = normal((10, 72), dt, 1), normal((3, 64, 72), dt, 2)
+    with B.GroupedPlan(B.GEMM_GROUPED_ROWS, 3, 10, 64, 72, B.GEMM_BF16, COL) as p:
+        ws = torch.empty(p.workspace_size, dtype=torch.uint8, device="cuda")
+        good = [A, Bm, C, offs, ws]
+        for i in range(5):
+            for value, status in ((None, B.GEMM_ERR_WORKSPACE if i == 4 else B.GEMM_ERR_INVALID_ARG),
+                                  (good[i].data_ptr() + 2, B.GEMM_ERR_WORKSPACE if i == 4 else B.GEMM_ERR_UNSUPPORTED)):
+                args = list(good)
+                args[i] = value
+                with pytest.raises(B.GemmError) as e:
+                    p.run(*args)
+                assert e.value.status == status
+        p.run(*good)
+        assert p.last_status() == B.GEMM_OK
