@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const GroupedTables tab{off, first};
     GroupedCursor cur;
     grouped_cursor_init(p.s, tab, unit, cur);
-    GroupedWork w;
+    GroupedWork w{};
 
     // INNER: whether k-block kb ends inside a 16-row step
     auto ragged = [&](int kb) { return INNER && kb + 1 == w.kb && ((w.r1 - w.r0) & 15) != 0; };
