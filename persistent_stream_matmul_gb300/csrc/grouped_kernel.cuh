@@ -30,7 +30,11 @@
 //              way, the gradient of 8 matrices of 14336 x 4096 over 16384 rows
 //              took 2780 us.
 //   warps 4-7  epilogue: accumulator fragments, packed to 16 bits, transposed
-//              through shared memory into rows, stored 16 bytes a lane.
+//              through shared memory into rows of 256 bytes, stored 16 bytes a
+//              lane.  (Tensor copies of 64-byte rows, a warp by itself, wrote
+//              128 matrices of 2048 x 1536 in 281 us against 233: short
+//              segments cost write bandwidth, which on this device is 4.0 TB/s
+//              for a plain fill.)
 //
 // Split tiles (fewer tiles than units): every contributor writes its fp32
 // partial to its workspace slot and counts itself in; the one that comes last
@@ -53,7 +57,7 @@ constexpr int G_EPI_WARP0 = 4;
 constexpr int G_EPI_THREADS = 128;
 constexpr int G_MAX_GROUPS = 1024;
 constexpr uint32_t G_CHUNK = 64 * 128;  // one 64 x 64 MN-major box
-enum : uint32_t { G_BAR_EPI = 1 };
+enum : uint32_t { G_BAR_EPI = 1, G_BAR_VOTE = 2 };
 enum : int { G_STATUS_PIPE_TIMEOUT = 2 };
 
 template <bool PAIR>
@@ -152,6 +156,20 @@ __device__ __forceinline__ void grouped_tables(const GroupedShape& s, const int3
         carry += __shfl_sync(0xffffffffu, v, 31);
     }
     if (lane == 0) first[s.groups] = carry;
+}
+
+// AND of a predicate over the 128 epilogue threads.
+__device__ __forceinline__ bool grouped_vote_all(bool v) {
+    uint32_t out;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(out)
+        : "r"((uint32_t)v), "r"((uint32_t)G_BAR_VOTE), "r"((uint32_t)G_EPI_THREADS)
+        : "memory");
+    return out != 0;
 }
 
 struct GroupedQMaps {
@@ -480,7 +498,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     st_u4(dst + 2 * ((int64_t)(32 * c + row) * p.m_total + col0 + u * 8), x.x, x.y, x.z, x.w);
             }
         };
-        bool ok = true;
         while (grouped_cursor_next(p.s, tab, cur, w)) {
             const bool empty = w.k1 <= w.k0;
             const bool split = w.k1 - w.k0 < w.kb;
@@ -488,13 +505,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const int chunks = (w.valid + 31) / 32;
             if (!empty) {
                 const bool got = mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) && !*abort_flag;
-                // one vote for all four warps
-                if (et == 0) *last_flag = 1;
-                barrier();
-                if (!got) *last_flag = 0;
-                barrier();
-                ok = *last_flag != 0;
-                if (!ok) {
+                if (!grouped_vote_all(got)) {
                     if (et == 0) fail_pipe();
                     break;
                 }
