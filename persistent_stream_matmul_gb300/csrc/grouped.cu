@@ -161,7 +161,6 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     s.tile_n = tile;
     s.step = 16 * ctas;
     s.band = 8;
-    s.min_iters = 4;
     s.units = p->num_sms / ctas;
     if (ctas == 2 && !p->offline) {
         const int n = resident_pairs(p->device);
@@ -169,10 +168,12 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     }
     const int64_t tiles_n = inner ? p->groups * s.tiles_n : p->rows / tile + std::min(p->groups, p->rows);
     if (s.tiles_m > 0 && tiles_n > MAX_INDEX / s.tiles_m) return GEMM_ERR_UNSUPPORTED;
+    const int64_t k_blocks = inner ? s.tiles_m * s.tiles_n * (p->rows / G_BK + p->groups) : (int64_t)s.units * s.kb;
+    s.may_split = k_blocks < MAX_INDEX && (!inner || tiles_n * s.tiles_m < s.units);
     p->ctas = ctas;
     p->shape = s;
     p->counter_bytes = p->ws_bytes = 0;
-    if (!inner && p->rows > 0 && p->K > 0 && p->N > 0) {
+    if (s.may_split && p->rows > 0 && p->K > 0 && p->N > 0) {
         // fewer tiles than units are split: a counter a tile and CTA, two partial slots a CTA
         const size_t slot = 128 * (size_t)tile * sizeof(float), grid = (size_t)s.units * ctas;
         p->counter_bytes = (grid * 8 + 255) / 256 * 256;
@@ -297,14 +298,16 @@ gemm_status_t gemm_grouped_plan_units(gemm_grouped_plan_t p, const int32_t* offs
         (max_units > 0 && !units))
         return GEMM_ERR_INVALID_ARG;
     const GroupedShape& s = p->shape;
-    int32_t first[G_MAX_GROUPS + 1];
+    int32_t first[G_MAX_GROUPS + 1], iters[G_MAX_GROUPS + 1];
     if (offsets[0] < 0 || offsets[s.groups] > s.rows) return GEMM_ERR_INVALID_ARG;
-    first[0] = 0;
+    first[0] = iters[0] = 0;
     for (int g = 0; g < s.groups; ++g) {
         if (offsets[g + 1] < offsets[g]) return GEMM_ERR_INVALID_ARG;
-        first[g + 1] = first[g] + grouped_tiles_of(s, offsets[g + 1] - offsets[g]);
+        const GroupedCounts c = grouped_counts(s, offsets[g + 1] - offsets[g]);
+        first[g + 1] = first[g] + c.tiles;
+        iters[g + 1] = iters[g] + c.iters;
     }
-    const GroupedTables tab{offsets, first};
+    const GroupedTables tab{offsets, first, iters};
     GroupedCursor cur;
     grouped_cursor_init(s, tab, (int32_t)unit, cur);
     GroupedWork w;

@@ -16,7 +16,7 @@
 // to 256; each CTA keeps its 128 lanes' P and half of Q.  Without it, 128 x up
 // to 128 a CTA.
 //
-// Warp roles (256 threads, one CTA per SM):
+// Warp roles (384 threads, one CTA per SM):
 //   warp 0     TMA producer, a ring of STAGES stages of 16 KB of P and up to
 //              16 KB of Q (128-byte swizzle), as many rows of Q as the tile has.
 //   warp 1     one lane issues the MMAs (pair: the first CTA's, for both).
@@ -29,9 +29,16 @@
 //              CTAs report to the issuing one).  With every block relayed this
 //              way, the gradient of 8 matrices of 14336 x 4096 over 16384 rows
 //              took 2780 us.
-//   warps 4-7  epilogue: accumulator fragments, packed to 16 bits, transposed
+//   warp 3     scheduler: walks this unit's work and hands every piece to the
+//              other warps through a queue of G_QUEUE entries in shared memory.
+//              With the walk (searches and divisions, ~1000 cycles) repeated
+//              in every role, its copies of the code were fetched cold before
+//              the first load, and the epilogue paid it between tiles.
+//   warps 4-11 epilogue, two halves that take the 32-row chunks of a tile in
+//              turn: accumulator fragments, packed to 16 bits, transposed
 //              through shared memory into rows of 256 bytes, stored 16 bytes a
-//              lane.  (Tensor copies of 64-byte rows, a warp by itself, wrote
+//              lane.  One half alone took 730 cycles a chunk, its latencies
+//              end to end, and bound the gradient of small groups.  (Tensor copies of 64-byte rows, a warp by itself, wrote
 //              128 matrices of 2048 x 1536 in 281 us against 233: short
 //              segments cost write bandwidth, which on this device is 4.0 TB/s
 //              for a plain fill.)
@@ -51,13 +58,14 @@
 
 namespace psm {
 
-constexpr int G_THREADS = 256;
+constexpr int G_THREADS = 384;
 constexpr int G_BK = 64;
 constexpr int G_EPI_WARP0 = 4;
-constexpr int G_EPI_THREADS = 128;
+constexpr int G_EPI_THREADS = 256;
 constexpr int G_MAX_GROUPS = 1024;
+constexpr int G_QUEUE = 4;
 constexpr uint32_t G_CHUNK = 64 * 128;  // one 64 x 64 MN-major box
-enum : uint32_t { G_BAR_EPI = 1, G_BAR_VOTE = 2 };
+enum : uint32_t { G_BAR_EPI = 1, G_BAR_VOTE = 2, G_BAR_HALF = 3 };  // G_BAR_HALF + half
 enum : int { G_STATUS_PIPE_TIMEOUT = 2 };
 
 template <bool PAIR>
@@ -71,13 +79,14 @@ struct GroupedCfg {
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
     static constexpr int STAGES = 6;
     static constexpr int OUT_BYTES = 32 * 256;    // one staged chunk: 32 rows x 128 columns
-    static constexpr int TABLE_BYTES = 2 * (G_MAX_GROUPS + 4) * 4;
-    static constexpr int BAR_BYTES = 256;
+    static constexpr int TABLE_BYTES = 3 * (G_MAX_GROUPS + 4) * 4 + 12 * (G_THREADS / 32);  // and scan scratch
+    static constexpr int QUEUE_BYTES = G_QUEUE * 64;
+    static constexpr int BAR_BYTES = 320;
     static constexpr int TMEM_COLS = 2 * TILE_N;  // two accumulators
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * OUT_BYTES + TABLE_BYTES + BAR_BYTES + 1024;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * OUT_BYTES + TABLE_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
     static constexpr int SLOT_FLOATS = 128 * TILE_N;  // a CTA's partial tile
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-    static_assert((4 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
+    static_assert((4 * STAGES + 5 + 2 * G_QUEUE) * 8 + 16 <= BAR_BYTES, "barrier area");
 };
 
 struct GroupedParams {
@@ -100,7 +109,7 @@ struct GroupedParams {
 // the workspace needs no clearing, and the last arrival leaves 0, so that a
 // replay of the same launch starts afresh.
 __device__ __forceinline__ bool grouped_count_in(unsigned long long* f, uint64_t epoch, uint32_t n) {
-    uint64_t cur = *reinterpret_cast<volatile unsigned long long*>(f);
+    uint64_t cur = (epoch << 16) | (n - 1);  // try as the last: one round trip for the one that matters
 #pragma unroll 1
     for (int tries = 0; tries < (1 << 20); ++tries) {
         const uint64_t have = (cur >> 16) == epoch ? (cur & 0xffffu) : 0;
@@ -124,41 +133,77 @@ __device__ __forceinline__ uint32_t grouped_pack2(float a, float b) {
     }
 }
 
-// One warp: bounded offsets and the tiles before each group, from the device
-// offsets (a value out of order or range becomes the nearest one in order and
-// range).
+// The whole CTA: the scheduler's tables from the device offsets, bounded (a
+// value out of order or range becomes the nearest one in order and range).
+// Each thread takes a few consecutive groups; sums and maxima go through
+// warp scans.  One warp that took 32 groups at a time, and units that walked
+// the groups one by one, spent 2.5 us more before the first copy with 64
+// groups, of the 18 us that one token then took.
 __device__ __forceinline__ void grouped_tables(const GroupedShape& s, const int32_t* offsets, int32_t* off,
-                                               int32_t* first) {
-    const int lane = threadIdx.x & 31;
-    int32_t carry = 0;
-    for (int b = 0; b <= s.groups; b += 32) {
-        const int i = b + lane;
-        int32_t v = i <= s.groups ? min(offsets[i], s.rows) : 0;
-        v = max(v, carry);
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = max(v, u);
-        }
-        if (i <= s.groups) off[i] = v;
-        carry = __shfl_sync(0xffffffffu, v, 31);
+                                               int32_t* first, int32_t* iters,
+                                               int32_t* scratch) {
+    constexpr int PER = (G_MAX_GROUPS + G_THREADS) / G_THREADS;  // of groups + 1 entries
+    constexpr int WARPS = G_THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (s.groups + G_THREADS) / G_THREADS;
+    const int i0 = threadIdx.x * per;
+    int32_t v[PER];
+    int32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = i < per && i0 + i <= s.groups ? offsets[i0 + i] : 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = top = max(top, min(v[i], s.rows));
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, u);
     }
-    __syncwarp();
-    carry = 0;
-    for (int b = 0; b < s.groups; b += 32) {
-        const int i = b + lane;
-        const int32_t mine = i < s.groups ? grouped_tiles_of(s, off[i + 1] - off[i]) : 0;
-        int32_t v = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
+    if (lane == 31) scratch[warp] = top;
+    top = __shfl_up_sync(0xffffffffu, top, 1);
+    if (lane == 0) top = 0;
+    __syncthreads();
+    for (int x = 0; x < warp; ++x) top = max(top, scratch[x]);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (i < per && i0 + i <= s.groups) off[i0 + i] = max(v[i], top);
+    __syncthreads();
+    GroupedCounts mine[PER], sum{0, 0};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        mine[i] = sum;
+        if (i < per && i0 + i < s.groups) {
+            const GroupedCounts c = grouped_counts(s, off[i0 + i + 1] - off[i0 + i]);
+            sum.tiles += c.tiles;
+            sum.iters += c.iters;
         }
-        if (i < s.groups) first[i] = carry + v - mine;
-        carry += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) first[s.groups] = carry;
+    const GroupedCounts own = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t a = __shfl_up_sync(0xffffffffu, sum.tiles, o);
+        const int32_t c = __shfl_up_sync(0xffffffffu, sum.iters, o);
+        if (lane >= o) {
+            sum.tiles += a;
+            sum.iters += c;
+        }
+    }
+    int32_t* warps = scratch + WARPS;
+    if (lane == 31) {
+        warps[warp] = sum.tiles;
+        warps[WARPS + warp] = sum.iters;
+    }
+    __syncthreads();
+    for (int x = 0; x < warp; ++x) {
+        sum.tiles += warps[x];
+        sum.iters += warps[WARPS + x];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (i < per && i0 + i <= s.groups) {
+            first[i0 + i] = sum.tiles - own.tiles + mine[i].tiles;
+            iters[i0 + i] = sum.iters - own.iters + mine[i].iters;
+        }
 }
 
-// AND of a predicate over the 128 epilogue threads.
+// AND of a predicate over the epilogue threads.
 __device__ __forceinline__ bool grouped_vote_all(bool v) {
     uint32_t out;
     asm volatile(
@@ -171,6 +216,11 @@ __device__ __forceinline__ bool grouped_vote_all(bool v) {
         : "memory");
     return out != 0;
 }
+
+// The first and last contributor of a split tile.
+struct GroupedShare {
+    int32_t u0, u1;
+};
 
 struct GroupedQMaps {
     CUtensorMap m[4];  // ROWS: boxes of 16, 32, 64 and 128 rows; INNER: m[0], 64 x 64
@@ -194,7 +244,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     uint8_t* tables = smem_raw + pad + STAGES * Cf::STAGE_BYTES + 2 * Cf::OUT_BYTES;
     int32_t* off = reinterpret_cast<int32_t*>(tables);
     int32_t* first = off + G_MAX_GROUPS + 4;
-    uint8_t* bar_area = tables + Cf::TABLE_BYTES;
+    int32_t* iters = first + G_MAX_GROUPS + 4;
+    const uint32_t queue = smem_addr(tables + Cf::TABLE_BYTES);
+    uint8_t* bar_area = tables + Cf::TABLE_BYTES + Cf::QUEUE_BYTES;
     const uint32_t bar_base = smem_addr(bar_area);
     auto full_bar = [&](int s) { return bar_base + 8u * s; };
     auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
@@ -205,9 +257,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     auto tfull_bar = [&](int b) { return bar_base + 8u * (4 * STAGES + b); };
     auto tempty_bar = [&](int b) { return bar_base + 8u * (4 * STAGES + 2 + b); };
     const uint32_t done_bar = bar_base + 8u * (4 * STAGES + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * (4 * STAGES + 5));
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 8 * (4 * STAGES + 5) + 4);
-    volatile int* last_flag = reinterpret_cast<volatile int*>(bar_area + 8 * (4 * STAGES + 5) + 8);
+    auto qfull_bar = [&](int s) { return bar_base + 8u * (4 * STAGES + 5 + s); };
+    auto qempty_bar = [&](int s) { return bar_base + 8u * (4 * STAGES + 5 + G_QUEUE + s); };
+    constexpr int BARS = 4 * STAGES + 5 + 2 * G_QUEUE;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 8 * BARS + 4);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(bar_area + 8 * BARS + 8);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -226,6 +281,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             mbar_init(tempty_bar(b), Cf::CM * G_EPI_THREADS / 32);
         }
         mbar_init(done_bar, 1);
+        // readers of the queue: producer, issuer (pair: the first CTA's), INNER's
+        // warp 2 and the epilogue warps
+        const int readers = 1 + (!PAIR || rank == 0) + INNER + G_EPI_THREADS / 32;
+        for (int s = 0; s < G_QUEUE; ++s) {
+            mbar_init(qfull_bar(s), 1);
+            mbar_init(qempty_bar(s), readers);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -245,24 +307,46 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     // everything above may overlap the previous kernel in the stream
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
-    if (warp == 3) grouped_tables(p.s, p.offsets, off, first);
+    grouped_tables(p.s, p.offsets, off, first, iters, iters + G_MAX_GROUPS + 4);
     tc_fence_before_sync();
     if constexpr (PAIR) cluster_sync_all();
     else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
 
-    const GroupedTables tab{off, first};
-    GroupedCursor cur;
-    grouped_cursor_init(p.s, tab, unit, cur);
-    GroupedWork w{};
-
-    // INNER: whether k-block kb ends inside a 16-row step
-    auto ragged = [&](int kb) { return INNER && kb + 1 == w.kb && ((w.r1 - w.r0) & 15) != 0; };
     auto fail_pipe = [&]() {
         *abort_flag = 1;
         atomicCAS(p.status, 0, G_STATUS_PIPE_TIMEOUT);
     };
+
+    GroupedWork w{};
+    GroupedShare share{};
+    int qslot = 0;
+    uint32_t qphase = 0;
+    // The next piece of work, for a whole warp; false at the end or after a
+    // wait that ran out.
+    auto next_work = [&]() {
+        const bool got = mbar_wait(qfull_bar(qslot), qphase, p.pipe_limit_ns);
+        if (!__all_sync(0xffffffffu, got && *abort_flag == 0)) {
+            if (lane == 0) fail_pipe();
+            return false;
+        }
+        const uint32_t at = queue + (uint32_t)qslot * 64u;
+        const uint4 a = ld_shared_u4(at), b = ld_shared_u4(at + 16), c = ld_shared_u4(at + 32), d = ld_shared_u4(at + 48);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty_bar(qslot));
+        if (++qslot == G_QUEUE) {
+            qslot = 0;
+            qphase ^= 1u;
+        }
+        w = GroupedWork{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y,
+                        (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
+        share.u0 = (int)d.x;
+        share.u1 = (int)d.y;
+        return w.tile >= 0;
+    };
+    // INNER: whether k-block kb ends inside a 16-row step
+    auto ragged = [&](int kb) { return INNER && kb + 1 == w.kb && ((w.r1 - w.r0) & 15) != 0; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -272,8 +356,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         uint32_t ragged_used = 0, ragged_parity = 0;  // per stage: parity of the last ragged fill
         bool ok = true;
         const uint32_t full0_c = PAIR ? mapa_shared(full_bar(0), 0) : 0u;
-        while (ok && grouped_cursor_next(p.s, tab, cur, w)) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        while (ok && next_work()) {
             const int m0 = (w.tm * Cf::CM + rank) * 128;
             const int rows_q = w.width / Cf::CM;  // this CTA's rows of Q
             const int q0 = w.n0 + rank * rows_q;
@@ -372,7 +455,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const uint64_t q_desc0 = smem_desc_sw128(ring + Cf::P_BYTES, INNER ? G_CHUNK : 16, 1024);
             constexpr uint64_t p_step = P_MN ? (16 * 128) >> 4 : 32 >> 4;
             constexpr uint64_t q_step = INNER ? (16 * 128) >> 4 : 32 >> 4;
-            while (ok && grouped_cursor_next(p.s, tab, cur, w)) {
+            while (ok && next_work()) {
                 if (w.k1 <= w.k0) continue;  // an empty group: the epilogue writes zeros
                 const int buf = iter & 1;
                 if (!__all_sync(0xffffffffu,
@@ -443,8 +526,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             int stage = 0;  // of the work's first block
             uint32_t phases = 0;
             const uint32_t ready0 = mapa_shared(ready_bar(0), 0);  // the issuing CTA's
-            while (grouped_cursor_next(p.s, tab, cur, w)) {
-                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            while (next_work()) {
                 if (w.k1 > w.k0 && ragged(w.k1 - 1)) {
                     const int st = (stage + (w.k1 - 1 - w.k0)) % STAGES;
                     if (!__all_sync(0xffffffffu,
@@ -467,48 +549,84 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 stage = (stage + w.k1 - w.k0) % STAGES;
             }
         }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ scheduler
+        const GroupedTables tab{off, first, iters};
+        GroupedCursor cur;
+        grouped_cursor_init(p.s, tab, unit, cur);
+        bool more = true;
+        while (more) {
+            more = grouped_cursor_next(p.s, tab, cur, w);
+            if (!more) w.tile = -1;
+            else if (w.k1 - w.k0 < w.kb)
+                share = GroupedShare{grouped_split_unit(cur, w.it0), grouped_split_unit(cur, w.it0 + w.kb - 1)};
+            if (!__all_sync(0xffffffffu, mbar_wait(qempty_bar(qslot), qphase ^ 1u, p.pipe_limit_ns))) {
+                if (lane == 0) fail_pipe();
+                break;
+            }
+            if (lane == 0) {
+                const uint32_t at = queue + (uint32_t)qslot * 64u;
+                st_shared_u4(at, w.tile, w.it0, w.group, w.tm);
+                st_shared_u4(at + 16, w.n0, w.width, w.valid, w.r0);
+                st_shared_u4(at + 32, w.r1, w.k0, w.k1, w.kb);
+                st_shared_u4(at + 48, share.u0, share.u1, 0, 0);
+                mbar_arrive(qfull_bar(qslot));
+            }
+            __syncwarp();
+            if (++qslot == G_QUEUE) {
+                qslot = 0;
+                qphase ^= 1u;
+            }
+        }
     } else if (warp >= G_EPI_WARP0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
-        const int et = threadIdx.x - G_EPI_WARP0 * 32;
-        uint32_t iter = 0, staged = 0;
+        const int half = (warp - G_EPI_WARP0) >> 2;
+        const int et = (threadIdx.x - G_EPI_WARP0 * 32) & 127;  // thread of its half
+        const bool lead = threadIdx.x == G_EPI_WARP0 * 32;
+        uint32_t iter = 0;
         auto barrier = [&]() { named_bar_sync(G_BAR_EPI, G_EPI_THREADS); };
+        const uint32_t stage_base = out_stage + half * Cf::OUT_BYTES;
+        const int read_row = et >> 4, read_unit = et & 15;
         // rows 32c .. 32c + 31 of the tile, from fragments, to the output
         auto store_chunk = [&](const float (&v)[32], int c) {
-            const uint32_t base = out_stage + (staged & 1u) * Cf::OUT_BYTES;
-            ++staged;
+            named_bar_sync(G_BAR_HALF + half, 128);  // the last chunk has been read
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = j * 8 + (lane & 7);
                 const int u = (q * 4 + (lane >> 3)) ^ (row & 7);
-                stmatrix_x4_trans(base + row * 256 + u * 16, grouped_pack2<OUT_BF16>(v[8 * j], v[8 * j + 1]),
+                stmatrix_x4_trans(stage_base + row * 256 + u * 16, grouped_pack2<OUT_BF16>(v[8 * j], v[8 * j + 1]),
                                   grouped_pack2<OUT_BF16>(v[8 * j + 2], v[8 * j + 3]),
                                   grouped_pack2<OUT_BF16>(v[8 * j + 4], v[8 * j + 5]),
                                   grouped_pack2<OUT_BF16>(v[8 * j + 6], v[8 * j + 7]));
             }
-            barrier();  // (the other buffer's readers are past the barrier before this one)
-            const int col0 = (w.tm * Cf::CM + rank) * 128;
-            uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) +
-                           2 * ((INNER ? (int64_t)w.group * p.out_group : 0) + (int64_t)w.n0 * p.m_total);
+            named_bar_sync(G_BAR_HALF + half, 128);
+            uint4 x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (et >> 4) + 8 * i, u = et & 15;
-                const uint4 x = ld_shared_u4(base + row * 256 + ((u ^ (row & 7)) * 16));
-                if (32 * c + row < w.valid && col0 + u * 8 < p.m_total)
-                    st_u4(dst + 2 * ((int64_t)(32 * c + row) * p.m_total + col0 + u * 8), x.x, x.y, x.z, x.w);
-            }
+            for (int i = 0; i < 4; ++i)
+                x[i] = ld_shared_u4(stage_base + (read_row + 8 * i) * 256 + ((read_unit ^ read_row) * 16));
+            const int col = (w.tm * Cf::CM + rank) * 128 + read_unit * 8, row = 32 * c + read_row;
+            uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) +
+                           2 * ((INNER ? (int64_t)w.group * p.out_group : 0) +
+                                (int64_t)(w.n0 + row) * p.m_total + col);
+            const int64_t step = (int64_t)p.m_total * 16;  // bytes of 8 rows
+            if (col < p.m_total)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row + 8 * i < w.valid) st_u4(dst + i * step, x[i].x, x[i].y, x[i].z, x[i].w);
         };
-        while (grouped_cursor_next(p.s, tab, cur, w)) {
+        while (true) {
+            const bool more = next_work();
             const bool empty = w.k1 <= w.k0;
             const bool split = w.k1 - w.k0 < w.kb;
             const int buf = iter & 1;
             const int chunks = (w.valid + 31) / 32;
+            const bool got = more && (empty || (mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) &&
+                                                *abort_flag == 0));
+            if (more && !got && lane == 0) fail_pipe();
+            // (a warp that gives up must not leave the others at a barrier)
+            if (!grouped_vote_all(got)) break;
             if (!empty) {
-                const bool got = mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) && !*abort_flag;
-                if (!grouped_vote_all(got)) {
-                    if (et == 0) fail_pipe();
-                    break;
-                }
                 tc_fence_after_sync();
             }
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * Cf::TILE_N);
@@ -517,7 +635,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 slot = reinterpret_cast<float4*>(p.partials +
                                                  (size_t)(2 * blockIdx.x + (w.k0 > 0 ? 0 : 1)) * Cf::SLOT_FLOATS);
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = half; c < chunks; c += 2) {
                 uint32_t r[32];
                 float v[32];
                 if (empty) {
@@ -532,7 +650,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 if (split) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        st_f4(slot + (c * 8 + i) * G_EPI_THREADS + et,
+                        st_f4(slot + (c * 8 + i) * 128 + et,
                               make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
                 } else {
                     store_chunk(v, c);
@@ -548,11 +666,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 ++iter;
             }
             if (split) {
-                const int64_t base_it = (int64_t)w.tile * w.kb;
-                const int u0 = grouped_split_unit(cur, base_it), u1 = grouped_split_unit(cur, base_it + w.kb - 1);
+                const int u0 = share.u0, u1 = share.u1;
                 __threadfence();
                 barrier();
-                if (et == 0)
+                if (lead)
                     *last_flag = grouped_count_in(p.counters + (size_t)w.tile * Cf::CM + rank, p.epoch,
                                                   (uint32_t)(u1 - u0 + 1));
                 barrier();
@@ -561,7 +678,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 if (last) {
                     __threadfence();
 #pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
+                    for (int c = half; c < chunks; c += 2) {
                         float v[32];
 #pragma unroll 1
                         for (int x = u0; x <= u1; ++x) {
@@ -569,10 +686,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                             const float4* from =
                                 reinterpret_cast<const float4*>(
                                     p.partials + (size_t)(2 * (x * Cf::CM + rank) + (x > u0 ? 0 : 1)) * Cf::SLOT_FLOATS) +
-                                c * 8 * G_EPI_THREADS + et;
+                                c * 8 * 128 + et;
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 y = ld_cg_f4(from + i * G_EPI_THREADS);
+                                const float4 y = ld_cg_f4(from + i * 128);
                                 v[4 * i] = x > u0 ? v[4 * i] + y.x : y.x;
                                 v[4 * i + 1] = x > u0 ? v[4 * i + 1] + y.y : y.y;
                                 v[4 * i + 2] = x > u0 ? v[4 * i + 2] + y.z : y.z;
@@ -587,7 +704,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         if constexpr (!INNER) {
             // the unused rows: +0, 16 bytes a thread
             const int64_t begin = (int64_t)off[p.s.groups] * p.m_total / 8, end = (int64_t)p.s.rows * p.m_total / 8;
-            for (int64_t i = begin + (int64_t)blockIdx.x * G_EPI_THREADS + et; i < end;
+            for (int64_t i = begin + (int64_t)blockIdx.x * G_EPI_THREADS + (threadIdx.x - G_EPI_WARP0 * 32); i < end;
                  i += (int64_t)gridDim.x * G_EPI_THREADS)
                 st_u4(reinterpret_cast<uint8_t*>(p.out) + i * 16, 0, 0, 0, 0);
         }

@@ -20,7 +20,8 @@ def _plan(kind, groups, rows, N, K, layout=1, sms=152, ctas=None):
 
 CASES = [([1], 8, 8), ([0, 1, 0], 64, 128), ([8] * 8, 1536, 2048), ([3, 0, 5, 1], 264, 520),
          ([1000, 0, 17, 256, 257, 255], 776, 200), ([0, 0], 64, 64), ([5000], 4096, 1024), ([2] * 300, 128, 4096),
-         ([129, 3000, 1], 14336, 4096), ([0, 700, 0], 2048, 72)]
+         ([129, 3000, 1], 14336, 4096), ([0, 700, 0], 2048, 72), ([4000, 0, 70, 0], 256, 128), ([0, 5000, 3], 8, 8),
+         ([3000, 40, 50, 0, 2000, 60, 70, 80, 1] * 4, 512, 640)]
 
 
 @pytest.mark.parametrize("ctas", [1, 2])
@@ -35,10 +36,7 @@ def test_units_cover_every_tile_once(counts, N, K, kind, sms, ctas):
     m_total = K if inner else N  # col-major matrices: K is contiguous in C for INNER
     tiles = {}
     for u in range(p.info("units")):
-        seen = -1
         for tile, g, tm, n0, valid, width, k0, k1, kb in p.units(offsets, u):
-            assert tile > seen or (tile == seen and k0 > 0)  # in order, so a group search never goes back
-            seen = tile
             tiles.setdefault(tile, []).append((k0, k1, g, tm, n0, valid, width, kb))
             n = counts[g]
             assert kb == ((n if inner else K) + 63) // 64 and 0 <= k0 <= k1 <= kb and (k1 > k0 or (inner and n == 0))
@@ -74,6 +72,14 @@ def test_shares_are_even_and_at_least_the_minimum():
     offsets = np.minimum(np.arange(65), 8)
     loads = [sum(k1 - k0 for *_, k0, k1, _ in p.units(offsets, u)) for u in range(152)]
     assert sum(loads) == 96 * 32 and max(loads) - min(loads) <= 1
+    p.close()
+
+
+def test_summed_rows_are_split_when_tiles_are_few():
+    """One 256 x 256 gradient over 16384 rows: eight shares of 32 k-blocks."""
+    p = _plan(B.GEMM_GROUPED_INNER, 1, 16384, 256, 256)
+    loads = [sum(k1 - k0 for *_, k0, k1, _ in p.units([0, 16384], u)) for u in range(p.info("units"))]
+    assert sorted(loads)[-8:] == [32] * 8 and sum(loads) == 256 and p.workspace_size > 0
     p.close()
 
 
