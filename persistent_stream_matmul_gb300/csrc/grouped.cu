@@ -159,6 +159,7 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     s.n_total = (int32_t)n_total;
     s.kb = inner ? 0 : (int32_t)cdiv(p->K, G_BK);
     s.tile_n = tile;
+    s.tile_shift = ctas == 2 ? 8 : 7;
     s.step = 16 * ctas;
     s.band = 8;
     s.units = p->num_sms / ctas;

@@ -79,7 +79,7 @@ struct GroupedCfg {
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
     static constexpr int STAGES = 6;
     static constexpr int OUT_BYTES = 32 * 256;    // one staged chunk: 32 rows x 128 columns
-    static constexpr int TABLE_BYTES = 3 * (G_MAX_GROUPS + 4) * 4 + 12 * (G_THREADS / 32);  // and scan scratch
+    static constexpr int TABLE_BYTES = 3 * (G_MAX_GROUPS + 4) * 4;
     static constexpr int QUEUE_BYTES = G_QUEUE * 64;
     static constexpr int BAR_BYTES = 320;
     static constexpr int TMEM_COLS = 2 * TILE_N;  // two accumulators
@@ -133,74 +133,72 @@ __device__ __forceinline__ uint32_t grouped_pack2(float a, float b) {
     }
 }
 
-// The whole CTA: the scheduler's tables from the device offsets, bounded (a
-// value out of order or range becomes the nearest one in order and range).
-// Each thread takes a few consecutive groups; sums and maxima go through
-// warp scans.  One warp that took 32 groups at a time, and units that walked
-// the groups one by one, spent 2.5 us more before the first copy with 64
-// groups, of the 18 us that one token then took.
+// One warp: the scheduler's tables from the device offsets, bounded (a value
+// out of order or range becomes the nearest one in order and range).  128
+// entries at a time, four a lane, the next ones loaded ahead of the scans.
 __device__ __forceinline__ void grouped_tables(const GroupedShape& s, const int32_t* offsets, int32_t* off,
-                                               int32_t* first, int32_t* iters,
-                                               int32_t* scratch) {
-    constexpr int PER = (G_MAX_GROUPS + G_THREADS) / G_THREADS;  // of groups + 1 entries
-    constexpr int WARPS = G_THREADS / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (s.groups + G_THREADS) / G_THREADS;
-    const int i0 = threadIdx.x * per;
-    int32_t v[PER];
-    int32_t top = 0;
+                                               int32_t* first, int32_t* iters) {
+    const int lane = threadIdx.x & 31;
+    int32_t v[4], next[4];
+    auto load = [&](int base, int32_t (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = i < per && i0 + i <= s.groups ? offsets[i0 + i] : 0;
+        for (int i = 0; i < 4; ++i) x[i] = base + lane * 4 + i <= s.groups ? offsets[base + lane * 4 + i] : 0;
+    };
+    load(0, v);
+    int32_t top = 0, tiles = 0, blocks = 0, last = 0;  // carried: maximum, sums, and the last entry
+    for (int base = 0; base <= s.groups; base += 128) {
+        load(base + 128, next);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = top = max(top, min(v[i], s.rows));
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t u = __shfl_up_sync(0xffffffffu, top, o);
-        if (lane >= o) top = max(top, u);
-    }
-    if (lane == 31) scratch[warp] = top;
-    top = __shfl_up_sync(0xffffffffu, top, 1);
-    if (lane == 0) top = 0;
-    __syncthreads();
-    for (int x = 0; x < warp; ++x) top = max(top, scratch[x]);
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (i < per && i0 + i <= s.groups) off[i0 + i] = max(v[i], top);
-    __syncthreads();
-    GroupedCounts mine[PER], sum{0, 0};
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        mine[i] = sum;
-        if (i < per && i0 + i < s.groups) {
-            const GroupedCounts c = grouped_counts(s, off[i0 + i + 1] - off[i0 + i]);
-            sum.tiles += c.tiles;
-            sum.iters += c.iters;
+        for (int i = 0; i < 4; ++i) v[i] = max(i ? v[i - 1] : 0, min(v[i], s.rows));
+        int32_t m = v[3];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, u);
         }
-    }
-    const GroupedCounts own = sum;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t a = __shfl_up_sync(0xffffffffu, sum.tiles, o);
-        const int32_t c = __shfl_up_sync(0xffffffffu, sum.iters, o);
-        if (lane >= o) {
-            sum.tiles += a;
-            sum.iters += c;
-        }
-    }
-    int32_t* warps = scratch + WARPS;
-    if (lane == 31) {
-        warps[warp] = sum.tiles;
-        warps[WARPS + warp] = sum.iters;
-    }
-    __syncthreads();
-    for (int x = 0; x < warp; ++x) {
-        sum.tiles += warps[x];
-        sum.iters += warps[WARPS + x];
-    }
+        int32_t before = __shfl_up_sync(0xffffffffu, m, 1);
+        before = max(top, lane ? before : 0);
+        top = max(top, __shfl_sync(0xffffffffu, m, 31));
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (i < per && i0 + i <= s.groups) {
-            first[i0 + i] = sum.tiles - own.tiles + mine[i].tiles;
-            iters[i0 + i] = sum.iters - own.iters + mine[i].iters;
+        for (int i = 0; i < 4; ++i) v[i] = max(v[i], before);
+        // entry i closes group i - 1
+        int32_t prev = __shfl_up_sync(0xffffffffu, v[3], 1);
+        if (lane == 0) prev = last;
+        last = __shfl_sync(0xffffffffu, v[3], 31);
+        GroupedCounts c[4], sum{0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = base + lane * 4 + i;
+            if (g > 0 && g <= s.groups) {
+                const GroupedCounts x = grouped_counts(s, v[i] - (i ? v[i - 1] : prev));
+                sum.tiles += x.tiles;
+                sum.iters += x.iters;
+            }
+            c[i] = sum;
         }
+        GroupedCounts run = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t a = __shfl_up_sync(0xffffffffu, run.tiles, o);
+            const int32_t b = __shfl_up_sync(0xffffffffu, run.iters, o);
+            if (lane >= o) {
+                run.tiles += a;
+                run.iters += b;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = base + lane * 4 + i;
+            if (g <= s.groups) {
+                off[g] = v[i];
+                first[g] = tiles + run.tiles - sum.tiles + c[i].tiles;
+                iters[g] = blocks + run.iters - sum.iters + c[i].iters;
+            }
+        }
+        tiles += __shfl_sync(0xffffffffu, run.tiles, 31);
+        blocks += __shfl_sync(0xffffffffu, run.iters, 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = next[i];
+    }
+    __syncwarp();
 }
 
 // AND of a predicate over the epilogue threads.
@@ -216,11 +214,6 @@ __device__ __forceinline__ bool grouped_vote_all(bool v) {
         : "memory");
     return out != 0;
 }
-
-// The first and last contributor of a split tile.
-struct GroupedShare {
-    int32_t u0, u1;
-};
 
 struct GroupedQMaps {
     CUtensorMap m[4];  // ROWS: boxes of 16, 32, 64 and 128 rows; INNER: m[0], 64 x 64
@@ -304,14 +297,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             tmem_relinquish();
         }
     }
-    // everything above may overlap the previous kernel in the stream
-    grid_dependency_wait();
-    if (threadIdx.x == 0) grid_launch_dependents();
-    grouped_tables(p.s, p.offsets, off, first, iters, iters + G_MAX_GROUPS + 4);
     tc_fence_before_sync();
     if constexpr (PAIR) cluster_sync_all();
     else __syncthreads();
     tc_fence_after_sync();
+    // everything above may overlap the previous kernel in the stream
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_launch_dependents();
     const uint32_t tmem_base = *tmem_slot;
 
     auto fail_pipe = [&]() {
@@ -320,7 +312,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     };
 
     GroupedWork w{};
-    GroupedShare share{};
+    int32_t split_q = 0, split_r = 0;  // the cursor's
     int qslot = 0;
     uint32_t qphase = 0;
     // The next piece of work, for a whole warp; false at the end or after a
@@ -341,8 +333,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
         w = GroupedWork{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y,
                         (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
-        share.u0 = (int)d.x;
-        share.u1 = (int)d.y;
+        split_q = (int)d.x;
+        split_r = (int)d.y;
         return w.tile >= 0;
     };
     // INNER: whether k-block kb ends inside a 16-row step
@@ -551,15 +543,17 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ scheduler
+        grouped_tables(p.s, p.offsets, off, first, iters);
         const GroupedTables tab{off, first, iters};
         GroupedCursor cur;
         grouped_cursor_init(p.s, tab, unit, cur);
         bool more = true;
         while (more) {
             more = grouped_cursor_next(p.s, tab, cur, w);
-            if (!more) w.tile = -1;
-            else if (w.k1 - w.k0 < w.kb)
-                share = GroupedShare{grouped_split_unit(cur, w.it0), grouped_split_unit(cur, w.it0 + w.kb - 1)};
+            if (!more) {
+                w.tile = -1;
+                w.r0 = off[p.s.groups];  // the end carries the first unused row
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(qempty_bar(qslot), qphase ^ 1u, p.pipe_limit_ns))) {
                 if (lane == 0) fail_pipe();
                 break;
@@ -569,7 +563,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 st_shared_u4(at, w.tile, w.it0, w.group, w.tm);
                 st_shared_u4(at + 16, w.n0, w.width, w.valid, w.r0);
                 st_shared_u4(at + 32, w.r1, w.k0, w.k1, w.kb);
-                st_shared_u4(at + 48, share.u0, share.u1, 0, 0);
+                st_shared_u4(at + 48, cur.q, cur.r, 0, 0);
                 mbar_arrive(qfull_bar(qslot));
             }
             __syncwarp();
@@ -585,6 +579,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int et = (threadIdx.x - G_EPI_WARP0 * 32) & 127;  // thread of its half
         const bool lead = threadIdx.x == G_EPI_WARP0 * 32;
         uint32_t iter = 0;
+        int32_t unused = p.s.rows;  // first unused row, from the end of the queue
         auto barrier = [&]() { named_bar_sync(G_BAR_EPI, G_EPI_THREADS); };
         const uint32_t stage_base = out_stage + half * Cf::OUT_BYTES;
         const int read_row = et >> 4, read_unit = et & 15;
@@ -621,11 +616,19 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const bool split = w.k1 - w.k0 < w.kb;
             const int buf = iter & 1;
             const int chunks = (w.valid + 31) / 32;
+            int u0 = 0, u1 = 0;  // contributors of a split tile
+            if (more && split) {
+                u0 = grouped_split_unit(split_q, split_r, w.it0);
+                u1 = grouped_split_unit(split_q, split_r, w.it0 + w.kb - 1);
+            }
             const bool got = more && (empty || (mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) &&
                                                 *abort_flag == 0));
             if (more && !got && lane == 0) fail_pipe();
             // (a warp that gives up must not leave the others at a barrier)
-            if (!grouped_vote_all(got)) break;
+            if (!grouped_vote_all(got)) {
+                if (w.tile < 0) unused = w.r0;
+                break;
+            }
             if (!empty) {
                 tc_fence_after_sync();
             }
@@ -666,8 +669,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 ++iter;
             }
             if (split) {
-                const int u0 = share.u0, u1 = share.u1;
-                __threadfence();
+                // the barrier orders the partial's stores before the lead's
+                // count, a release and acquire at GPU scope
                 barrier();
                 if (lead)
                     *last_flag = grouped_count_in(p.counters + (size_t)w.tile * Cf::CM + rank, p.epoch,
@@ -676,25 +679,38 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 const bool last = *last_flag != 0;
                 barrier();
                 if (last) {
-                    __threadfence();
 #pragma unroll 1
                     for (int c = half; c < chunks; c += 2) {
                         float v[32];
-#pragma unroll 1
-                        for (int x = u0; x <= u1; ++x) {
-                            // the tile's first contributor holds k-block 0: its unit's last share
-                            const float4* from =
-                                reinterpret_cast<const float4*>(
-                                    p.partials + (size_t)(2 * (x * Cf::CM + rank) + (x > u0 ? 0 : 1)) * Cf::SLOT_FLOATS) +
-                                c * 8 * 128 + et;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 y = ld_cg_f4(from + i * 128);
-                                v[4 * i] = x > u0 ? v[4 * i] + y.x : y.x;
-                                v[4 * i + 1] = x > u0 ? v[4 * i + 1] + y.y : y.y;
-                                v[4 * i + 2] = x > u0 ? v[4 * i + 2] + y.z : y.z;
-                                v[4 * i + 3] = x > u0 ? v[4 * i + 3] + y.w : y.w;
-                            }
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        // two contributors' loads are in flight together
+#pragma unroll 1
+                        for (int x = u0; x <= u1; x += 2) {
+                            float4 y[2][8];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (x + h <= u1) {
+                                    // the tile's first contributor holds k-block 0: its unit's last share
+                                    const float4* from =
+                                        reinterpret_cast<const float4*>(
+                                            p.partials +
+                                            (size_t)(2 * ((x + h) * Cf::CM + rank) + (x + h > u0 ? 0 : 1)) *
+                                                Cf::SLOT_FLOATS) +
+                                        c * 8 * 128 + et;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) y[h][i] = ld_cg_f4(from + i * 128);
+                                }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (x + h <= u1)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        v[4 * i] += y[h][i].x;
+                                        v[4 * i + 1] += y[h][i].y;
+                                        v[4 * i + 2] += y[h][i].z;
+                                        v[4 * i + 3] += y[h][i].w;
+                                    }
                         }
                         store_chunk(v, c);
                     }
@@ -703,7 +719,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
         if constexpr (!INNER) {
             // the unused rows: +0, 16 bytes a thread
-            const int64_t begin = (int64_t)off[p.s.groups] * p.m_total / 8, end = (int64_t)p.s.rows * p.m_total / 8;
+            const int64_t begin = (int64_t)unused * p.m_total / 8, end = (int64_t)p.s.rows * p.m_total / 8;
             for (int64_t i = begin + (int64_t)blockIdx.x * G_EPI_THREADS + (threadIdx.x - G_EPI_WARP0 * 32); i < end;
                  i += (int64_t)gridDim.x * G_EPI_THREADS)
                 st_u4(reinterpret_cast<uint8_t*>(p.out) + i * 16, 0, 0, 0, 0);

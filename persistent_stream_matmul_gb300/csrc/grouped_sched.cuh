@@ -28,7 +28,8 @@ struct GroupedShape {
     int32_t tiles_n;       // INNER: tiles along the other side of the output
     int32_t n_total;       // INNER: extent of that side
     int32_t kb;            // ROWS: k-blocks of 64 a tile
-    int32_t tile_n, step;
+    int32_t tile_n, step;  // tile_n: 1 << tile_shift; step a power of two
+    int32_t tile_shift;
     int32_t band;          // raster: tiles along the columns side visited before the next lanes tile
     int32_t units;         // scheduling units
     int32_t may_split;     // the k-blocks of fewer than `units` tiles fit an int32
@@ -48,7 +49,7 @@ struct GroupedCounts {
 
 __host__ __device__ __forceinline__ GroupedCounts grouped_counts(const GroupedShape& s, int32_t n) {
     GroupedCounts c;
-    c.tiles = s.inner ? s.tiles_m * s.tiles_n : s.tiles_m * ((n + s.tile_n - 1) / s.tile_n);
+    c.tiles = s.inner ? s.tiles_m * s.tiles_n : s.tiles_m * ((n + s.tile_n - 1) >> s.tile_shift);
     c.iters = s.inner && s.may_split ? c.tiles * ((n + 63) / 64) : 0;
     return c;
 }
@@ -85,7 +86,7 @@ __host__ __device__ __forceinline__ void grouped_cursor_init(const GroupedShape&
         // tile: the joined time is least near sqrt(k-blocks) / 2 shares a
         // tile.  Narrow tiles, bound by the reads of the matrix, bear twice that.
         const int32_t total = s.inner ? t.iters[s.groups] : c.tiles * s.kb;
-        const int32_t mean = total / c.tiles;
+        const int32_t mean = s.inner ? total / c.tiles : s.kb;
         int32_t shares = 1;
         while (shares < 32 && (shares + 1) * (shares + 1) <= (s.step == 16 ? mean : mean / 4)) ++shares;
         const int32_t n = c.tiles * shares < s.units ? c.tiles * shares : s.units;
@@ -98,22 +99,32 @@ __host__ __device__ __forceinline__ void grouped_cursor_init(const GroupedShape&
     }
 }
 
-// The unit that runs split k-block `it`.
-__host__ __device__ __forceinline__ int32_t grouped_split_unit(const GroupedCursor& c, int32_t it) {
-    const int32_t big = c.r * (c.q + 1);
-    return it < big ? it / (c.q + 1) : c.r + (it - big) / c.q;
+// The unit that runs split k-block `it`, for a cursor's q and r.
+__host__ __device__ __forceinline__ int32_t grouped_split_unit(int32_t q, int32_t r, int32_t it) {
+    const int32_t big = r * (q + 1);
+    return it < big ? it / (q + 1) : r + (it - big) / q;
 }
 
-// The group g with sum(g) <= x < sum(g + 1).
-template <typename F>
-__host__ __device__ __forceinline__ int32_t grouped_search(int32_t groups, int32_t x, F sum) {
-    int32_t lo = 0, hi = groups;  // sum(lo) <= x < sum(hi)
+// The group g with sum[g] <= x < sum[g + 1].
+__host__ __device__ __forceinline__ int32_t grouped_search(int32_t groups, int32_t x, const int32_t* sum) {
+#ifdef __CUDA_ARCH__
+    const int lane = threadIdx.x & 31;
+    int32_t base = 0;
+    if (groups > 32) {
+        const int32_t i = lane * 32;
+        base = 32 * (__popc(__ballot_sync(0xffffffffu, i < groups && sum[i] <= x)) - 1);
+    }
+    const int32_t i = base + lane;
+    return base + __popc(__ballot_sync(0xffffffffu, i < groups && sum[i] <= x)) - 1;
+#else
+    int32_t lo = 0, hi = groups;  // sum[lo] <= x < sum[hi]
     while (hi - lo > 1) {
         const int32_t mid = (lo + hi) >> 1;
-        if (sum(mid) <= x) lo = mid;
+        if (sum[mid] <= x) lo = mid;
         else hi = mid;
     }
     return lo;
+#endif
 }
 
 __host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape& s, const GroupedTables& t,
@@ -125,7 +136,7 @@ __host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape&
         if (c.it < c.it_end) {
             w.k1 = c.it_end - c.it;  // an upper bound, from k0
             if (s.inner) {
-                g = grouped_search(s.groups, c.it, [&](int32_t i) { return t.iters[i]; });
+                g = grouped_search(s.groups, c.it, t.iters);
                 const int32_t kb = (t.off[g + 1] - t.off[g] + 63) / 64;
                 local = (c.it - t.iters[g]) / kb;
                 w.it0 = t.iters[g] + local * kb;
@@ -133,7 +144,7 @@ __host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape&
             } else {
                 w.tile = c.it / s.kb;
                 w.it0 = w.tile * s.kb;
-                g = grouped_search(s.groups, w.tile, [&](int32_t i) { return t.first[i]; });
+                g = grouped_search(s.groups, w.tile, t.first);
                 local = w.tile - t.first[g];
             }
             w.k0 = c.it - w.it0;
@@ -141,7 +152,7 @@ __host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape&
             w.tile = c.next_tile;
             c.next_tile += s.units;
             w.it0 = 0;
-            g = grouped_search(s.groups, w.tile, [&](int32_t i) { return t.first[i]; });
+            g = grouped_search(s.groups, w.tile, t.first);
             local = w.tile - t.first[g];
             // INNER: a split leaves the tiles of empty groups to be cleared
             if (c.split && t.off[g + 1] > t.off[g]) continue;
@@ -154,19 +165,25 @@ __host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape&
     w.r0 = t.off[g];
     w.r1 = t.off[g + 1];
     const int32_t n = w.r1 - w.r0;
-    const int32_t side = s.inner ? s.tiles_n : (n + s.tile_n - 1) / s.tile_n;
-    // bands of `band` tiles along the columns side, the lanes side slow within one
-    const int32_t b = local / (s.band * s.tiles_m), in = local - b * s.band * s.tiles_m;
-    const int32_t wide = side - b * s.band < s.band ? side - b * s.band : s.band;
-    w.tm = in / wide;
-    const int32_t tn = b * s.band + in - w.tm * wide;
+    const int32_t side = s.inner ? s.tiles_n : (n + s.tile_n - 1) >> s.tile_shift;
+    // bands of `band` tiles along the columns side, the lanes side slow within
+    // one; without the divisions that the common shapes do not need
+    int32_t first_tn = 0, wide = side;
+    if (side > s.band) {
+        const int32_t b = local / (s.band * s.tiles_m);
+        local -= b * s.band * s.tiles_m;
+        first_tn = b * s.band;
+        wide = side - first_tn < s.band ? side - first_tn : s.band;
+    }
+    w.tm = wide == 1 ? local : local / wide;
+    const int32_t tn = first_tn + local - w.tm * wide;
     if (s.inner) {
         w.width = s.tile_n;
         w.n0 = tn * s.tile_n;
         w.valid = s.n_total - w.n0 < s.tile_n ? s.n_total - w.n0 : s.tile_n;
         w.kb = (n + 63) / 64;
     } else {
-        w.width = ((n + side - 1) / side + s.step - 1) / s.step * s.step;
+        w.width = ((side == 1 ? n : (n + side - 1) / side) + s.step - 1) & ~(s.step - 1);
         w.n0 = w.r0 + tn * w.width;
         w.valid = w.r1 - w.n0 < w.width ? w.r1 - w.n0 : w.width;
         w.kb = s.kb;
