@@ -65,8 +65,9 @@ gemm_status_t gemm_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t
  * tokens == 0: only offsets is written, as zeros.
  * Errors: INVALID_ARG (NULL operand, negative size, topk < 1, experts < 1,
  * ld_ids < topk, bad id_type), UNSUPPORTED (experts > GEMM_MOE_MAX_EXPERTS,
- * tokens * topk > 2^31 - 1024, an operand not aligned to its element),
- * WORKSPACE (NULL or not 16-byte aligned while one is needed), LAUNCH.
+ * topk > 65535, tokens * topk > 2^31 - 1024, an operand not aligned to its
+ * element),
+ * WORKSPACE (NULL or not 16-byte aligned while one is needed), CUDA, LAUNCH.
  */
 gemm_status_t gemm_moe_sort(const void *ids, gemm_index_t id_type, int64_t ld_ids, int64_t tokens,
                             int64_t topk, int64_t experts, int32_t *offsets, int32_t *rows,
@@ -77,9 +78,9 @@ gemm_status_t gemm_moe_sort(const void *ids, gemm_index_t id_type, int64_t ld_id
  * unused rows.  x: tokens x hidden; xs: (tokens * topk) x hidden; rows and
  * slots as gemm_moe_sort wrote them.
  * Errors (this and the next three): INVALID_ARG (NULL operand, negative size,
- * topk < 1, a leading dimension below hidden, bad dtype), UNSUPPORTED (tokens *
- * topk > 2^31 - 1024, hidden > 2^31 - 1024, an operand not aligned to its
- * element), LAUNCH.  tokens == 0 or hidden == 0: an empty output is left
+ * topk < 1, a leading dimension below hidden, bad dtype), UNSUPPORTED (topk >
+ * 65535, tokens * topk > 2^31 - 1024, hidden > 2^30, an operand not aligned to
+ * its element), LAUNCH.  tokens == 0 or hidden == 0: an empty output is left
  * alone.
  */
 gemm_status_t gemm_moe_dispatch(const void *x, int64_t ldx, const int32_t *rows,

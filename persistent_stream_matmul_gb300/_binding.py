@@ -123,19 +123,17 @@ def load(path: str = LIB_PATH):
 
 
 def _addr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return int(x.data_ptr())
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x  # an address or None
 
 
 def _stream(s) -> int | None:
-    if s is None:
-        return None
-    if isinstance(s, int):
-        return s
-    return int(s.cuda_stream)
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        return s  # a handle or None
 
 
 def _check(st: int, where: str):

@@ -15,6 +15,8 @@ using namespace psm;
 namespace {
 
 constexpr int64_t MAX_INDEX = (1ll << 31) - 1024;
+constexpr int64_t MAX_TOPK = 65535;
+constexpr int64_t MAX_HIDDEN = 1ll << 30;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -31,8 +33,10 @@ template <> __device__ __forceinline__ __half from_f<__half>(float v) { return _
 // block of place_kernel sums the table itself, so there is no third launch
 // and no block waits for another.  The counts are whole numbers, so the order
 // of the atomics in shared memory changes nothing.
-constexpr int SORT_CHUNK = 4096;   // slots a block, until there are SORT_BLOCKS
+constexpr int SORT_SINGLE = 4096;  // up to this many slots one block does it all
+constexpr int SORT_CHUNK = 4096;   // else slots a block, until there are SORT_BLOCKS
 constexpr int SORT_BLOCKS = 128;
+constexpr int SORT_BATCH = 8;      // slots a lane in flight
 
 struct SortArgs {
     int64_t ld, total, chunk;   // chunk: slots a block, a multiple of 1024
@@ -53,10 +57,13 @@ __global__ void __launch_bounds__(1024) count_kernel(const I* ids, SortArgs a, u
     grid_launch_dependents();
     __syncthreads();
     const int64_t s0 = (int64_t)blockIdx.x * a.chunk, s1 = min(a.total, s0 + a.chunk);
-#pragma unroll 4
-    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
-        const int e = key_of(ids, a, s);
-        if (e < a.experts) atomicAdd(&hist[e], 1u);
+    for (int64_t b = s0 + threadIdx.x; b < s1; b += 4 * blockDim.x) {
+        int e[4];  // four loads in flight
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = b + i * blockDim.x < s1 ? key_of(ids, a, b + i * blockDim.x) : a.experts;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (e[i] < a.experts) atomicAdd(&hist[e[i]], 1u);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
@@ -79,20 +86,43 @@ __global__ void __launch_bounds__(1024)
     __syncthreads();
     const int64_t per = a.chunk / warps;
     const int64_t w0 = blockIdx.x * a.chunk + warp * per, w1 = min(a.total, w0 + per);
-    // this block's counts by warp
-    for (int64_t b = w0; b < w1; b += 32) {
-        const int e = b + lane < w1 ? key_of(ids, a, b + lane) : E;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e < E && lane == __ffs(same) - 1) own[e] += __popc(same);
-        __syncwarp();
-    }
+    // This block's counts by warp, SORT_BATCH slots a lane loaded ahead.  A slot's
+    // place among its warp's slots of the same expert is the count so far and
+    // the equal keys in lower lanes.  The lanes with an equal key come from one
+    // ballot a key bit; __match_any_sync took about three times as long.
+    int bits = 1;
+    while ((1 << bits) <= E) ++bits;
+    int key[SORT_BATCH];
+    uint32_t place[SORT_BATCH];
+    auto count_batch = [&](int64_t b) {
+#pragma unroll
+        for (int i = 0; i < SORT_BATCH; ++i) {
+            const int64_t s = b + i * 32 + lane;
+            key[i] = s < w1 ? key_of(ids, a, s) : E;
+        }
+#pragma unroll
+        for (int i = 0; i < SORT_BATCH; ++i) {
+            if (b + i * 32 >= w1) break;
+            unsigned same = 0xffffffffu;
+            for (int bit = 0; bit < bits; ++bit) {
+                const unsigned ones = __ballot_sync(0xffffffffu, (key[i] >> bit) & 1);
+                same &= (key[i] >> bit) & 1 ? ones : ~ones;
+            }
+            const uint32_t at = key[i] < E ? own[key[i]] : 0;
+            place[i] = at + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (key[i] < E && lane == __ffs(same) - 1) own[key[i]] = at + __popc(same);
+            __syncwarp();
+        }
+    };
+    for (int64_t b = w0; b < w1; b += 32 * SORT_BATCH) count_batch(b);
     // all blocks' counts, and those of the blocks before this one
     if (a.blocks > 1) {
         const int parts = max(1, (int)blockDim.x / E);
         for (int i = threadIdx.x; i < parts * E; i += blockDim.x) {
             const int e = i % E;
             uint32_t sum = 0, prior = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (int b = i / E; b < a.blocks; b += parts) {
                 const uint32_t c = table[(size_t)b * E + e];
                 sum += c;
@@ -104,8 +134,12 @@ __global__ void __launch_bounds__(1024)
         __syncthreads();
     } else {
         __syncthreads();
-        for (int e = threadIdx.x; e < E; e += blockDim.x)
-            for (int w = 0; w < warps; ++w) all[e] += mine[w * E + e];
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            uint32_t sum = 0;
+#pragma unroll 8
+            for (int w = 0; w < warps; ++w) sum += mine[w * E + e];
+            all[e] = sum;
+        }
         __syncthreads();
     }
     // exclusive sum over the experts, blockDim.x at a time
@@ -133,31 +167,36 @@ __global__ void __launch_bounds__(1024)
         carry += sums[warps - 1];
         if (e < E) {
             uint32_t at = first + before[e];
-            for (int w = 0; w < warps; ++w) {
-                const uint32_t n = mine[w * E + e];
-                mine[w * E + e] = at;
-                at += n;
+            for (int w = 0; w < warps; w += 8) {  // warps is a multiple of 8
+                uint32_t n[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n[i] = mine[(w + i) * E + e];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    mine[(w + i) * E + e] = at;
+                    at += n[i];
+                }
             }
             if (blockIdx.x == 0) offsets[e] = (int32_t)first;
         }
         __syncthreads();
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = (int32_t)carry;
-    for (int64_t b = w0; b < w1; b += 32) {
-        const bool in = b + lane < w1;
-        const int e = in ? key_of(ids, a, b + lane) : E;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const uint32_t at = e < E ? own[e] : 0;
-        __syncwarp();
-        if (e < E) {
-            const uint32_t r = at + __popc(same & ((1u << lane) - 1));
-            rows[b + lane] = (int32_t)r;
-            slots[r] = (int32_t)(b + lane);
-            if (lane == __ffs(same) - 1) own[e] = at + __popc(same);
-        } else if (in) {
-            rows[b + lane] = -1;
+    // place: own[e] now holds the warp's first row of expert e
+    const bool one_batch = w1 - w0 <= 32 * SORT_BATCH;  // its keys and places are still here
+    for (int64_t b = w0; b < w1; b += 32 * SORT_BATCH) {
+        if (!one_batch) count_batch(b);  // advances own, so that places are rows
+#pragma unroll
+        for (int i = 0; i < SORT_BATCH; ++i) {
+            const int64_t s = b + i * 32 + lane;
+            if (key[i] < E) {
+                const uint32_t r = one_batch ? own[key[i]] + place[i] : place[i];
+                rows[s] = (int32_t)r;
+                slots[r] = (int32_t)s;
+            } else if (s < w1) {
+                rows[s] = -1;
+            }
         }
-        __syncwarp();
     }
     for (int64_t r = carry + blockIdx.x * (int64_t)blockDim.x + threadIdx.x; r < a.total;
          r += (int64_t)gridDim.x * blockDim.x)
@@ -170,172 +209,325 @@ SortArgs sort_shape(int64_t tokens, int64_t topk, int64_t experts) {
     a.topk = (int)topk;
     a.experts = (int)experts;
     const int64_t even = (a.total + SORT_BLOCKS - 1) / SORT_BLOCKS;
-    a.chunk = even > SORT_CHUNK ? (even + 1023) / 1024 * 1024 : SORT_CHUNK;
+    a.chunk = a.total <= SORT_SINGLE ? (a.total + 1023) / 1024 * 1024
+              : even > SORT_CHUNK    ? (even + 1023) / 1024 * 1024
+                                     : SORT_CHUNK;
+    if (a.chunk < 1024) a.chunk = 1024;
     a.blocks = (int)((a.total + a.chunk - 1) / a.chunk);
     if (a.blocks < 1) a.blocks = 1;
     return a;
 }
 
 // ---------------------------------------------------------------- row movements
-// Bound by memory: every row is read or written once, V elements (16 bytes
-// where all rows are 16-byte aligned, else one element) a thread and access.
-template <typename T, int V>
-struct alignas(V * sizeof(T)) Vec {
-    T v[V];
+// Bound by memory: every row is read or written once, 16 bytes a thread and
+// access.  A group of whole warps takes a row (blockDim = width x rows a
+// block), each thread C chunks of eight elements of it, strided by `width`,
+// and U rows at a time, B blocks of 256 an SM.  What counts is the bytes in
+// flight an SM, so U and C are weighed against the registers that B allows:
+// the sum of 2 choices of 16384 tokens of 4096 takes 68 us with U, C, B = 2, 1, 4
+// (5.9 TB/s), 71 with 2, 2, 4, 84 with 4, 1, 4 and 115 with 2, 2, 6, whose
+// registers spill.
+//
+// ALIGNED: every row starts at a 16-byte boundary and its length is a multiple
+// of 8.  Otherwise the chunks are cut at the 16-byte boundaries of the row
+// that is written, so its inner chunks are stored whole, and a chunk of
+// another row is put together from the two aligned 16-byte words that hold it
+// (words without an element of the row are not read).
+struct alignas(16) Chunk {
+    uint32_t w[4];
 };
 
-// i / d for 0 <= i, 0 < d: 32-bit division, several times shorter, where it does
-__device__ __forceinline__ int64_t quotient(int64_t i, int d) {
-    return i >> 32 ? i / d : (int64_t)((uint32_t)i / (uint32_t)d);
+// STREAM: read once; else the neighbouring thread's chunk shares the word.
+template <bool STREAM>
+__device__ __forceinline__ Chunk load_word(const void* p) {
+    const uint4* q = static_cast<const uint4*>(p);
+    const uint4 x = STREAM ? __ldcs(q) : __ldg(q);
+    return Chunk{{x.x, x.y, x.z, x.w}};
 }
 
-__device__ __forceinline__ bool in_range(int64_t r, int64_t total) { return r >= 0 && r < total; }
+// Elements h .. h + 7 of a row of n; those outside [0, n) are unspecified.
+template <bool ALIGNED>
+__device__ __forceinline__ Chunk load_chunk(const uint16_t* row, int h, int n) {
+    if constexpr (ALIGNED) return load_word<true>(row + h);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row) + 2 * (int64_t)h;
+    const int s = (int)(at >> 1) & 7;  // elements of the first word before the chunk
+    const char* word = reinterpret_cast<const char*>(at - 2 * s);
+    uint32_t w[8] = {};
+    if (h + 8 - s > 0 && h < n) {
+        const Chunk a = load_word<false>(word);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = a.w[i];
+    }
+    if (s > 0 && h + 8 > 0 && h + 8 - s < n) {
+        const Chunk b = load_word<false>(word + 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 + i] = b.w[i];
+    }
+    if (s & 1) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        w[7] >>= 16;
+    }
+    if (s & 2)
+#pragma unroll
+        for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+    if (s & 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = w[i + 2];
+    return Chunk{{w[0], w[1], w[2], w[3]}};
+}
 
-// out[rows[t, j]] = x[t] for one (token, chunk) a thread: x is read once.
-template <typename T, int V>
+template <bool ALIGNED>
+__device__ __forceinline__ void store_chunk(uint16_t* row, int h, int n, const Chunk& c) {
+    if (ALIGNED || (h >= 0 && h + 8 <= n)) {
+        *reinterpret_cast<uint4*>(row + h) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (h + i >= 0 && h + i < n) row[h + i] = (uint16_t)(c.w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// Elements of the row at `row` before its first 16-byte boundary cut, 0 .. 7:
+// chunk c of the row starts at element 8c - lead.
+template <bool ALIGNED>
+__device__ __forceinline__ int lead_of(const uint16_t* row) {
+    return ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 7;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Chunk& c, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w = c.w[i];
+        const T* e = reinterpret_cast<const T*>(&w);
+        x[2 * i] = to_f(e[0]);
+        x[2 * i + 1] = to_f(e[1]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Chunk pack(const float (&x)[8]) {
+    Chunk c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        T e[2] = {from_f<T>(x[2 * i]), from_f<T>(x[2 * i + 1])};
+        c.w[i] = *reinterpret_cast<uint32_t*>(e);
+    }
+    return c;
+}
+
+// A row index out of range counts as dropped.
+__device__ __forceinline__ int64_t row_at(const int32_t* rows, int64_t s, int64_t total) {
+    const int64_t r = rows[s];
+    return r >= 0 && r < total ? r : -1;
+}
+
+// out[rows[t, j]] = x[t], a token a thread group: x is read once (or, not
+// aligned, once more from the cache for every choice, cut for its row).
+template <bool ALIGNED, int C>
 __global__ void __launch_bounds__(256)
-    dispatch_kernel(const T* x, int64_t ldx, const int32_t* rows, const int32_t* slots, int topk,
-                    int64_t tokens, int chunks, T* out, int64_t ldo) {
-    using Vt = Vec<T, V>;
+    dispatch_kernel(const uint16_t* x, int64_t ldx, const int32_t* rows, const int32_t* slots, int topk,
+                    int64_t tokens, int n, uint16_t* out, int64_t ldo) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t total = tokens * topk, n = tokens * chunks;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = quotient(i, chunks), h = (i - t * chunks) * V;
-        const Vt v = *reinterpret_cast<const Vt*>(x + t * ldx + h);
-        for (int j = 0; j < topk; ++j) {
-            const int64_t s = t * topk + j, r = rows[s];
-            if (in_range(r, total)) *reinterpret_cast<Vt*>(out + r * ldo + h) = v;
-            if (slots[s] < 0) {  // row s is unused
-                Vt z;
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, total = tokens * topk;
+    if (t >= tokens) return;
+    const uint16_t* src = x + t * ldx;
+    const int width = blockDim.x, span = width * 8;
+    for (int h0 = threadIdx.x * 8; h0 < n + (ALIGNED ? 0 : 7); h0 += span * C) {
+        Chunk v[C];
+        if constexpr (ALIGNED)
 #pragma unroll
-                for (int k = 0; k < V; ++k) z.v[k] = from_f<T>(0.f);
-                *reinterpret_cast<Vt*>(out + s * ldo + h) = z;
+            for (int c = 0; c < C; ++c)
+                if (h0 + c * span < n) v[c] = load_chunk<true>(src, h0 + c * span, n);
+        for (int j = 0; j < topk; ++j) {
+            const int64_t s = t * topk + j, r = row_at(rows, s, total);
+            if (r >= 0) {
+                uint16_t* dst = out + r * ldo;
+                const int lead = lead_of<ALIGNED>(dst);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int h = h0 + c * span - lead;
+                    if constexpr (!ALIGNED)
+                        if (h < n) v[c] = load_chunk<false>(src, h, n);
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int h = h0 + c * span - lead;
+                    if (h < n) store_chunk<ALIGNED>(dst, h, n, v[c]);
+                }
+            }
+            if (slots[s] < 0) {  // row s is unused
+                uint16_t* dst = out + s * ldo;
+                const int lead = lead_of<ALIGNED>(dst);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int h = h0 + c * span - lead;
+                    if (h < n) store_chunk<ALIGNED>(dst, h, n, Chunk{});
+                }
             }
         }
     }
 }
 
-// out[t] = the sum over j of w[t, j] * src[rows[t, j]], one (token, chunk) a
-// thread, the loads of U choices in flight together.
-template <typename T, int V, int U, bool WEIGHTED>
-__global__ void __launch_bounds__(256)
-    gather_kernel(const T* src, int64_t lds, const int32_t* rows, const float* weights, int topk,
-                  int64_t tokens, int chunks, T* out, int64_t ldo) {
-    using Vt = Vec<T, V>;
+// out[t] = the sum over j of w[t, j] * src[rows[t, j]] (w NULL: 1), a token a
+// thread group, in fp32 and ascending j.
+template <typename T, bool ALIGNED, int U, int C, int B>
+__global__ void __launch_bounds__(256, B)
+    gather_kernel(const uint16_t* src, int64_t lds, const int32_t* rows, const float* weights, int topk,
+                  int64_t tokens, int n, uint16_t* out, int64_t ldo) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t total = tokens * topk, n = tokens * chunks;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = quotient(i, chunks), h = (i - t * chunks) * V;
-        float acc[V] = {};
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, total = tokens * topk;
+    if (t >= tokens) return;
+    uint16_t* dst = out + t * ldo;
+    const int lead = lead_of<ALIGNED>(dst);
+    const int span = blockDim.x * 8;
+    for (int h0 = threadIdx.x * 8 - lead; h0 < n; h0 += span * C) {
+        float acc[C][8] = {};
         for (int j0 = 0; j0 < topk; j0 += U) {
-            Vt v[U];
+            Chunk v[U][C];
             float w[U];
             bool use[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t s = t * topk + j0 + u;
-                const int64_t r = j0 + u < topk ? rows[s] : -1;
-                use[u] = in_range(r, total);
+                const int64_t r = j0 + u < topk ? row_at(rows, s, total) : -1;
+                use[u] = r >= 0;
                 if (use[u]) {
-                    v[u] = *reinterpret_cast<const Vt*>(src + r * lds + h);
-                    w[u] = WEIGHTED ? weights[s] : 1.f;
+                    w[u] = weights ? weights[s] : 1.f;
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (h0 + c * span < n) v[u][c] = load_chunk<ALIGNED>(src + r * lds, h0 + c * span, n);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (use[u])
 #pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        acc[k] = WEIGHTED ? fmaf(w[u], to_f(v[u].v[k]), acc[k]) : acc[k] + to_f(v[u].v[k]);
-        }
-        Vt o;
+                    for (int c = 0; c < C; ++c) {
+                        float x[8];
+                        unpack<T>(v[u][c], x);
 #pragma unroll
-        for (int k = 0; k < V; ++k) o.v[k] = from_f<T>(acc[k]);
-        *reinterpret_cast<Vt*>(out + t * ldo + h) = o;
+                        for (int i = 0; i < 8; ++i) acc[c][i] = fmaf(w[u], x[i], acc[c][i]);
+                    }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (h0 + c * span < n) store_chunk<ALIGNED>(dst, h0 + c * span, n, pack<T>(acc[c]));
     }
 }
 
-// One block a token: dys[rows[t, j]] = w[t, j] * dy[t], and dweights[t, j] =
-// dy[t] . ys[rows[t, j]], U choices at a time (dy is read again from the cache
-// for the next U).  A thread adds its chunks in ascending order, then the
-// warps' sums are added in order: fixed whatever the timing.
-template <typename T, int V, int U>
-__global__ void __launch_bounds__(256)
-    combine_grad_kernel(const T* dy, int64_t lddy, const T* ys, int64_t ldys, const int32_t* rows,
-                        const int32_t* slots, const float* weights, int topk, int64_t tokens, int chunks,
-                        T* dys, int64_t lddys, float* dweights) {
-    using Vt = Vec<T, V>;
+// dys[rows[t, j]] = w[t, j] * dy[t], and dweights[t, j] = dy[t] . ys[rows[t, j]],
+// a token a thread group, U choices at a time (dy comes from the cache for the
+// next U).  blockIdx.y takes every gridDim.y-th U.  A thread adds its chunks in
+// ascending order, then the lanes and the warps are added in a fixed order.
+template <typename T, bool ALIGNED, int U, int C, int B>
+__global__ void __launch_bounds__(256, B)
+    combine_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* ys, int64_t ldys, const int32_t* rows,
+                        const int32_t* slots, const float* weights, int topk, int64_t tokens, int n,
+                        uint16_t* dys, int64_t lddys, float* dweights) {
     __shared__ float part[U][8];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t total = tokens * topk, t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    for (int j0 = 0; j0 < topk; j0 += U) {
-        int64_t r[U];
-        float w[U], dot[U];
-        bool zero[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t s = t * topk + j0 + u;
-            const bool in = j0 + u < topk;
-            r[u] = in ? rows[s] : -1;
-            if (!in_range(r[u], total)) r[u] = -1;
-            w[u] = r[u] >= 0 ? weights[s] : 0.f;
-            zero[u] = in && slots[s] < 0;
-            dot[u] = 0.f;
-        }
-        for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-            const int64_t h = (int64_t)c * V;
-            const Vt d = *reinterpret_cast<const Vt*>(dy + t * lddy + h);
-            Vt y[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r[u] >= 0) y[u] = *reinterpret_cast<const Vt*>(ys + r[u] * ldys + h);
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, total = tokens * topk;
+    const bool in = t < tokens;
+    const int span = blockDim.x * 8;
+    const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5, warps = blockDim.x >> 5;
+    const uint16_t* d = dy + t * lddy;
+    for (int j0 = blockIdx.y * U; j0 < topk; j0 += gridDim.y * U) {
+        float dot[U] = {};
+        if (in) {
+            int64_t r[U];
+            float w[U];
+            bool zero[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (r[u] >= 0) {
-                    Vt o;
+                const int64_t s = t * topk + j0 + u;
+                r[u] = j0 + u < topk ? row_at(rows, s, total) : -1;
+                w[u] = r[u] >= 0 ? weights[s] : 0.f;
+                zero[u] = j0 + u < topk && slots[s] < 0;
+            }
+            for (int h0 = threadIdx.x * 8; h0 < n + (ALIGNED ? 0 : 7); h0 += span * C) {
+                constexpr int D = ALIGNED ? 1 : U;  // not aligned, dy is cut for each choice's row
+                Chunk dv[D][C], yv[U][C];
+                int lead[U];
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float x = to_f(d.v[k]);
-                        o.v[k] = from_f<T>(w[u] * x);
-                        dot[u] = fmaf(x, to_f(y[u].v[k]), dot[u]);
+                for (int u = 0; u < U; ++u) lead[u] = lead_of<ALIGNED>(dys + r[u] * lddys);
+                if constexpr (ALIGNED)
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (h0 + c * span < n) dv[0][c] = load_chunk<true>(d, h0 + c * span, n);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (r[u] >= 0)
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            const int h = h0 + c * span - lead[u];
+                            if (h < n) {
+                                yv[u][c] = load_chunk<ALIGNED>(ys + r[u] * ldys, h, n);
+                                if constexpr (!ALIGNED) dv[u][c] = load_chunk<false>(d, h, n);
+                            }
+                        }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const int h = h0 + c * span - lead[u];
+                        if (r[u] >= 0 && h < n) {
+                            float x[8], y[8], o[8];
+                            unpack<T>(dv[ALIGNED ? 0 : u][c], x);
+                            unpack<T>(yv[u][c], y);
+                            if (!ALIGNED && (h < 0 || h + 8 > n))
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (h + i < 0 || h + i >= n) x[i] = y[i] = 0.f;  // not of the rows
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                o[i] = w[u] * x[i];
+                                dot[u] = fmaf(x[i], y[i], dot[u]);
+                            }
+                            store_chunk<ALIGNED>(dys + r[u] * lddys, h, n, pack<T>(o));
+                        }
+                        if (zero[u]) {  // row t * topk + j is unused
+                            uint16_t* dst = dys + (t * topk + j0 + u) * lddys;
+                            const int z = h0 + c * span - lead_of<ALIGNED>(dst);
+                            if (z < n) store_chunk<ALIGNED>(dst, z, n, Chunk{});
+                        }
                     }
-                    *reinterpret_cast<Vt*>(dys + r[u] * lddys + h) = o;
-                }
-                if (zero[u]) {  // row t * topk + j is unused
-                    Vt z;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) z.v[k] = from_f<T>(0.f);
-                    *reinterpret_cast<Vt*>(dys + (t * topk + j0 + u) * lddys + h) = z;
-                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             for (int o = 16; o; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-        __syncthreads();
-        if (lane == 0)
+        if (warps > 1) {
+            __syncthreads();  // the sums of the choices before have been read
+            if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int u = 0; u < U; ++u) part[u][warp] = dot[u];
-        __syncthreads();
-        if (threadIdx.x < U && j0 + (int)threadIdx.x < topk) {
+                for (int u = 0; u < U; ++u) part[u][warp] = dot[u];
+            __syncthreads();
+        }
+        if (in && threadIdx.x < U && j0 + (int)threadIdx.x < topk) {
             float sum = 0.f;
-            for (int i = 0; i < warps; ++i) sum += part[threadIdx.x][i];
+            if (warps > 1)
+                for (int i = 0; i < warps; ++i) sum += part[threadIdx.x][threadIdx.y * warps + i];
+            else
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if ((int)threadIdx.x == u) sum = dot[u];
             dweights[t * topk + j0 + threadIdx.x] = sum;
         }
     }
 }
 
 template <typename... P, typename... A>
-gemm_status_t launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, gemm_stream_t stream,
+gemm_status_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, gemm_stream_t stream,
                      A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.dynamicSmemBytes = smem;
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)block, 1, 1);
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     // as the products: the grid may start while the kernel before it drains,
     // and waits for it before it touches global memory
@@ -357,59 +549,78 @@ bool misaligned(const void* p, size_t size) { return ((uintptr_t)p & (size - 1))
 gemm_status_t check_rows(int64_t tokens, int64_t topk, int64_t hidden, int dtype) {
     if (tokens < 0 || topk < 1 || hidden < 0 || (dtype != GEMM_F16 && dtype != GEMM_BF16))
         return GEMM_ERR_INVALID_ARG;
-    if (topk > MAX_INDEX || tokens > MAX_INDEX / topk || hidden > MAX_INDEX) return GEMM_ERR_UNSUPPORTED;
+    if (topk > MAX_TOPK || tokens > MAX_INDEX / topk || hidden > MAX_HIDDEN) return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
 }
 
-// 16 bytes an access when the rows allow it: aligned starts, leading
-// dimensions and length.
-bool wide(int64_t hidden, std::initializer_list<const void*> bases, std::initializer_list<int64_t> lds) {
+// Whether every row starts at a 16-byte boundary and holds whole chunks.
+bool aligned_rows(int64_t hidden, std::initializer_list<const void*> bases, std::initializer_list<int64_t> lds) {
     int64_t bits = hidden * 2;
     for (const void* b : bases) bits |= (int64_t)(uintptr_t)b;
     for (int64_t ld : lds) bits |= ld * 2;
     return (bits & 15) == 0;
 }
 
-// Blocks of 256 threads for n independent items; beyond 2^20 blocks the kernels
-// stride over the rest.
-int64_t blocks_for(int64_t n) { return std::min<int64_t>((n + 255) / 256, 1 << 20); }
+// Whole warps for a row, c chunks a thread, at most 256 threads (a longer row
+// takes several even rounds), and as many rows a block as fit 256 threads.
+dim3 row_block(int64_t hidden, int c) {
+    const int64_t chunks = (hidden + 7) / 8;
+    const int64_t rounds = std::max<int64_t>(1, (chunks + 256 * c - 1) / (256 * c));
+    const int64_t threads = (chunks + rounds * c - 1) / (rounds * c);
+    const unsigned width = (unsigned)std::max<int64_t>(32, (threads + 31) / 32 * 32);
+    return dim3(width, width < 256 ? 256 / width : 1, 1);
+}
 
-template <typename T, int V>
+dim3 row_grid(int64_t tokens, dim3 block, int64_t groups = 1) {
+    return dim3((unsigned)((tokens + block.y - 1) / block.y), (unsigned)groups, 1);
+}
+
+template <typename T, bool ALIGNED, int U, int C, int B>
 gemm_status_t gather_v(const void* src, int64_t lds, const int32_t* rows, const float* weights,
                        int64_t tokens, int64_t topk, int64_t hidden, void* out, int64_t ldo,
                        gemm_stream_t stream) {
-    const int chunks = (int)(hidden / V);
-    auto* fn = weights ? (topk <= 2 ? gather_kernel<T, V, 2, true> : topk <= 4 ? gather_kernel<T, V, 4, true> : gather_kernel<T, V, 8, true>)
-                       : (topk <= 2 ? gather_kernel<T, V, 2, false> : topk <= 4 ? gather_kernel<T, V, 4, false> : gather_kernel<T, V, 8, false>);
-    return launch(fn, blocks_for(tokens * chunks), 256, 0, stream, static_cast<const T*>(src), lds, rows,
-                  weights, (int)topk, tokens, chunks, static_cast<T*>(out), ldo);
+    const dim3 block = row_block(hidden, C);
+    return launch(gather_kernel<T, ALIGNED, U, C, B>, row_grid(tokens, block), block, 0, stream,
+                  static_cast<const uint16_t*>(src), lds, rows, weights, (int)topk, tokens, (int)hidden,
+                  static_cast<uint16_t*>(out), ldo);
 }
 
 template <typename T>
 gemm_status_t gather(const void* src, int64_t lds, const int32_t* rows, const float* weights,
                      int64_t tokens, int64_t topk, int64_t hidden, void* out, int64_t ldo,
                      gemm_stream_t stream) {
-    return (wide(hidden, {src, out}, {lds, ldo}) ? gather_v<T, 8> : gather_v<T, 1>)(
-        src, lds, rows, weights, tokens, topk, hidden, out, ldo, stream);
+    // (1 choice: 50 us with this, 54 with the next; 4 choices: 108.9 with this, 109.8
+    // with U = 4, and 54.2 against 57.4 on rows of 1024 with C = 1.  Not aligned,
+    // rows of 2047: 19 us, with U = 2 20.)
+    auto* fn = !aligned_rows(hidden, {src, out}, {lds, ldo}) ? gather_v<T, false, 1, 1, 4>
+               : topk == 1                                   ? gather_v<T, true, 1, 2, 6>
+               : topk == 2                                   ? gather_v<T, true, 2, 1, 4>
+                                                             : gather_v<T, true, 2, 2, 4>;
+    return fn(src, lds, rows, weights, tokens, topk, hidden, out, ldo, stream);
 }
 
-template <typename T, int V>
+template <typename T, bool ALIGNED, int U, int C, int B>
 gemm_status_t combine_grad_v(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* rows,
                              const int32_t* slots, const float* weights, int64_t tokens, int64_t topk,
                              int64_t hidden, void* dys, int64_t lddys, float* dweights, gemm_stream_t stream) {
-    const int chunks = (int)(hidden / V);
-    const int threads = (int)std::min<int64_t>(256, std::max<int64_t>(32, (chunks + 31) / 32 * 32));
-    auto* fn = topk <= 2 ? combine_grad_kernel<T, V, 2> : combine_grad_kernel<T, V, 4>;
-    return launch(fn, tokens, threads, 0, stream, static_cast<const T*>(dy), lddy, static_cast<const T*>(ys),
-                  ldys, rows, slots, weights, (int)topk, tokens, chunks, static_cast<T*>(dys), lddys, dweights);
+    const dim3 block = row_block(hidden, C);
+    // a choice a thread group when the tokens alone would not fill the device
+    const int64_t groups = tokens < 512 ? (topk + U - 1) / U : 1;
+    return launch(combine_grad_kernel<T, ALIGNED, U, C, B>, row_grid(tokens, block, groups), block, 0, stream,
+                  static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(ys), ldys, rows, slots,
+                  weights, (int)topk, tokens, (int)hidden, static_cast<uint16_t*>(dys), lddys, dweights);
 }
 
 template <typename T>
 gemm_status_t combine_grad(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* rows,
                            const int32_t* slots, const float* weights, int64_t tokens, int64_t topk,
                            int64_t hidden, void* dys, int64_t lddys, float* dweights, gemm_stream_t stream) {
-    return (wide(hidden, {dy, ys, dys}, {lddy, ldys, lddys}) ? combine_grad_v<T, 8> : combine_grad_v<T, 1>)(
-        dy, lddy, ys, ldys, rows, slots, weights, tokens, topk, hidden, dys, lddys, dweights, stream);
+    // (4 choices of 16384 tokens of 4096: 192 us with U = 4, 201 with 2; 2 choices:
+    // 107 with U = 2, 115 with C = 2 besides)
+    auto* fn = !aligned_rows(hidden, {dy, ys, dys}, {lddy, ldys, lddys}) ? combine_grad_v<T, false, 1, 2, 4>
+               : topk <= 2                                               ? combine_grad_v<T, true, 2, 1, 6>
+                                                                         : combine_grad_v<T, true, 4, 1, 4>;
+    return fn(dy, lddy, ys, ldys, rows, slots, weights, tokens, topk, hidden, dys, lddys, dweights, stream);
 }
 
 template <typename I>
@@ -419,25 +630,23 @@ gemm_status_t sort(const void* ids, int64_t ld, const SortArgs& shape, int32_t* 
     a.ld = ld;
     uint32_t* table = static_cast<uint32_t*>(workspace);
     if (a.blocks > 1) {
-        const gemm_status_t st = launch(count_kernel<I>, a.blocks, 1024, 0, stream, static_cast<const I*>(ids), a, table);
+        const gemm_status_t st = launch(count_kernel<I>, dim3(a.blocks), dim3(1024), 0, stream, static_cast<const I*>(ids), a, table);
         if (st != GEMM_OK) return st;
     }
-    // a warp handles 128 slots of a full chunk; a short one takes fewer warps
     const int threads = a.total > 1024 ? 1024 : 256;
-    if (threads == 256) a.chunk = 1024;
     const size_t smem = (size_t)threads / 32 * a.experts * sizeof(uint32_t);
     if (smem > 32 * 1024 && cudaFuncSetAttribute((const void*)place_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
-    return launch(place_kernel<I>, a.blocks, threads, smem, stream, static_cast<const I*>(ids), a, table,
+    return launch(place_kernel<I>, dim3(a.blocks), dim3(threads), smem, stream, static_cast<const I*>(ids), a, table,
                   offsets, rows, slots);
 }
 
 gemm_status_t check_sort(int64_t tokens, int64_t topk, int64_t experts) {
     if (tokens < 0 || topk < 1 || experts < 1) return GEMM_ERR_INVALID_ARG;
-    if (experts > GEMM_MOE_MAX_EXPERTS || topk > MAX_INDEX || tokens > MAX_INDEX / topk)
+    if (experts > GEMM_MOE_MAX_EXPERTS || topk > MAX_TOPK || tokens > MAX_INDEX / topk)
         return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
 }
@@ -483,12 +692,11 @@ gemm_status_t gemm_moe_dispatch(const void* x, int64_t ldx, const int32_t* rows,
     if (misaligned(x, 2) || misaligned(xs, 2) || misaligned(rows, 4) || misaligned(slots, 4))
         return GEMM_ERR_UNSUPPORTED;
     if (tokens == 0 || hidden == 0) return GEMM_OK;
-    // a copy: the type does not matter
-    const bool w = wide(hidden, {x, xs}, {ldx, ldxs});
-    const int chunks = (int)(w ? hidden / 8 : hidden);
-    return launch(w ? dispatch_kernel<__half, 8> : dispatch_kernel<__half, 1>, blocks_for(tokens * chunks), 256, 0,
-                  stream, static_cast<const __half*>(x), ldx, rows, slots, (int)topk, tokens, chunks,
-                  static_cast<__half*>(xs), ldxs);
+    const bool al = aligned_rows(hidden, {x, xs}, {ldx, ldxs});
+    const dim3 block = row_block(hidden, 4);
+    return launch(al ? dispatch_kernel<true, 4> : dispatch_kernel<false, 4>, row_grid(tokens, block), block, 0, stream,
+                  static_cast<const uint16_t*>(x), ldx, rows, slots, (int)topk, tokens, (int)hidden,
+                  static_cast<uint16_t*>(xs), ldxs);
 }
 
 gemm_status_t gemm_moe_dispatch_grad(const void* dxs, int64_t lddxs, const int32_t* rows,

@@ -34,7 +34,7 @@ SORT = dict(ids=P, id_type=1, ld=2, tokens=4, topk=2, experts=8, offsets=P, rows
 @pytest.mark.parametrize("status,changes", [
     (INV, dict(ids=None)), (INV, dict(offsets=None)), (INV, dict(rows=None)), (INV, dict(slots=None)),
     (INV, dict(id_type=2)), (INV, dict(id_type=-1)), (INV, dict(ld=1)), (INV, dict(tokens=-1)), (INV, dict(topk=0)),
-    (INV, dict(experts=0)), (UNS, dict(experts=1025)), (UNS, dict(tokens=2 ** 30)), (UNS, dict(tokens=2 ** 62)),
+    (INV, dict(experts=0)), (UNS, dict(experts=1025)), (UNS, dict(tokens=2 ** 30)), (UNS, dict(tokens=2 ** 62)), (UNS, dict(topk=65536, ld=65536)),
     (UNS, dict(ids=P + 4)), (UNS, dict(ids=P + 2, id_type=0)), (UNS, dict(offsets=P + 2)), (UNS, dict(rows=P + 1)),
     (UNS, dict(slots=P + 2))])
 def test_sort_refusals(status, changes):
@@ -78,6 +78,7 @@ def test_row_operator_refusals(name, base):
         refused(INV, fn, *_with(base, **bad))
     refused(UNS, fn, *_with(base, tokens=2 ** 31))
     refused(UNS, fn, *_with(base, tokens=2 ** 62))
+    refused(UNS, fn, *_with(base, topk=65536))
     refused(UNS, fn, *_with(base, **{"hidden": 2 ** 31, **{k: 2 ** 31 for k in base if k.startswith("ld")}}))
     fn(*_with(base, tokens=0))  # nothing to do, nothing launched
 
