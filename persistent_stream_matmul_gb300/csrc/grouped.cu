@@ -146,8 +146,17 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     const int64_t n_total = inner ? (col ? p->N : p->K) : 0;
     int ctas = p->opt_ctas;
     if (ctas == 0) {
-        if (inner) ctas = p->m_total > 128 && n_total > 128 ? 2 : 1;
-        else ctas = p->rows > 128 * p->groups && p->m_total > 128 ? 2 : 1;
+        // Pairs halve the reads of Q and P a multiplication: they win when the
+        // tensor cores bound the time and there are tiles enough for all pairs.
+        // us, one CTA against a pair: ROWS 64 groups of 2048 x 1536, 128 rows
+        // each 80.3 / 80.3, 512 rows 176 / 140; one group of 4096 x 4096, 256
+        // rows (16 pair tiles) 16.0 / 21.2, 1024 rows (64) 31.6 / 24.6; 16 groups
+        // of 512 x 512, 512 rows (64 tiles of 8 k-blocks) 9.0 / 10.5.  INNER is
+        // bound by its stores for few rows: 64 groups, 128 rows 120 / 130, 512
+        // rows 263 / 189; 8 groups of 14336 x 4096, 256 rows 346 / 318.
+        const bool wide = p->m_total > 128 && (!inner || n_total > 128);
+        const int64_t pair_tiles = inner ? INT64_MAX : cdiv(p->m_total, 256) * cdiv(p->rows, 256);
+        ctas = wide && p->rows > (inner ? 192 : 128) * p->groups && pair_tiles >= 64 ? 2 : 1;
     }
     const int tile = 128 * ctas;
     GroupedShape s{};
@@ -162,6 +171,7 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     s.tile_shift = ctas == 2 ? 8 : 7;
     s.step = 16 * ctas;
     s.band = 8;
+    s.least_share = ctas == 2 ? 24 : 20;
     s.units = p->num_sms / ctas;
     if (ctas == 2 && !p->offline) {
         const int n = resident_pairs(p->device);
@@ -175,10 +185,10 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     p->shape = s;
     p->counter_bytes = p->ws_bytes = 0;
     if (s.may_split && p->rows > 0 && p->K > 0 && p->N > 0) {
-        // fewer tiles than units are split: a counter a tile and CTA, two partial slots a CTA
+        // fewer tiles than units are split: a counter a tile and CTA, a partial slot a CTA
         const size_t slot = 128 * (size_t)tile * sizeof(float), grid = (size_t)s.units * ctas;
         p->counter_bytes = (grid * 8 + 255) / 256 * 256;
-        p->ws_bytes = p->counter_bytes + 2 * grid * slot;
+        p->ws_bytes = p->counter_bytes + grid * slot;
     }
     return GEMM_OK;
 }
@@ -299,26 +309,31 @@ gemm_status_t gemm_grouped_plan_units(gemm_grouped_plan_t p, const int32_t* offs
         (max_units > 0 && !units))
         return GEMM_ERR_INVALID_ARG;
     const GroupedShape& s = p->shape;
-    int32_t first[G_MAX_GROUPS + 1], iters[G_MAX_GROUPS + 1];
+    int32_t first[G_MAX_GROUPS + 1];
     if (offsets[0] < 0 || offsets[s.groups] > s.rows) return GEMM_ERR_INVALID_ARG;
-    first[0] = iters[0] = 0;
-    for (int g = 0; g < s.groups; ++g) {
+    for (int g = 0; g < s.groups; ++g)
         if (offsets[g + 1] < offsets[g]) return GEMM_ERR_INVALID_ARG;
-        const GroupedCounts c = grouped_counts(s, offsets[g + 1] - offsets[g]);
-        first[g + 1] = first[g] + c.tiles;
-        iters[g + 1] = iters[g] + c.iters;
-    }
-    const GroupedTables tab{offsets, first, iters};
-    GroupedCursor cur;
-    grouped_cursor_init(s, tab, (int32_t)unit, cur);
+    int32_t blocks = 0;
+    auto fill = [&](int32_t most) {
+        first[0] = 0;
+        for (int g = 0; g < s.groups; ++g) {
+            const int32_t n = offsets[g + 1] - offsets[g], kb = grouped_k_blocks(s, n);
+            if (most == 0 && s.may_split) blocks += s.inner ? grouped_tiles(s, n) * kb : 0;
+            first[g + 1] = first[g] + grouped_tiles(s, n) * grouped_shares(kb, most);
+        }
+    };
+    fill(0);
+    const int32_t tiles = first[s.groups];
+    const int32_t most = grouped_share_limit(s, tiles, s.inner ? blocks : tiles * s.kb);
+    if (most > 0) fill(most);
+    const GroupedTables tab{offsets, first};
     GroupedWork w;
     int64_t n = 0;
-    while (grouped_cursor_next(s, tab, cur, w)) {
-        if (n < max_units) {
-            const int32_t v[9] = {w.tile, w.group, w.tm, w.n0, w.valid, w.width, w.k0, w.k1, w.kb};
-            std::copy(v, v + 9, units + 9 * n);
-        }
-        ++n;
+    for (int32_t item = (int32_t)unit; item < first[s.groups]; item += s.units, ++n) {
+        if (n >= max_units) continue;
+        grouped_work(s, tab, most, item, w);
+        const int32_t v[9] = {w.item, w.group, w.tm, w.n0, w.valid, w.width, w.k0, w.k1, w.kb};
+        std::copy(v, v + 9, units + 9 * n);
     }
     *n_units = n;
     return GEMM_OK;

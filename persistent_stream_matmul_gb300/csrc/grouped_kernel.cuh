@@ -46,7 +46,8 @@
 // Split tiles (fewer tiles than units): every contributor writes its fp32
 // partial to its workspace slot and counts itself in; the one that comes last
 // adds all partials in ascending k and stores.  Nothing waits, and the sum
-// does not depend on who comes last.
+// does not depend on who comes last.  Joining costs about 3 us, the time of 16
+// k-blocks at the rate of one SM, hence the least share.
 //
 // Waits inside the CTA are bounded, as in gemm_kernel.cuh.
 #pragma once
@@ -79,8 +80,8 @@ struct GroupedCfg {
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
     static constexpr int STAGES = 6;
     static constexpr int OUT_BYTES = 32 * 256;    // one staged chunk: 32 rows x 128 columns
-    static constexpr int TABLE_BYTES = 3 * (G_MAX_GROUPS + 4) * 4;
-    static constexpr int QUEUE_BYTES = G_QUEUE * 64;
+    static constexpr int TABLE_BYTES = 2 * (G_MAX_GROUPS + 4) * 4;
+    static constexpr int QUEUE_BYTES = G_QUEUE * 48;
     static constexpr int BAR_BYTES = 320;
     static constexpr int TMEM_COLS = 2 * TILE_N;  // two accumulators
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * OUT_BYTES + TABLE_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
@@ -96,7 +97,7 @@ struct GroupedParams {
     int64_t out_group;            // INNER: elements of one output matrix
     void* out;
     const int32_t* offsets;
-    float* partials;              // two slots a CTA
+    float* partials;              // a slot a CTA
     unsigned long long* counters; // one a split tile and CTA of the pair
     uint64_t epoch;               // run number tagged into the counters, 48 bits
     int* status;
@@ -104,22 +105,42 @@ struct GroupedParams {
     uint64_t pipe_limit_ns;
 };
 
-// Count one contribution to a split tile in; true when it was the last of n.
-// The word holds (epoch << 16) | count; a word of another run counts as 0, so
-// the workspace needs no clearing, and the last arrival leaves 0, so that a
-// replay of the same launch starts afresh.
-__device__ __forceinline__ bool grouped_count_in(unsigned long long* f, uint64_t epoch, uint32_t n) {
-    uint64_t cur = (epoch << 16) | (n - 1);  // try as the last: one round trip for the one that matters
+// The counter of a split tile holds (epoch << 16) | count.  A word with another
+// epoch (of another run, or whatever the workspace held) counts as none, so the
+// workspace needs no clearing, and the last arrival leaves 0, so that a replay
+// of the same launch starts afresh.  The tile's first contributor opens the
+// counter long before anyone arrives; an arrival is then one atomic add.  (With
+// a compare-and-swap an arrival, five contributors took up to 6 us to count.)
+// An arrival that finds it unopened opens it itself.
+__device__ __forceinline__ void grouped_open_counter(unsigned long long* f, uint64_t epoch) {
+    uint64_t cur = *reinterpret_cast<volatile unsigned long long*>(f);
 #pragma unroll 1
-    for (int tries = 0; tries < (1 << 20); ++tries) {
-        const uint64_t have = (cur >> 16) == epoch ? (cur & 0xffffu) : 0;
-        const bool last = have + 1 == n;
-        const uint64_t want = last ? 0 : ((epoch << 16) | (have + 1));
-        const uint64_t prev = atom_cas_acq_rel_u64(f, cur, want);
-        if (prev == cur) return last;
+    for (int tries = 0; tries < (1 << 20) && (cur >> 16) != epoch; ++tries) {
+        const uint64_t prev = atom_cas_acq_rel_u64(f, cur, epoch << 16);
+        if (prev == cur) return;
         cur = prev;
     }
-    return false;
+}
+
+// Count one contribution in; true when it was the last of n.
+__device__ __forceinline__ bool grouped_count_in(unsigned long long* f, uint64_t epoch, uint32_t n) {
+    uint64_t have = atom_add_acq_rel_u64(f, 1);
+    if ((have >> 16) != epoch) {
+        uint64_t cur = have + 1;  // what the add left; it has not counted
+#pragma unroll 1
+        for (int tries = 0; tries < (1 << 20); ++tries) {
+            const uint64_t base = (cur >> 16) == epoch ? cur : epoch << 16;
+            const uint64_t prev = atom_cas_acq_rel_u64(f, cur, base + 1);
+            if (prev == cur) {
+                have = base;
+                break;
+            }
+            cur = prev;
+        }
+    }
+    const bool last = (have & 0xffffu) + 1 == n;
+    if (last) *reinterpret_cast<volatile unsigned long long*>(f) = 0;
+    return last;
 }
 
 template <bool OUT_BF16>
@@ -136,8 +157,9 @@ __device__ __forceinline__ uint32_t grouped_pack2(float a, float b) {
 // One warp: the scheduler's tables from the device offsets, bounded (a value
 // out of order or range becomes the nearest one in order and range).  128
 // entries at a time, four a lane, the next ones loaded ahead of the scans.
-__device__ __forceinline__ void grouped_tables(const GroupedShape& s, const int32_t* offsets, int32_t* off,
-                                               int32_t* first, int32_t* iters) {
+// Returns the k-blocks of all tiles (INNER).
+__device__ __forceinline__ int32_t grouped_tables(const GroupedShape& s, const int32_t* offsets, int32_t* off,
+                                                  int32_t* first) {
     const int lane = threadIdx.x & 31;
     int32_t v[4], next[4];
     auto load = [&](int base, int32_t (&x)[4]) {
@@ -164,40 +186,58 @@ __device__ __forceinline__ void grouped_tables(const GroupedShape& s, const int3
         int32_t prev = __shfl_up_sync(0xffffffffu, v[3], 1);
         if (lane == 0) prev = last;
         last = __shfl_sync(0xffffffffu, v[3], 31);
-        GroupedCounts c[4], sum{0, 0};
+        int32_t c[4], sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int g = base + lane * 4 + i;
             if (g > 0 && g <= s.groups) {
-                const GroupedCounts x = grouped_counts(s, v[i] - (i ? v[i - 1] : prev));
-                sum.tiles += x.tiles;
-                sum.iters += x.iters;
+                const int32_t n = v[i] - (i ? v[i - 1] : prev);
+                const int32_t x = grouped_tiles(s, n);
+                sum += x;
+                if (s.inner && s.may_split) blocks += x * grouped_k_blocks(s, n);
             }
             c[i] = sum;
         }
-        GroupedCounts run = sum;
+        int32_t run = sum;
         for (int o = 1; o < 32; o <<= 1) {
-            const int32_t a = __shfl_up_sync(0xffffffffu, run.tiles, o);
-            const int32_t b = __shfl_up_sync(0xffffffffu, run.iters, o);
-            if (lane >= o) {
-                run.tiles += a;
-                run.iters += b;
-            }
+            const int32_t a = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += a;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int g = base + lane * 4 + i;
             if (g <= s.groups) {
                 off[g] = v[i];
-                first[g] = tiles + run.tiles - sum.tiles + c[i].tiles;
-                iters[g] = blocks + run.iters - sum.iters + c[i].iters;
+                first[g] = tiles + run - sum + c[i];
             }
         }
-        tiles += __shfl_sync(0xffffffffu, run.tiles, 31);
-        blocks += __shfl_sync(0xffffffffu, run.iters, 31);
+        tiles += __shfl_sync(0xffffffffu, run, 31);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = next[i];
     }
+    for (int o = 16; o; o >>= 1) blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+    __syncwarp();
+    return blocks;
+}
+
+// One warp: `first` in shares instead of tiles.
+__device__ __forceinline__ void grouped_split_table(const GroupedShape& s, const int32_t* off, int32_t* first,
+                                                    int32_t most) {
+    const int lane = threadIdx.x & 31;
+    int32_t carry = 0;
+    for (int base = 0; base < s.groups; base += 32) {
+        const int g = base + lane;
+        const int32_t n = g < s.groups ? off[g + 1] - off[g] : 0;
+        const int32_t mine = g < s.groups ? grouped_tiles(s, n) * grouped_shares(grouped_k_blocks(s, n), most) : 0;
+        int32_t v = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (g < s.groups) first[g] = carry + v - mine;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) first[s.groups] = carry;
     __syncwarp();
 }
 
@@ -237,7 +277,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     uint8_t* tables = smem_raw + pad + STAGES * Cf::STAGE_BYTES + 2 * Cf::OUT_BYTES;
     int32_t* off = reinterpret_cast<int32_t*>(tables);
     int32_t* first = off + G_MAX_GROUPS + 4;
-    int32_t* iters = first + G_MAX_GROUPS + 4;
     const uint32_t queue = smem_addr(tables + Cf::TABLE_BYTES);
     uint8_t* bar_area = tables + Cf::TABLE_BYTES + Cf::QUEUE_BYTES;
     const uint32_t bar_base = smem_addr(bar_area);
@@ -312,7 +351,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     };
 
     GroupedWork w{};
-    int32_t split_q = 0, split_r = 0;  // the cursor's
     int qslot = 0;
     uint32_t qphase = 0;
     // The next piece of work, for a whole warp; false at the end or after a
@@ -323,8 +361,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (lane == 0) fail_pipe();
             return false;
         }
-        const uint32_t at = queue + (uint32_t)qslot * 64u;
-        const uint4 a = ld_shared_u4(at), b = ld_shared_u4(at + 16), c = ld_shared_u4(at + 32), d = ld_shared_u4(at + 48);
+        const uint32_t at = queue + (uint32_t)qslot * 48u;
+        const uint4 a = ld_shared_u4(at), b = ld_shared_u4(at + 16), c = ld_shared_u4(at + 32);
         __syncwarp();
         if (lane == 0) mbar_arrive(qempty_bar(qslot));
         if (++qslot == G_QUEUE) {
@@ -333,9 +371,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
         w = GroupedWork{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y,
                         (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
-        split_q = (int)d.x;
-        split_r = (int)d.y;
-        return w.tile >= 0;
+        return w.item >= 0;
     };
     // INNER: whether k-block kb ends inside a 16-row step
     auto ragged = [&](int kb) { return INNER && kb + 1 == w.kb && ((w.r1 - w.r0) & 15) != 0; };
@@ -352,7 +388,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const int m0 = (w.tm * Cf::CM + rank) * 128;
             const int rows_q = w.width / Cf::CM;  // this CTA's rows of Q
             const int q0 = w.n0 + rank * rows_q;
-            // ROWS: the smallest box that holds them
+            // ROWS: the smallest box that holds them (a box a bit of their number,
+            // which reads fewer rows in more copies, measured the same)
             const int box = rows_q <= 16 ? 0 : rows_q <= 32 ? 1 : rows_q <= 64 ? 2 : 3;
             const uint32_t q_bytes = INNER ? (uint32_t)Cf::Q_BYTES : (16u << box) * 128u;
             for (int kb = w.k0; kb < w.k1; ++kb) {
@@ -543,15 +580,21 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ scheduler
-        grouped_tables(p.s, p.offsets, off, first, iters);
-        const GroupedTables tab{off, first, iters};
-        GroupedCursor cur;
-        grouped_cursor_init(p.s, tab, unit, cur);
+        const int32_t blocks = grouped_tables(p.s, p.offsets, off, first);
+        const GroupedTables tab{off, first};
+        const int32_t tiles = first[p.s.groups];
+        const int32_t most = grouped_share_limit(p.s, tiles, INNER ? blocks : tiles * p.s.kb);
+        if (most > 0 && (INNER || most < p.s.kb)) grouped_split_table(p.s, off, first, most);
+        const int32_t items = first[p.s.groups];
+        int open = -1;  // the split tile whose counter this CTA opens
         bool more = true;
-        while (more) {
-            more = grouped_cursor_next(p.s, tab, cur, w);
-            if (!more) {
-                w.tile = -1;
+        for (int32_t item = unit; more; item += p.s.units) {
+            more = item < items;
+            if (more) {
+                grouped_work(p.s, tab, most, item, w);
+                if (w.shares > 1 && w.item == item) open = item;
+            } else {
+                w.item = -1;
                 w.r0 = off[p.s.groups];  // the end carries the first unused row
             }
             if (!__all_sync(0xffffffffu, mbar_wait(qempty_bar(qslot), qphase ^ 1u, p.pipe_limit_ns))) {
@@ -559,11 +602,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 break;
             }
             if (lane == 0) {
-                const uint32_t at = queue + (uint32_t)qslot * 64u;
-                st_shared_u4(at, w.tile, w.it0, w.group, w.tm);
+                const uint32_t at = queue + (uint32_t)qslot * 48u;
+                st_shared_u4(at, w.item, w.shares, w.group, w.tm);
                 st_shared_u4(at + 16, w.n0, w.width, w.valid, w.r0);
                 st_shared_u4(at + 32, w.r1, w.k0, w.k1, w.kb);
-                st_shared_u4(at + 48, cur.q, cur.r, 0, 0);
                 mbar_arrive(qfull_bar(qslot));
             }
             __syncwarp();
@@ -572,6 +614,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 qphase ^= 1u;
             }
         }
+        if (open >= 0 && lane == 0)
+            grouped_open_counter(p.counters + (size_t)open * Cf::CM + rank, p.epoch);
     } else if (warp >= G_EPI_WARP0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
@@ -613,30 +657,22 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         while (true) {
             const bool more = next_work();
             const bool empty = w.k1 <= w.k0;
-            const bool split = w.k1 - w.k0 < w.kb;
+            const bool split = w.shares > 1;
             const int buf = iter & 1;
             const int chunks = (w.valid + 31) / 32;
-            int u0 = 0, u1 = 0;  // contributors of a split tile
-            if (more && split) {
-                u0 = grouped_split_unit(split_q, split_r, w.it0);
-                u1 = grouped_split_unit(split_q, split_r, w.it0 + w.kb - 1);
-            }
             const bool got = more && (empty || (mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) &&
                                                 *abort_flag == 0));
             if (more && !got && lane == 0) fail_pipe();
             // (a warp that gives up must not leave the others at a barrier)
             if (!grouped_vote_all(got)) {
-                if (w.tile < 0) unused = w.r0;
+                if (w.item < 0) unused = w.r0;
                 break;
             }
             if (!empty) {
                 tc_fence_after_sync();
             }
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * Cf::TILE_N);
-            float4* slot = nullptr;
-            if (split)  // a unit's first share may start inside a tile, its last may end inside one
-                slot = reinterpret_cast<float4*>(p.partials +
-                                                 (size_t)(2 * blockIdx.x + (w.k0 > 0 ? 0 : 1)) * Cf::SLOT_FLOATS);
+            float4* slot = reinterpret_cast<float4*>(p.partials + (size_t)blockIdx.x * Cf::SLOT_FLOATS);
 #pragma unroll 1
             for (int c = half; c < chunks; c += 2) {
                 uint32_t r[32];
@@ -673,8 +709,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 // count, a release and acquire at GPU scope
                 barrier();
                 if (lead)
-                    *last_flag = grouped_count_in(p.counters + (size_t)w.tile * Cf::CM + rank, p.epoch,
-                                                  (uint32_t)(u1 - u0 + 1));
+                    *last_flag = grouped_count_in(p.counters + (size_t)w.item * Cf::CM + rank, p.epoch,
+                                                  (uint32_t)w.shares);
                 barrier();
                 const bool last = *last_flag != 0;
                 barrier();
@@ -686,24 +722,22 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                         // two contributors' loads are in flight together
 #pragma unroll 1
-                        for (int x = u0; x <= u1; x += 2) {
+                        for (int x = 0; x < w.shares; x += 2) {
                             float4 y[2][8];
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                if (x + h <= u1) {
-                                    // the tile's first contributor holds k-block 0: its unit's last share
+                                if (x + h < w.shares) {
+                                    // share x is item w.item + x, run by the unit of that number
                                     const float4* from =
                                         reinterpret_cast<const float4*>(
-                                            p.partials +
-                                            (size_t)(2 * ((x + h) * Cf::CM + rank) + (x + h > u0 ? 0 : 1)) *
-                                                Cf::SLOT_FLOATS) +
+                                            p.partials + (size_t)((w.item + x + h) * Cf::CM + rank) * Cf::SLOT_FLOATS) +
                                         c * 8 * 128 + et;
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) y[h][i] = ld_cg_f4(from + i * 128);
                                 }
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                if (x + h <= u1)
+                                if (x + h < w.shares)
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) {
                                         v[4 * i] += y[h][i].x;

@@ -14,8 +14,11 @@
 // groups with few rows, which are bound by memory, evenly among the others
 // changed 24006 skewed rows over 64 groups by less than 1 %.)
 //
-// Split.  With fewer tiles than units, the k-blocks of all tiles are split
-// evenly over units; a share may end inside a tile and the next begin there.
+// Split.  With fewer tiles than units, the k-blocks of a tile are cut into
+// near-equal shares, each run by a unit of its own: ceil(kb / L) of them, with
+// L k-blocks a share at most, chosen so that the shares of all tiles fit the
+// units.  A unit never has more than one share, so it never joins one tile
+// while another waits.
 #pragma once
 #include <stdint.h>
 
@@ -33,31 +36,42 @@ struct GroupedShape {
     int32_t band;          // raster: tiles along the columns side visited before the next lanes tile
     int32_t units;         // scheduling units
     int32_t may_split;     // the k-blocks of fewer than `units` tiles fit an int32
+    int32_t least_share;   // least k-blocks of a share worth joining
 };
 
-// off[0 .. groups]: bounded offsets.  Sums over the groups before g, for g =
-// 0 .. groups: tiles, and (INNER) k-blocks of the tiles.
+// off[0 .. groups]: bounded offsets.  first: sums over the groups before g, for
+// g = 0 .. groups, of their items: tiles, or shares of tiles once split.
 struct GroupedTables {
     const int32_t* off;
-    const int32_t* first;
-    const int32_t* iters;
+    int32_t* first;
 };
 
-struct GroupedCounts {
-    int32_t tiles, iters;
-};
+__host__ __device__ __forceinline__ int32_t grouped_tiles(const GroupedShape& s, int32_t n) {
+    return s.inner ? s.tiles_m * s.tiles_n : s.tiles_m * ((n + s.tile_n - 1) >> s.tile_shift);
+}
 
-__host__ __device__ __forceinline__ GroupedCounts grouped_counts(const GroupedShape& s, int32_t n) {
-    GroupedCounts c;
-    c.tiles = s.inner ? s.tiles_m * s.tiles_n : s.tiles_m * ((n + s.tile_n - 1) >> s.tile_shift);
-    c.iters = s.inner && s.may_split ? c.tiles * ((n + 63) / 64) : 0;
-    return c;
+__host__ __device__ __forceinline__ int32_t grouped_k_blocks(const GroupedShape& s, int32_t n) {
+    return s.inner ? (n + 63) / 64 : s.kb;
+}
+
+// Shares of a tile of kb k-blocks, at most `most` each (0: not split).
+__host__ __device__ __forceinline__ int32_t grouped_shares(int32_t kb, int32_t most) {
+    return most == 0 || kb <= most ? 1 : (kb + most - 1) / most;
+}
+
+// The k-blocks of a share at most, for all tiles and the k-blocks of all tiles
+// (0: no split).  sum over tiles of ceil(kb / L) <= total / L + tiles, so this L
+// keeps the shares within the units.
+__host__ __device__ __forceinline__ int32_t grouped_share_limit(const GroupedShape& s, int32_t tiles, int32_t total) {
+    if (!s.may_split || tiles == 0 || tiles >= s.units) return 0;
+    const int32_t l = (total + s.units - tiles - 1) / (s.units - tiles);
+    return l > s.least_share ? l : s.least_share;
 }
 
 // A unit of work: k-blocks [k0, k1) of the kb of one tile.
 struct GroupedWork {
-    int32_t tile;
-    int32_t it0;      // its first k-block among all split ones
+    int32_t item;     // of the tile's first share; the others follow
+    int32_t shares;
     int32_t group, tm;
     int32_t n0;       // first row of the tile: of A (ROWS), of the output matrix (INNER)
     int32_t width;    // columns of the accumulator
@@ -65,45 +79,6 @@ struct GroupedWork {
     int32_t r0, r1;   // the group's rows
     int32_t k0, k1, kb;
 };
-
-struct GroupedCursor {
-    int32_t tiles;
-    bool split;
-    int32_t q, r;                // split k-blocks a unit: q, one more for the first r
-    int32_t it, it_end;          // this unit's split k-blocks
-    int32_t next_tile;
-};
-
-__host__ __device__ __forceinline__ void grouped_cursor_init(const GroupedShape& s, const GroupedTables& t,
-                                                             int32_t unit, GroupedCursor& c) {
-    c.tiles = t.first[s.groups];
-    c.split = s.may_split && c.tiles < s.units;
-    c.q = c.r = c.it = c.it_end = 0;
-    c.next_tile = c.split && !s.inner ? c.tiles : unit;
-    if (c.split && c.tiles > 0) {
-        // A share costs its k-blocks, and the contributor that joins a tile
-        // reads every share's partial, worth about 4 k-blocks of the widest
-        // tile: the joined time is least near sqrt(k-blocks) / 2 shares a
-        // tile.  Narrow tiles, bound by the reads of the matrix, bear twice that.
-        const int32_t total = s.inner ? t.iters[s.groups] : c.tiles * s.kb;
-        const int32_t mean = s.inner ? total / c.tiles : s.kb;
-        int32_t shares = 1;
-        while (shares < 32 && (shares + 1) * (shares + 1) <= (s.step == 16 ? mean : mean / 4)) ++shares;
-        const int32_t n = c.tiles * shares < s.units ? c.tiles * shares : s.units;
-        c.q = total / n;
-        c.r = total - c.q * n;
-        if (unit < n) {
-            c.it = unit * c.q + (unit < c.r ? unit : c.r);
-            c.it_end = c.it + c.q + (unit < c.r ? 1 : 0);
-        }
-    }
-}
-
-// The unit that runs split k-block `it`, for a cursor's q and r.
-__host__ __device__ __forceinline__ int32_t grouped_split_unit(int32_t q, int32_t r, int32_t it) {
-    const int32_t big = r * (q + 1);
-    return it < big ? it / (q + 1) : r + (it - big) / q;
-}
 
 // The group g with sum[g] <= x < sum[g + 1].
 __host__ __device__ __forceinline__ int32_t grouped_search(int32_t groups, int32_t x, const int32_t* sum) {
@@ -127,44 +102,25 @@ __host__ __device__ __forceinline__ int32_t grouped_search(int32_t groups, int32
 #endif
 }
 
-__host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape& s, const GroupedTables& t,
-                                                             GroupedCursor& c, GroupedWork& w) {
-    int32_t g, local;  // group, and tile within it
-    while (true) {
-        w.k0 = 0;
-        w.k1 = -1;
-        if (c.it < c.it_end) {
-            w.k1 = c.it_end - c.it;  // an upper bound, from k0
-            if (s.inner) {
-                g = grouped_search(s.groups, c.it, t.iters);
-                const int32_t kb = (t.off[g + 1] - t.off[g] + 63) / 64;
-                local = (c.it - t.iters[g]) / kb;
-                w.it0 = t.iters[g] + local * kb;
-                w.tile = t.first[g] + local;
-            } else {
-                w.tile = c.it / s.kb;
-                w.it0 = w.tile * s.kb;
-                g = grouped_search(s.groups, w.tile, t.first);
-                local = w.tile - t.first[g];
-            }
-            w.k0 = c.it - w.it0;
-        } else if (c.next_tile < c.tiles) {
-            w.tile = c.next_tile;
-            c.next_tile += s.units;
-            w.it0 = 0;
-            g = grouped_search(s.groups, w.tile, t.first);
-            local = w.tile - t.first[g];
-            // INNER: a split leaves the tiles of empty groups to be cleared
-            if (c.split && t.off[g + 1] > t.off[g]) continue;
-        } else {
-            return false;
-        }
-        break;
-    }
+// Work item `item`, for shares of at most `most` k-blocks.
+__host__ __device__ __forceinline__ void grouped_work(const GroupedShape& s, const GroupedTables& t, int32_t most,
+                                                      int32_t item, GroupedWork& w) {
+    const int32_t g = grouped_search(s.groups, item, t.first);
     w.group = g;
     w.r0 = t.off[g];
     w.r1 = t.off[g + 1];
     const int32_t n = w.r1 - w.r0;
+    w.kb = grouped_k_blocks(s, n);
+    w.shares = grouped_shares(w.kb, most);
+    int32_t local = item - t.first[g], share = 0;
+    if (w.shares > 1) {
+        const int32_t tile = local / w.shares;
+        share = local - tile * w.shares;
+        local = tile;
+    }
+    w.item = item - share;
+    w.k0 = w.shares > 1 ? (int32_t)((int64_t)w.kb * share / w.shares) : 0;
+    w.k1 = w.shares > 1 ? (int32_t)((int64_t)w.kb * (share + 1) / w.shares) : w.kb;
     const int32_t side = s.inner ? s.tiles_n : (n + s.tile_n - 1) >> s.tile_shift;
     // bands of `band` tiles along the columns side, the lanes side slow within
     // one; without the divisions that the common shapes do not need
@@ -181,17 +137,11 @@ __host__ __device__ __forceinline__ bool grouped_cursor_next(const GroupedShape&
         w.width = s.tile_n;
         w.n0 = tn * s.tile_n;
         w.valid = s.n_total - w.n0 < s.tile_n ? s.n_total - w.n0 : s.tile_n;
-        w.kb = (n + 63) / 64;
     } else {
         w.width = ((side == 1 ? n : (n + side - 1) / side) + s.step - 1) & ~(s.step - 1);
         w.n0 = w.r0 + tn * w.width;
         w.valid = w.r1 - w.n0 < w.width ? w.r1 - w.n0 : w.width;
-        w.kb = s.kb;
     }
-    if (w.k1 < 0 || w.k0 + w.k1 > w.kb) w.k1 = w.kb;
-    else w.k1 += w.k0;
-    if (c.it < c.it_end) c.it += w.k1 - w.k0;
-    return true;
 }
 
 }  // namespace psm

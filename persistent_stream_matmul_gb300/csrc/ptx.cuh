@@ -466,6 +466,12 @@ __device__ __forceinline__ uint64_t atom_cas_acq_rel_u64(unsigned long long* p, 
     return old;
 }
 
+__device__ __forceinline__ uint64_t atom_add_acq_rel_u64(unsigned long long* p, uint64_t val) {
+    uint64_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(val) : "memory");
+    return old;
+}
+
 __device__ __forceinline__ float4 ld_cg_f4(const float4* p) {
     float4 v;
     asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"

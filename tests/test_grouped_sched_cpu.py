@@ -43,7 +43,11 @@ def test_units_cover_every_tile_once(counts, N, K, kind, sms, ctas):
             assert 0 < valid <= width <= side and width % (16 * ctas) == 0 and 0 <= tm * lanes < m_total
             if not inner:
                 assert offsets[g] <= n0 and n0 + valid <= offsets[g + 1]
-    assert sorted(tiles) == list(range(len(tiles)))
+    # tiles are numbered by their shares, without a gap
+    assert sorted(t + i for t, sh in tiles.items() for i in range(len(sh))) == \
+        list(range(sum(len(sh) for sh in tiles.values())))
+    if len(tiles) < p.info("units"):
+        assert sum(len(sh) for sh in tiles.values()) <= p.info("units")
     covered = set()
     for shares in tiles.values():
         shares.sort()
@@ -64,22 +68,27 @@ def test_units_cover_every_tile_once(counts, N, K, kind, sms, ctas):
     p.close()
 
 
-def test_shares_are_even_and_at_least_the_minimum():
-    """Eight single rows over 12 column tiles of 32 k-blocks: split evenly over
-    all SMs."""
-    p = _plan(B.GEMM_GROUPED_ROWS, 64, 8, 1536, 2048)
-    assert p.info("ctas") == 1 and p.info("units") == 152
-    offsets = np.minimum(np.arange(65), 8)
-    loads = [sum(k1 - k0 for *_, k0, k1, _ in p.units(offsets, u)) for u in range(152)]
-    assert sum(loads) == 96 * 32 and max(loads) - min(loads) <= 1
-    p.close()
+def test_shares_are_even_and_worth_joining():
+    """Twelve column tiles of 128 k-blocks over 152 SMs: seven shares of at most
+    twenty each, a unit each; with 32 k-blocks two; with 16 none."""
+    for K, shares in ((8192, 7), (2048, 2), (1024, 1)):
+        p = _plan(B.GEMM_GROUPED_ROWS, 64, 8, 1536, K)
+        assert p.info("ctas") == 1 and p.info("units") == 152
+        offsets = np.minimum(np.arange(65), 1)
+        loads = [[k1 - k0 for *_, k0, k1, _ in p.units(offsets, u)] for u in range(152)]
+        loads = [x for x in loads if x]
+        assert all(len(x) == 1 for x in loads) and len(loads) == 12 * shares
+        assert sum(x[0] for x in loads) == 12 * K // 64 and max(loads)[0] - min(loads)[0] <= 1
+        p.close()
 
 
 def test_summed_rows_are_split_when_tiles_are_few():
-    """One 256 x 256 gradient over 16384 rows: eight shares of 32 k-blocks."""
+    """One 256 x 256 gradient over 16384 rows: eleven shares of 23 or 24
+    k-blocks."""
     p = _plan(B.GEMM_GROUPED_INNER, 1, 16384, 256, 256)
     loads = [sum(k1 - k0 for *_, k0, k1, _ in p.units([0, 16384], u)) for u in range(p.info("units"))]
-    assert sorted(loads)[-8:] == [32] * 8 and sum(loads) == 256 and p.workspace_size > 0
+    loads = [x for x in loads if x]
+    assert len(loads) == 11 and set(loads) <= {23, 24} and sum(loads) == 256 and p.workspace_size > 0
     p.close()
 
 
@@ -87,7 +96,10 @@ def test_variant_rule_and_info():
     assert _plan(0, 8, 1024, 4096, 4096).info("ctas") == 1
     assert _plan(0, 8, 1025, 4096, 4096).info("ctas") == 2
     assert _plan(0, 1, 4096, 128, 4096).info("ctas") == 1
+    assert _plan(0, 1, 4096, 512, 4096).info("ctas") == 1  # 32 tiles for 76 pairs
+    assert _plan(0, 1, 8192, 512, 4096).info("ctas") == 2
     assert _plan(1, 8, 4096, 256, 4096).info("ctas") == 2
+    assert _plan(1, 8, 1536, 256, 4096).info("ctas") == 1
     assert _plan(1, 8, 4096, 128, 4096).info("ctas") == 1
     p = _plan(0, 8, 4096, 4096, 4096)
     assert (p.info("tile_m"), p.info("tile_n"), p.info("units")) == (256, 256, 76)
