@@ -146,17 +146,18 @@ gemm_status_t derive(gemm_grouped_plan* p) {
     const int64_t n_total = inner ? (col ? p->N : p->K) : 0;
     int ctas = p->opt_ctas;
     if (ctas == 0) {
-        // Pairs halve the reads of Q and P a multiplication: they win when the
-        // tensor cores bound the time and there are tiles enough for all pairs.
-        // us, one CTA against a pair: ROWS 64 groups of 2048 x 1536, 128 rows
-        // each 80.3 / 80.3, 512 rows 176 / 140; one group of 4096 x 4096, 256
-        // rows (16 pair tiles) 16.0 / 21.2, 1024 rows (64) 31.6 / 24.6; 16 groups
-        // of 512 x 512, 512 rows (64 tiles of 8 k-blocks) 9.0 / 10.5.  INNER is
-        // bound by its stores for few rows: 64 groups, 128 rows 120 / 130, 512
-        // rows 263 / 189; 8 groups of 14336 x 4096, 256 rows 346 / 318.
+        // Pairs halve the reads of Q and P a multiplication and store longer runs:
+        // they win when there are rows enough for the tensor cores (INNER: always)
+        // and tiles for all pairs.  us, one CTA against a pair: ROWS 64 groups of
+        // 2048 x 1536, 128 rows each 79.4 / 78.6, 512 rows 178 / 138; one group of
+        // 4096 x 4096, 256 rows (16 pair tiles) 16.4 / 21.2, 1024 rows (64) 32.2 /
+        // 24.6; 16 groups of 512 x 512, 512 rows (64 tiles of 8 k-blocks) 9.0 / 9.5.
+        // INNER 64 groups of 2048 x 1536, 32 rows 103 / 83, 512 rows 210 / 141; 16
+        // groups of 512 x 512 (64 pair tiles), 32 rows 6.6 / 7.4.
         const bool wide = p->m_total > 128 && (!inner || n_total > 128);
-        const int64_t pair_tiles = inner ? INT64_MAX : cdiv(p->m_total, 256) * cdiv(p->rows, 256);
-        ctas = wide && p->rows > (inner ? 192 : 128) * p->groups && pair_tiles >= 64 ? 2 : 1;
+        const int64_t pair_tiles = cdiv(p->m_total, 256) * (inner ? p->groups * cdiv(n_total, 256) : cdiv(p->rows, 256));
+        const bool enough = inner ? 2 * pair_tiles > p->num_sms : p->rows > 128 * p->groups && pair_tiles >= 64;
+        ctas = wide && enough ? 2 : 1;
     }
     const int tile = 128 * ctas;
     GroupedShape s{};

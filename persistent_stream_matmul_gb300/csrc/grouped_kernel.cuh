@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)st);
+                    if (lane == 0) mbar_arrive_cluster_fenced(ready0 + 8u * (uint32_t)st);
                 }
                 stage = (stage + w.k1 - w.k0) % STAGES;
             }
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
+                    if constexpr (PAIR) mbar_arrive_cluster_fenced(mapa_shared(tempty_bar(buf), 0));
                     else mbar_arrive(tempty_bar(buf));
                 }
                 ++iter;

@@ -98,8 +98,8 @@ def test_variant_rule_and_info():
     assert _plan(0, 1, 4096, 128, 4096).info("ctas") == 1
     assert _plan(0, 1, 4096, 512, 4096).info("ctas") == 1  # 32 tiles for 76 pairs
     assert _plan(0, 1, 8192, 512, 4096).info("ctas") == 2
-    assert _plan(1, 8, 4096, 256, 4096).info("ctas") == 2
-    assert _plan(1, 8, 1536, 256, 4096).info("ctas") == 1
+    assert _plan(1, 8, 40, 256, 4096).info("ctas") == 2
+    assert _plan(1, 4, 4096, 256, 4096).info("ctas") == 1  # 64 tiles for 76 pairs
     assert _plan(1, 8, 4096, 128, 4096).info("ctas") == 1
     p = _plan(0, 8, 4096, 4096, 4096)
     assert (p.info("tile_m"), p.info("tile_n"), p.info("units")) == (256, 256, 76)
