@@ -85,7 +85,7 @@ def test_shares_are_even_and_worth_joining():
 def test_summed_rows_are_split_when_tiles_are_few():
     """One 256 x 256 gradient over 16384 rows: eleven shares of 23 or 24
     k-blocks."""
-    p = _plan(B.GEMM_GROUPED_INNER, 1, 16384, 256, 256)
+    p = _plan(B.GEMM_GROUPED_INNER, 1, 16384, 256, 256, ctas=2)
     loads = [sum(k1 - k0 for *_, k0, k1, _ in p.units([0, 16384], u)) for u in range(p.info("units"))]
     loads = [x for x in loads if x]
     assert len(loads) == 11 and set(loads) <= {23, 24} and sum(loads) == 256 and p.workspace_size > 0
