@@ -371,7 +371,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void*
 
     // The maps are encoded for every run: they cost well under a microsecond
     // of host time, and nothing is kept by an operand's address.
-    CUtensorMap tmP;
+    CUtensorMap tmP, tmC;
     GroupedQMaps tmQ;
     bool ok;
     if (inner) {
@@ -386,6 +386,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void*
         for (int i = 0; i < 4; ++i)
             ok = ok && encode(&tmQ.m[i], p->dtype, A, 2, p->K, p->rows, 1, G_BK, 16u << i);
     }
+    ok = ok && encode(&tmC, p->dtype, C, 3, p->m_total, inner ? p->shape.n_total : p->rows, inner ? p->groups : 1, 64, 32);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
 
     GroupedParams kp{};
@@ -424,7 +425,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void*
     ++na;
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    void* args[3] = {&tmP, &tmQ, &kp};
+    void* args[4] = {&tmP, &tmQ, &tmC, &kp};
     if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;

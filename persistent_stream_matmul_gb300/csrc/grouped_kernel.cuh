@@ -35,13 +35,16 @@
 //              in every role, its copies of the code were fetched cold before
 //              the first load, and the epilogue paid it between tiles.
 //   warps 4-11 epilogue, two halves that take the 32-row chunks of a tile in
-//              turn: accumulator fragments, packed to 16 bits, transposed
-//              through shared memory into rows of 256 bytes, stored 16 bytes a
-//              lane.  One half alone took 730 cycles a chunk, its latencies
-//              end to end, and bound the gradient of small groups.  (Tensor copies of 64-byte rows, a warp by itself, wrote
-//              128 matrices of 2048 x 1536 in 281 us against 233: short
-//              segments cost write bandwidth, which on this device is 4.0 TB/s
-//              for a plain fill.)
+//              turn (one half alone takes 730 cycles a chunk, its latencies end
+//              to end): accumulator fragments, packed to 16 bits, transposed
+//              into shared memory as two 128-byte-swizzled boxes of 32 rows x 64
+//              columns.  Tiles of G_BOX_BLOCKS k-blocks or more are written by
+//              tensor copies, the others, and the rows before a group's end
+//              inside a box, by the lanes, 256 bytes a row.  us, lanes against
+//              copies: 16384 rows of 14336 x 4096 1187 / 1178 and their gradient
+//              1151 / 1125, where the copies leave the tensor cores more of
+//              shared memory; gradients of 64 matrices over 512 rows each (8
+//              k-blocks) 143 / 140, over 128 rows 90 / 105, where stores bound.
 //
 // Split tiles (fewer tiles than units): every contributor writes its fp32
 // partial to its workspace slot and counts itself in; the one that comes last
@@ -65,6 +68,7 @@ constexpr int G_EPI_WARP0 = 4;
 constexpr int G_EPI_THREADS = 256;
 constexpr int G_MAX_GROUPS = 1024;
 constexpr int G_QUEUE = 4;
+constexpr int G_BOX_BLOCKS = 8;
 constexpr uint32_t G_CHUNK = 64 * 128;  // one 64 x 64 MN-major box
 enum : uint32_t { G_BAR_EPI = 1, G_BAR_VOTE = 2, G_BAR_HALF = 3 };  // G_BAR_HALF + half
 enum : int { G_STATUS_PIPE_TIMEOUT = 2 };
@@ -263,7 +267,7 @@ struct GroupedQMaps {
 template <bool PAIR, bool INNER, bool P_MN, bool OUT_BF16>
 __global__ void __launch_bounds__(G_THREADS, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ GroupedQMaps tmQ,
-                   const __grid_constant__ GroupedParams p) {
+                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GroupedParams p) {
     using Cf = GroupedCfg<PAIR>;
     static_assert(!INNER || P_MN, "INNER reads both operands MN-major");
     constexpr int STAGES = Cf::STAGES;
@@ -629,22 +633,34 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int read_row = et >> 4, read_unit = et & 15;
         // rows 32c .. 32c + 31 of the tile, from fragments, to the output
         auto store_chunk = [&](const float (&v)[32], int c) {
+            if (et == 0) bulk_wait_group_read_0();  // this thread issues the half's copies
             named_bar_sync(G_BAR_HALF + half, 128);  // the last chunk has been read
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = j * 8 + (lane & 7);
-                const int u = (q * 4 + (lane >> 3)) ^ (row & 7);
-                stmatrix_x4_trans(stage_base + row * 256 + u * 16, grouped_pack2<OUT_BF16>(v[8 * j], v[8 * j + 1]),
+                const int u = ((q & 1) * 4 + (lane >> 3)) ^ (row & 7);
+                stmatrix_x4_trans(stage_base + (q >> 1) * 4096 + row * 128 + u * 16, grouped_pack2<OUT_BF16>(v[8 * j], v[8 * j + 1]),
                                   grouped_pack2<OUT_BF16>(v[8 * j + 2], v[8 * j + 3]),
                                   grouped_pack2<OUT_BF16>(v[8 * j + 4], v[8 * j + 5]),
                                   grouped_pack2<OUT_BF16>(v[8 * j + 6], v[8 * j + 7]));
             }
+            const int col0 = (w.tm * Cf::CM + rank) * 128;
+            const bool box = w.kb >= G_BOX_BLOCKS && (INNER || 32 * c + 32 <= w.valid);
+            if (box) fence_proxy_async_smem();
             named_bar_sync(G_BAR_HALF + half, 128);
+            if (box) {
+                if (et == 0) {
+                    if (col0 < p.m_total) tma_store_3d(&tmC, stage_base, col0, w.n0 + 32 * c, INNER ? w.group : 0);
+                    if (col0 + 64 < p.m_total) tma_store_3d(&tmC, stage_base + 4096, col0 + 64, w.n0 + 32 * c, INNER ? w.group : 0);
+                    bulk_commit_group();
+                }
+                return;
+            }
             uint4 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[i] = ld_shared_u4(stage_base + (read_row + 8 * i) * 256 + ((read_unit ^ read_row) * 16));
-            const int col = (w.tm * Cf::CM + rank) * 128 + read_unit * 8, row = 32 * c + read_row;
+                x[i] = ld_shared_u4(stage_base + (read_unit >> 3) * 4096 + (read_row + 8 * i) * 128 + (((read_unit & 7) ^ read_row) * 16));
+            const int col = col0 + read_unit * 8, row = 32 * c + read_row;
             uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) +
                            2 * ((INNER ? (int64_t)w.group * p.out_group : 0) +
                                 (int64_t)(w.n0 + row) * p.m_total + col);
@@ -751,6 +767,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 }
             }
         }
+        if (et == 0) bulk_wait_group_0();  // the copies are complete before the CTA ends
         if constexpr (!INNER) {
             // the unused rows: +0, 16 bytes a thread
             const int64_t begin = (int64_t)unused * p.m_total / 8, end = (int64_t)p.s.rows * p.m_total / 8;
