@@ -33,7 +33,8 @@ struct GroupedShape {
     int32_t kb;            // ROWS: k-blocks of 64 a tile
     int32_t tile_n, step;  // tile_n: 1 << tile_shift; step a power of two
     int32_t tile_shift;
-    int32_t band;          // raster: tiles along the columns side visited before the next lanes tile
+    int32_t band;          // raster: about how many tiles along the columns side are visited before
+                           // the next lanes tile
     int32_t units;         // scheduling units
     int32_t may_split;     // the k-blocks of fewer than `units` tiles fit an int32
     int32_t least_share;   // least k-blocks of a share worth joining
@@ -122,14 +123,17 @@ __host__ __device__ __forceinline__ void grouped_work(const GroupedShape& s, con
     w.k0 = w.shares > 1 ? (int32_t)((int64_t)w.kb * share / w.shares) : 0;
     w.k1 = w.shares > 1 ? (int32_t)((int64_t)w.kb * (share + 1) / w.shares) : w.kb;
     const int32_t side = s.inner ? s.tiles_n : (n + s.tile_n - 1) >> s.tile_shift;
-    // bands of `band` tiles along the columns side, the lanes side slow within
-    // one; without the divisions that the common shapes do not need
+    // bands of about `band` tiles along the columns side, even ones (with eight
+    // and a rest of one, nine tiles of rows read the matrix twice), the lanes
+    // side slow within one
     int32_t first_tn = 0, wide = side;
-    if (side > s.band) {
-        const int32_t b = local / (s.band * s.tiles_m);
-        local -= b * s.band * s.tiles_m;
-        first_tn = b * s.band;
-        wide = side - first_tn < s.band ? side - first_tn : s.band;
+    const int32_t bands = (side + s.band / 2 - 1) / s.band;
+    if (bands > 1) {
+        const int32_t most_wide = (side + bands - 1) / bands;
+        const int32_t b = local / (most_wide * s.tiles_m);
+        local -= b * most_wide * s.tiles_m;
+        first_tn = b * most_wide;
+        wide = side - first_tn < most_wide ? side - first_tn : most_wide;
     }
     w.tm = wide == 1 ? local : local / wide;
     const int32_t tn = first_tn + local - w.tm * wide;
