@@ -27,7 +27,8 @@
  *    operator that writes rows writes them as +0.
  *  - Row matrices have a leading dimension in elements (ldx and so on), at
  *    least the row length.  Any alignment of the 16-bit element is accepted;
- *    16-byte aligned rows are faster.  Offsets, rows, slots and the weights are
+ *    16-byte aligned rows are faster (of others, the whole aligned 16-byte
+ *    words that hold an element of the row are read).  Offsets, rows, slots and the weights are
  *    contiguous.
  *  - Sums are in fp32, in ascending choice order, rounded once; results do
  *    not depend on timing (no floating-point atomics).

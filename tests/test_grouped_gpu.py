@@ -108,6 +108,76 @@ def test_products_of_groups(counts, unused, N, K, ctas, kind, dtype, layout):
     assert torch.equal(got, exact.to(got.dtype))
 
 
+# few tiles over a long sum, so that every tile is split: (kind, sizes, unused, N, K)
+SPLITS = [
+    (0, [1], 0, 64, 8192), (0, [3, 0, 40], 2, 136, 6000), (0, [200], 0, 512, 16384), (0, [0, 300, 0], 0, 264, 4104),
+    (0, [16, 1, 16], 0, 8, 20000), (0, [257], 1, 256, 4096), (1, [5000], 3, 264, 136), (1, [4000, 0, 700, 1], 0, 128, 256),
+    (1, [16385], 0, 8, 8), (1, [0, 3000, 0], 0, 520, 72), (1, [9999, 5, 2501], 10, 64, 512),
+]
+
+
+@pytest.mark.parametrize("layout", [COL, ROW])
+@pytest.mark.parametrize("ctas", [1, 2])
+@pytest.mark.parametrize("kind,counts,unused,N,K", SPLITS)
+def test_split_tiles(kind, counts, unused, N, K, ctas, layout):
+    """Partials of several units joined by whoever comes last: within the bound,
+    the same bits on every run, whatever the workspace held."""
+    R = sum(counts) + unused
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    with B.GroupedPlan(kind, len(counts), R, N, K, B.GEMM_BF16, layout, ctas=ctas) as p:
+        work = [w for u in range(p.info("units")) for w in p.units(offsets, u)]
+        assert any(k1 - k0 < kb for *_, k0, k1, kb in work)  # the case splits
+    A, Bm = _operands(kind, counts, R, N, K, "bf16", layout, 23)
+    exact, absolute = _reference(kind, counts, R, N, K, layout, A, Bm)
+    first = None
+    for _ in range(4):
+        got = _run(kind, counts, unused, N, K, "bf16", layout, A, Bm, ctas=ctas)
+        assert_rounded_sum(got, exact, absolute, K if kind == 0 else max(counts))
+        first = got if first is None else first
+        assert torch.equal(got.view(torch.int16), first.view(torch.int16))
+    A, Bm = _operands(kind, counts, R, N, K, "f16", layout, 24, integers=True)
+    exact, _ = _reference(kind, counts, R, N, K, layout, A, Bm)
+    assert torch.equal(_run(kind, counts, unused, N, K, "f16", layout, A, Bm, ctas=ctas), exact.half())
+
+
+@pytest.mark.parametrize("ctas", [1, 2])
+@pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
+def test_split_tiles_replay_and_share_a_workspace(kind, ctas):
+    """A captured launch keeps its run number: replays, other plans' runs in the
+    same workspace between them, and sizes that change which tiles split all
+    give the bits of a fresh run."""
+    E, R, N, K = 3, 9000, 72, 8192 if kind == B.GEMM_GROUPED_ROWS else 136
+    code, dt = DTYPES["bf16"]
+    sizes = ([2, 0, 5], [700, 8300, 0], [0, 0, 0], [9000, 0, 0], [1, 1, 1])
+    A = normal((R, K), dt, 1)
+    Bm = normal((E, N, K) if kind == B.GEMM_GROUPED_ROWS else (R, N), dt, 2, 0.25)
+    plans = [B.GroupedPlan(kind, E, R, N, K, code, COL, ctas=ctas) for _ in range(2)]
+    ws = torch.randint(0, 256, (plans[0].workspace_size,), dtype=torch.uint8, device="cuda")
+    C = torch.empty((R, N) if kind == B.GEMM_GROUPED_ROWS else (E, N, K), dtype=dt, device="cuda")
+    offs = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plans[0].run(A, Bm, C, offs, ws, torch.cuda.current_stream())
+    for counts in sizes:
+        fresh, _ = _sizes(counts)
+        offs.copy_(fresh)
+        want = torch.empty_like(C)
+        plans[1].run(A, Bm, want, offs, torch.zeros_like(ws), torch.cuda.current_stream())
+        for _ in range(3):
+            C.fill_(7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(C.view(torch.int16), want.view(torch.int16))
+            C.fill_(7)
+            plans[1].run(A, Bm, C, offs, ws, torch.cuda.current_stream())
+            torch.cuda.synchronize()
+            assert torch.equal(C.view(torch.int16), want.view(torch.int16))
+        assert all(p.last_status() == B.GEMM_OK for p in plans)
+    for p in plans:
+        p.close()
+
+
 @pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
 def test_many_groups(kind, ctas):
