@@ -241,10 +241,12 @@ struct alignas(16) Chunk {
 };
 
 // STREAM: read once; else the neighbouring thread's chunk shares the word.
+// (Plain loads, not the read-only path: the grid may have started before the
+// kernel that wrote the rows ended.)
 template <bool STREAM>
 __device__ __forceinline__ Chunk load_word(const void* p) {
     const uint4* q = static_cast<const uint4*>(p);
-    const uint4 x = STREAM ? __ldcs(q) : __ldg(q);
+    const uint4 x = STREAM ? __ldcs(q) : *q;
     return Chunk{{x.x, x.y, x.z, x.w}};
 }
 
