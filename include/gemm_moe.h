@@ -175,7 +175,8 @@ gemm_status_t gemm_grouped_plan_get_info(gemm_grouped_plan_t plan, int key, int6
 /*
  * Host twin of the device scheduler: the work of scheduling unit `unit` for
  * the HOST offsets given (groups + 1, ascending, at most rows), in order, 9
- * int32 each: tile (numbered by its first share), group, tile along C's contiguous dimension, first row of
+ * int32 each: tile (a split one as -1 - the unit of its first share), group,
+ * tile along C's contiguous dimension, first row of
  * the tile (of C for ROWS, of the group's matrix along its other dimension
  * for INNER), rows stored, accumulator width, first and end k-block of 64,
  * and the tile's k-blocks.  Writes at most max_units and the full count to

@@ -324,16 +324,14 @@ gemm_status_t gemm_grouped_plan_units(gemm_grouped_plan_t p, const int32_t* offs
         }
     };
     fill(0);
-    const int32_t tiles = first[s.groups];
-    const int32_t most = grouped_share_limit(s, tiles, s.inner ? blocks : tiles * s.kb);
-    if (most > 0) fill(most);
+    const GroupedSplit split = grouped_split(s, first[s.groups], blocks);
+    if (s.inner && split.most > 0) fill(split.most);
     const GroupedTables tab{offsets, first};
     GroupedWork w;
     int64_t n = 0;
-    for (int32_t item = (int32_t)unit; item < first[s.groups]; item += s.units, ++n) {
+    for (; grouped_work(s, tab, split, (int32_t)unit, (int32_t)n, first[s.groups], w); ++n) {
         if (n >= max_units) continue;
-        grouped_work(s, tab, most, item, w);
-        const int32_t v[9] = {w.item, w.group, w.tm, w.n0, w.valid, w.width, w.k0, w.k1, w.kb};
+        const int32_t v[9] = {w.shares > 1 ? -1 - w.item : w.item, w.group, w.tm, w.n0, w.valid, w.width, w.k0, w.k1, w.kb};
         std::copy(v, v + 9, units + 9 * n);
     }
     *n_units = n;

@@ -46,11 +46,11 @@
 //              shared memory; gradients of 64 matrices over 512 rows each (8
 //              k-blocks) 143 / 140, over 128 rows 90 / 105, where stores bound.
 //
-// Split tiles (fewer tiles than units): every contributor writes its fp32
-// partial to its workspace slot and counts itself in; the one that comes last
-// adds all partials in ascending k and stores.  Nothing waits, and the sum
-// does not depend on who comes last.  Joining costs about 3 us, the time of 16
-// k-blocks at the rate of one SM, hence the least share.
+// Split tiles (grouped_sched.cuh): every contributor writes its fp32 partial to
+// its workspace slot and counts itself in; the one that comes last adds all
+// partials in ascending k and stores.  Nothing waits, and the sum does not
+// depend on who comes last.  Joining costs about 3 us, the time of 16 k-blocks
+// at the rate of one SM, hence the least share.
 //
 // Waits inside the CTA are bounded, as in gemm_kernel.cuh.
 #pragma once
@@ -587,16 +587,15 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int32_t blocks = grouped_tables(p.s, p.offsets, off, first);
         const GroupedTables tab{off, first};
         const int32_t tiles = first[p.s.groups];
-        const int32_t most = grouped_share_limit(p.s, tiles, INNER ? blocks : tiles * p.s.kb);
-        if (most > 0 && (INNER || most < p.s.kb)) grouped_split_table(p.s, off, first, most);
+        const GroupedSplit split = grouped_split(p.s, tiles, blocks);
+        if (INNER && split.most > 0) grouped_split_table(p.s, off, first, split.most);
         const int32_t items = first[p.s.groups];
         int open = -1;  // the split tile whose counter this CTA opens
         bool more = true;
-        for (int32_t item = unit; more; item += p.s.units) {
-            more = item < items;
+        for (int32_t step = 0; more; ++step) {
+            more = grouped_work(p.s, tab, split, unit, step, items, w);
             if (more) {
-                grouped_work(p.s, tab, most, item, w);
-                if (w.shares > 1 && w.item == item) open = item;
+                if (w.shares > 1 && w.item == unit) open = unit;
             } else {
                 w.item = -1;
                 w.r0 = off[p.s.groups];  // the end carries the first unused row
@@ -743,7 +742,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
                                 if (x + h < w.shares) {
-                                    // share x is item w.item + x, run by the unit of that number
+                                    // share x was run by unit w.item + x
                                     const float4* from =
                                         reinterpret_cast<const float4*>(
                                             p.partials + (size_t)((w.item + x + h) * Cf::CM + rank) * Cf::SLOT_FLOATS) +

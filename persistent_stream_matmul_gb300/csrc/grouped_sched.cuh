@@ -14,11 +14,17 @@
 // groups with few rows, which are bound by memory, evenly among the others
 // changed 24006 skewed rows over 64 groups by less than 1 %.)
 //
-// Split.  With fewer tiles than units, the k-blocks of a tile are cut into
-// near-equal shares, each run by a unit of its own: ceil(kb / L) of them, with
-// L k-blocks a share at most, chosen so that the shares of all tiles fit the
-// units.  A unit never has more than one share, so it never joins one tile
-// while another waits.
+// Split.  Tiles that do not fill a round of the units (all of them when there
+// are fewer than units, else, for ROWS, the remainder) run first, the k-blocks
+// of each cut into near-equal shares, each share run by a unit of its own:
+// ceil(kb / L) of them, with L k-blocks a share at most, chosen so that the
+// shares fit the units.  A unit never has more than one share, so it never
+// joins one tile while another waits; what it has after it are whole tiles,
+// which hide the joining.  us with the remainder whole against split: 79 / 55
+// (2 groups, 4096 rows of 8192, 85 tiles for 76 pairs), 59 / 46 (13 groups,
+// 1482 rows of 5952 x 1424), 43.6 / 34.5 (one group, 1024 rows of 4096 x 5120),
+// 68.5 / 65.9 (64 groups of 2048 x 1536), the same where the shares would be
+// too short.
 #pragma once
 #include <stdint.h>
 
@@ -41,7 +47,7 @@ struct GroupedShape {
 };
 
 // off[0 .. groups]: bounded offsets.  first: sums over the groups before g, for
-// g = 0 .. groups, of their items: tiles, or shares of tiles once split.
+// g = 0 .. groups, of their items: tiles, or for a split INNER shares of tiles.
 struct GroupedTables {
     const int32_t* off;
     int32_t* first;
@@ -60,18 +66,29 @@ __host__ __device__ __forceinline__ int32_t grouped_shares(int32_t kb, int32_t m
     return most == 0 || kb <= most ? 1 : (kb + most - 1) / most;
 }
 
-// The k-blocks of a share at most, for all tiles and the k-blocks of all tiles
-// (0: no split).  sum over tiles of ceil(kb / L) <= total / L + tiles, so this L
-// keeps the shares within the units.
-__host__ __device__ __forceinline__ int32_t grouped_share_limit(const GroupedShape& s, int32_t tiles, int32_t total) {
-    if (!s.may_split || tiles == 0 || tiles >= s.units) return 0;
-    const int32_t l = (total + s.units - tiles - 1) / (s.units - tiles);
-    return l > s.least_share ? l : s.least_share;
+struct GroupedSplit {
+    int32_t tiles;   // the first tiles are split
+    int32_t most;    // k-blocks of a share at most; 0: no split
+    int32_t shares;  // ROWS: shares of each
+};
+
+// For all tiles and (INNER) their k-blocks.  The sum over the split tiles of
+// ceil(kb / L) is at most total / L + tiles, so this L keeps it within the units.
+__host__ __device__ __forceinline__ GroupedSplit grouped_split(const GroupedShape& s, int32_t tiles, int32_t blocks) {
+    GroupedSplit p{0, 0, 1};
+    const int32_t rest = tiles < s.units ? tiles : (s.inner ? 0 : tiles % s.units);
+    if (!s.may_split || rest == 0) return p;
+    const int32_t total = s.inner ? blocks : rest * s.kb;
+    const int32_t l = (total + s.units - rest - 1) / (s.units - rest);
+    const int32_t most = l > s.least_share ? l : s.least_share;
+    const int32_t shares = s.inner ? 1 : grouped_shares(s.kb, most);
+    if (s.inner || shares > 1) p = GroupedSplit{rest, most, shares};
+    return p;
 }
 
 // A unit of work: k-blocks [k0, k1) of the kb of one tile.
 struct GroupedWork {
-    int32_t item;     // of the tile's first share; the others follow
+    int32_t item;     // split: the unit of the first share, the others' follow; else the tile
     int32_t shares;
     int32_t group, tm;
     int32_t n0;       // first row of the tile: of A (ROWS), of the output matrix (INNER)
@@ -103,23 +120,45 @@ __host__ __device__ __forceinline__ int32_t grouped_search(int32_t groups, int32
 #endif
 }
 
-// Work item `item`, for shares of at most `most` k-blocks.
-__host__ __device__ __forceinline__ void grouped_work(const GroupedShape& s, const GroupedTables& t, int32_t most,
-                                                      int32_t item, GroupedWork& w) {
-    const int32_t g = grouped_search(s.groups, item, t.first);
+// The unit's work number `step`; false past its last.  `items`: first[groups].
+__host__ __device__ __forceinline__ bool grouped_work(const GroupedShape& s, const GroupedTables& t,
+                                                      const GroupedSplit& p, int32_t unit, int32_t step,
+                                                      int32_t items, GroupedWork& w) {
+    int32_t at;          // the tile, or for INNER the share
+    int32_t share = 0;
+    w.shares = 1;
+    if (!s.inner && p.most > 0) {
+        const bool has = unit < p.tiles * p.shares;
+        if (has && step == 0) {
+            at = unit / p.shares;
+            share = unit - at * p.shares;
+            w.shares = p.shares;
+        } else {
+            at = p.tiles + unit + (step - has) * s.units;
+        }
+    } else {
+        at = unit + step * s.units;
+    }
+    if (at >= items) return false;
+    const int32_t g = grouped_search(s.groups, at, t.first);
     w.group = g;
     w.r0 = t.off[g];
     w.r1 = t.off[g + 1];
     const int32_t n = w.r1 - w.r0;
     w.kb = grouped_k_blocks(s, n);
-    w.shares = grouped_shares(w.kb, most);
-    int32_t local = item - t.first[g], share = 0;
-    if (w.shares > 1) {
-        const int32_t tile = local / w.shares;
-        share = local - tile * w.shares;
-        local = tile;
+    int32_t local = at - t.first[g];
+    w.item = at;
+    if (s.inner && p.most > 0) {
+        w.shares = grouped_shares(w.kb, p.most);
+        if (w.shares > 1) {
+            const int32_t tile = local / w.shares;
+            share = local - tile * w.shares;
+            local = tile;
+        }
+        w.item = at - share;
+    } else if (w.shares > 1) {
+        w.item = unit - share;
     }
-    w.item = item - share;
     w.k0 = w.shares > 1 ? (int32_t)((int64_t)w.kb * share / w.shares) : 0;
     w.k1 = w.shares > 1 ? (int32_t)((int64_t)w.kb * (share + 1) / w.shares) : w.kb;
     const int32_t side = s.inner ? s.tiles_n : (n + s.tile_n - 1) >> s.tile_shift;
@@ -146,6 +185,7 @@ __host__ __device__ __forceinline__ void grouped_work(const GroupedShape& s, con
         w.n0 = w.r0 + tn * w.width;
         w.valid = w.r1 - w.n0 < w.width ? w.r1 - w.n0 : w.width;
     }
+    return true;
 }
 
 }  // namespace psm

@@ -140,6 +140,22 @@ def test_split_tiles(kind, counts, unused, N, K, ctas, layout):
     assert torch.equal(_run(kind, counts, unused, N, K, "f16", layout, A, Bm, ctas=ctas), exact.half())
 
 
+@pytest.mark.parametrize("ctas,counts,N,K", [(1, [128 * 100, 128 * 55], 128, 2048), (2, [256 * 60, 0, 256 * 18], 256, 4096),
+                                             (1, [20, 19900, 7], 64, 4104), (2, [19968, 300], 200, 3080)])
+def test_a_remainder_of_tiles_is_split(ctas, counts, N, K):
+    """Tiles that are left over a whole round of the units run in shares before
+    the whole ones."""
+    R = sum(counts)
+    with B.GroupedPlan(0, len(counts), R, N, K, B.GEMM_F16, COL, ctas=ctas) as p:
+        work = [p.units(np.concatenate([[0], np.cumsum(counts)]), u) for u in range(p.info("units"))]
+        assert any(w[0][7] - w[0][6] < w[0][8] for w in work) and all(w[-1][8] == w[-1][7] for w in work)
+    A, Bm = _operands(0, counts, R, N, K, "f16", COL, 31)
+    exact, absolute = _reference(0, counts, R, N, K, COL, A, Bm)
+    got = _run(0, counts, 0, N, K, "f16", COL, A, Bm, ctas=ctas)
+    assert_rounded_sum(got, exact, absolute, K)
+    assert torch.equal(got.view(torch.int16), _run(0, counts, 0, N, K, "f16", COL, A, Bm, ctas=ctas).view(torch.int16))
+
+
 @pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
 def test_split_tiles_replay_and_share_a_workspace(kind, ctas):

@@ -43,11 +43,10 @@ def test_units_cover_every_tile_once(counts, N, K, kind, sms, ctas):
             assert 0 < valid <= width <= side and width % (16 * ctas) == 0 and 0 <= tm * lanes < m_total
             if not inner:
                 assert offsets[g] <= n0 and n0 + valid <= offsets[g + 1]
-    # tiles are numbered by their shares, without a gap
-    assert sorted(t + i for t, sh in tiles.items() for i in range(len(sh))) == \
-        list(range(sum(len(sh) for sh in tiles.values())))
-    if len(tiles) < p.info("units"):
-        assert sum(len(sh) for sh in tiles.values()) <= p.info("units")
+    split = [t for t in tiles if t < 0]
+    units = sorted(-1 - t + i for t in split for i in range(len(tiles[t])))
+    assert len(set(units)) == len(units) and (not units or units[-1] < p.info("units"))  # one share a unit
+    assert all(len(tiles[t]) == 1 for t in tiles if t >= 0)
     covered = set()
     for shares in tiles.values():
         shares.sort()
@@ -80,6 +79,18 @@ def test_shares_are_even_and_worth_joining():
         assert all(len(x) == 1 for x in loads) and len(loads) == 12 * shares
         assert sum(x[0] for x in loads) == 12 * K // 64 and max(loads)[0] - min(loads)[0] <= 1
         p.close()
+
+
+def test_a_remainder_of_tiles_is_split_first():
+    """155 tiles of 64 k-blocks over 152 units: three tiles run first, in four
+    shares each, then every unit has one whole tile."""
+    p = _plan(B.GEMM_GROUPED_ROWS, 2, 128 * 155, 128, 4096, ctas=1)
+    offsets = [0, 128 * 100, 128 * 155]
+    work = [p.units(offsets, u) for u in range(152)]
+    assert [len(x) for x in work] == [2] * 12 + [1] * 140
+    assert all(w[0][7] - w[0][6] == 16 and w[0][0] == -1 - u // 4 * 4 for u, w in enumerate(work[:12]))
+    assert all(w[-1][6:] == (0, 64, 64) for w in work)
+    p.close()
 
 
 def test_summed_rows_are_split_when_tiles_are_few():
