@@ -33,7 +33,10 @@ template <> __device__ __forceinline__ __half from_f<__half>(float v) { return _
 // block of place_kernel sums the table itself, so there is no third launch
 // and no block waits for another.  The counts are whole numbers, so the order
 // of the atomics in shared memory changes nothing.
-constexpr int SORT_SINGLE = 4096;  // up to this many slots one block does it all
+// Up to this many slots one block does it all: us against two launches, 1024
+// slots of 64 experts 3.6 / 4.6, 4096 of 256 8.0 / 7.8 (and the second launch's
+// cost on the host), 8192 of 64 11.2 / 7.6.
+constexpr int SORT_SINGLE = 4096;
 // Else slots a block: 2048 while there are at most 64 blocks, then 4096 until
 // there are SORT_BLOCKS, then an even part.  Every block reads all blocks'
 // counts: 32768 slots of 64 experts take 7.9 us with 2048 and 9.7 with 4096,
@@ -609,8 +612,10 @@ gemm_status_t combine_grad_v(const void* dy, int64_t lddy, const void* ys, int64
                              const int32_t* slots, const float* weights, int64_t tokens, int64_t topk,
                              int64_t hidden, void* dys, int64_t lddys, float* dweights, gemm_stream_t stream) {
     const dim3 block = row_block(hidden, C);
-    // a choice a thread group when the tokens alone would not fill the device
-    const int64_t groups = tokens < 512 ? (topk + U - 1) / U : 1;
+    // U choices a thread group when the tokens alone would not fill the device
+    // (us, one group after another against each its own block: 8 choices of 4096,
+    // 16 tokens 5.6 / 3.5, 256 6.9 / 6.1, 1024 23.7 / 23.3)
+    const int64_t groups = tokens <= 1024 ? (topk + U - 1) / U : 1;
     return launch(combine_grad_kernel<T, ALIGNED, U, C, B>, row_grid(tokens, block, groups), block, 0, stream,
                   static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(ys), ldys, rows, slots,
                   weights, (int)topk, tokens, (int)hidden, static_cast<uint16_t*>(dys), lddys, dweights);
