@@ -77,7 +77,7 @@ struct GroupedSplit {
 __host__ __device__ __forceinline__ GroupedSplit grouped_split(const GroupedShape& s, int32_t tiles, int32_t blocks) {
     GroupedSplit p{0, 0, 1};
     const int32_t rest = tiles < s.units ? tiles : (s.inner ? 0 : tiles % s.units);
-    if (!s.may_split || rest == 0) return p;
+    if (!s.may_split || rest == 0 || (!s.inner && s.kb <= s.least_share)) return p;
     const int32_t total = s.inner ? blocks : rest * s.kb;
     const int32_t l = (total + s.units - rest - 1) / (s.units - rest);
     const int32_t most = l > s.least_share ? l : s.least_share;
@@ -166,8 +166,8 @@ __host__ __device__ __forceinline__ bool grouped_work(const GroupedShape& s, con
     // and a rest of one, nine tiles of rows read the matrix twice), the lanes
     // side slow within one
     int32_t first_tn = 0, wide = side;
-    const int32_t bands = (side + s.band / 2 - 1) / s.band;
-    if (bands > 1) {
+    if (2 * side > 3 * s.band) {
+        const int32_t bands = (side + s.band / 2 - 1) / s.band;
         const int32_t most_wide = (side + bands - 1) / bands;
         const int32_t b = local / (most_wide * s.tiles_m);
         local -= b * most_wide * s.tiles_m;
