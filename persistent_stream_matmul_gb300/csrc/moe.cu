@@ -232,7 +232,8 @@ SortArgs sort_shape(int64_t tokens, int64_t topk, int64_t experts) {
 // flight an SM, so U and C are weighed against the registers that B allows:
 // the sum of 2 choices of 16384 tokens of 4096 takes 68 us with U, C, B = 2, 1, 4
 // (5.9 TB/s), 71 with 2, 2, 4, 84 with 4, 1, 4 and 115 with 2, 2, 6, whose
-// registers spill; the streaming stores below take each 4 to 5 us less.
+// registers spill (before the streaming stores below, with which the first
+// takes 63).
 //
 // ALIGNED: every row starts at a 16-byte boundary and its length is a multiple
 // of 8.  Otherwise the chunks are cut at the 16-byte boundaries of the row
