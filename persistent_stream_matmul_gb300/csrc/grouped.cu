@@ -391,7 +391,6 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void*
 
     GroupedParams kp{};
     kp.s = p->shape;
-    kp.K = (int32_t)p->K;
     kp.m_total = (int32_t)p->m_total;
     kp.out_group = p->N * p->K;
     kp.out = C;

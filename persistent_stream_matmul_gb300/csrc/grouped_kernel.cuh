@@ -76,9 +76,7 @@ enum : int { G_STATUS_PIPE_TIMEOUT = 2 };
 template <bool PAIR>
 struct GroupedCfg {
     static constexpr int CM = PAIR ? 2 : 1;
-    static constexpr int TILE_M = 128 * CM;
     static constexpr int TILE_N = 128 * CM;
-    static constexpr int STEP = 16 * CM;          // granularity of the instruction's N
     static constexpr int P_BYTES = 128 * G_BK * 2;
     static constexpr int Q_BYTES = 128 * G_BK * 2;  // this CTA's rows of Q
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
@@ -96,7 +94,6 @@ struct GroupedCfg {
 
 struct GroupedParams {
     GroupedShape s;
-    int32_t K;                    // ROWS: summed extent
     int32_t m_total;              // extent of the output's contiguous dimension
     int64_t out_group;            // INNER: elements of one output matrix
     void* out;
@@ -590,13 +587,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const GroupedSplit split = grouped_split(p.s, tiles, blocks);
         if (INNER && split.most > 0) grouped_split_table(p.s, off, first, split.most);
         const int32_t items = first[p.s.groups];
-        int open = -1;  // the split tile whose counter this CTA opens
         bool more = true;
         for (int32_t step = 0; more; ++step) {
             more = grouped_work(p.s, tab, split, unit, step, items, w);
-            if (more) {
-                if (w.shares > 1 && w.item == unit) open = unit;
-            } else {
+            if (!more) {
                 w.item = -1;
                 w.r0 = off[p.s.groups];  // the end carries the first unused row
             }
@@ -610,6 +604,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 st_shared_u4(at + 16, w.n0, w.width, w.valid, w.r0);
                 st_shared_u4(at + 32, w.r1, w.k0, w.k1, w.kb);
                 mbar_arrive(qfull_bar(qslot));
+                if (more && w.shares > 1 && w.item == unit)  // this unit has the first share
+                    grouped_open_counter(p.counters + (size_t)unit * Cf::CM + rank, p.epoch);
             }
             __syncwarp();
             if (++qslot == G_QUEUE) {
@@ -617,8 +613,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 qphase ^= 1u;
             }
         }
-        if (open >= 0 && lane == 0)
-            grouped_open_counter(p.counters + (size_t)open * Cf::CM + rank, p.epoch);
     } else if (warp >= G_EPI_WARP0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
