@@ -632,9 +632,11 @@ template <typename T>
 gemm_status_t combine_grad(const void* dy, int64_t lddy, const void* ys, int64_t ldys, const int32_t* rows,
                            const int32_t* slots, const float* weights, int64_t tokens, int64_t topk,
                            int64_t hidden, void* dys, int64_t lddys, float* dweights, gemm_stream_t stream) {
-    // (4 choices of 16384 tokens of 4096: 192 us with U = 4, 201 with 2; 2 choices:
-    // 107 with U = 2, 115 with C = 2 besides)
+    // us with U, C, B = 4, 1, 4 (2, 1, 6 for 2 choices) against 2, 2, 4: 4 choices
+    // of 4096 184 / 186 and 2 of them 98 / 107, but 6 of 4096 146 / 138, 8 of 2048
+    // 96 / 92, 6 of 1080 76 / 70, 4 of 512 25.4 / 22.1, 2 of 1024 26.6 / 24.0
     auto* fn = !aligned_rows(hidden, {dy, ys, dys}, {lddy, ldys, lddys}) ? combine_grad_v<T, false, 1, 2, 4>
+               : topk > 4 || hidden < 2048                               ? combine_grad_v<T, true, 2, 2, 4>
                : topk <= 2                                               ? combine_grad_v<T, true, 2, 1, 6>
                                                                          : combine_grad_v<T, true, 4, 1, 4>;
     return fn(dy, lddy, ys, ldys, rows, slots, weights, tokens, topk, hidden, dys, lddys, dweights, stream);
