@@ -194,7 +194,9 @@ gemm_status_t gemm_grouped_workspace_size(gemm_grouped_plan_t plan, size_t *byte
  * Run the products on `stream`, asynchronously.  offsets: groups + 1 device
  * int32, ascending, at most `rows` (gemm_moe_sort writes such); a value out of
  * order or range is taken as the nearest one in order and range, so no
- * access leaves the operands.  C is written in full.
+ * access leaves the operands.  The rows before offsets[0] (offsets + e of a
+ * longer array runs the groups from e on) and from offsets[groups] on are
+ * unused.  C is written in full.
  * Errors: INVALID_ARG (NULL plan, or a NULL operand that is not empty),
  * UNSUPPORTED (alignment), WORKSPACE (NULL or not 16-byte aligned while one is
  * needed), NO_DEVICE (offline plan), CUDA, LAUNCH.

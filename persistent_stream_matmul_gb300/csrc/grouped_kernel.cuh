@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             more = grouped_work(p.s, tab, split, unit, step, items, w);
             if (!more) {
                 w.item = -1;
-                w.r0 = off[p.s.groups];  // the end carries the first unused row
+                w.r0 = off[0];  // the end carries the rows that belong to a group
+                w.r1 = off[p.s.groups];
             }
             if (!__all_sync(0xffffffffu, mbar_wait(qempty_bar(qslot), qphase ^ 1u, p.pipe_limit_ns))) {
                 if (lane == 0) fail_pipe();
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int et = (threadIdx.x - G_EPI_WARP0 * 32) & 127;  // thread of its half
         const bool lead = threadIdx.x == G_EPI_WARP0 * 32;
         uint32_t iter = 0;
-        int32_t unused = p.s.rows;  // first unused row, from the end of the queue
+        int32_t used0 = 0, used1 = p.s.rows;  // the rows of the groups, from the end of the queue
         auto barrier = [&]() { named_bar_sync(G_BAR_EPI, G_EPI_THREADS); };
         const uint32_t stage_base = out_stage + half * Cf::OUT_BYTES;
         const int read_row = et >> 4, read_unit = et & 15;
@@ -674,7 +675,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (more && !got && lane == 0) fail_pipe();
             // (a warp that gives up must not leave the others at a barrier)
             if (!grouped_vote_all(got)) {
-                if (w.item < 0) unused = w.r0;
+                if (w.item < 0) {
+                    used0 = w.r0;
+                    used1 = w.r1;
+                }
                 break;
             }
             if (!empty) {
@@ -762,11 +766,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
         if (et == 0) bulk_wait_group_0();  // the copies are complete before the CTA ends
         if constexpr (!INNER) {
-            // the unused rows: +0, 16 bytes a thread
-            const int64_t begin = (int64_t)unused * p.m_total / 8, end = (int64_t)p.s.rows * p.m_total / 8;
-            for (int64_t i = begin + (int64_t)blockIdx.x * G_EPI_THREADS + (threadIdx.x - G_EPI_WARP0 * 32); i < end;
+            // the unused rows, before the first group and after the last: +0, 16 bytes a thread
+            const int64_t head = (int64_t)used0 * p.m_total / 8, used = (int64_t)(used1 - used0) * p.m_total / 8;
+            const int64_t end = (int64_t)p.s.rows * p.m_total / 8 - used;
+            for (int64_t i = (int64_t)blockIdx.x * G_EPI_THREADS + (threadIdx.x - G_EPI_WARP0 * 32); i < end;
                  i += (int64_t)gridDim.x * G_EPI_THREADS)
-                st_u4(reinterpret_cast<uint8_t*>(p.out) + i * 16, 0, 0, 0, 0);
+                st_u4(reinterpret_cast<uint8_t*>(p.out) + (i < head ? i : i + used) * 16, 0, 0, 0, 0);
         }
     }
 

@@ -1,0 +1,49 @@
+"""GPU tests of the mixture-of-experts operators at their edges."""
+import numpy as np
+import pytest
+import torch
+
+from persistent_stream_matmul_gb300 import _binding as B
+from tests.gpu_util import ensure_built
+from tests.moe_util import DTYPES, Rows, assert_rounded_sum, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+@pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
+@pytest.mark.parametrize("ctas", [1, 2])
+@pytest.mark.parametrize("first,counts,unused,N,K", [(11, [9, 13], 7, 64, 128), (1, [0, 0], 5, 72, 200), (300, [40], 0, 520, 2304),
+                                                     (5000, [0, 700, 3], 300, 264, 64), (17, [0], 0, 8, 8)])
+def test_offsets_that_start_inside_the_rows(first, counts, unused, N, K, ctas, kind):
+    """The rows before the first group are unused: +0 in ROWS, and whatever
+    they hold, in no sum."""
+    code, dt = DTYPES["bf16"]
+    R, G, rows = first + sum(counts) + unused, len(counts), kind == B.GEMM_GROUPED_ROWS
+    offsets = first + np.concatenate([[0], np.cumsum(counts)])
+    A, Bm = normal((R, K), dt, 1), normal((G, K, N) if rows else (R, N), dt, 2, 0.25)
+    for used in ([A] if rows else [A, Bm]):
+        used[:first] = float("nan")
+        used[first + sum(counts):] = float("nan")
+    C = Rows(R if rows else G * K, N, dt, offset=64)
+    with B.GroupedPlan(kind, G, R, N, K, code, B.GEMM_ROW_MAJOR, ctas=ctas) as p:
+        ws = torch.empty(max(1, p.workspace_size), dtype=torch.uint8, device="cuda")
+        p.run(A, Bm, C, torch.tensor(offsets, dtype=torch.int32, device="cuda"), ws)
+        assert p.last_status() == B.GEMM_OK
+    C.check_guards()
+    exact = torch.zeros(C.view.shape, dtype=torch.float64, device="cuda")
+    absolute = torch.zeros_like(exact)
+    for g, n in enumerate(counts):
+        at = slice(offsets[g], offsets[g + 1])
+        a, b = A[at].double(), (Bm[g] if rows else Bm[at]).double()
+        out = at if rows else slice(g * K, (g + 1) * K)
+        a = a if rows else a.t()
+        exact[out], absolute[out] = a @ b, a.abs() @ b.abs()
+    assert_rounded_sum(C.view, exact, absolute, K if rows else max(1, max(counts)))
+    if rows:
+        unused_rows = torch.cat([C.view[:first], C.view[first + sum(counts):]])
+        assert not bool(unused_rows.view(torch.int16).any())  # +0
