@@ -568,8 +568,11 @@ gemm_status_t check_rows(int64_t tokens, int64_t topk, int64_t hidden, int dtype
     return GEMM_OK;
 }
 
-// Whether every row starts at a 16-byte boundary and holds whole chunks.
+// Whether every row starts at a 16-byte boundary and holds whole chunks.  Rows
+// without elements do, wherever they are: the aligned kernels then touch no
+// row, while the others cut a first chunk at the written row's boundary.
 bool aligned_rows(int64_t hidden, std::initializer_list<const void*> bases, std::initializer_list<int64_t> lds) {
+    if (hidden == 0) return true;
     int64_t bits = hidden * 2;
     for (const void* b : bases) bits |= (int64_t)(uintptr_t)b;
     for (int64_t ld : lds) bits |= ld * 2;

@@ -47,3 +47,23 @@ def test_offsets_that_start_inside_the_rows(first, counts, unused, N, K, ctas, k
     if rows:
         unused_rows = torch.cat([C.view[:first], C.view[first + sum(counts):]])
         assert not bool(unused_rows.view(torch.int16).any())  # +0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,k,ld", [(1, 1, 0), (5, 2, 1), (40, 3, 3), (1500, 2, 1), (300, 9, 8)])
+def test_gradient_of_combine_without_elements(T, k, ld, dtype):
+    """hidden == 0: no row has an element to read, at NULL or at any address;
+    the weights' gradients are empty sums."""
+    code, dt = DTYPES[dtype]
+    rows = torch.arange(T * k, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    rows[::3] = -1
+    slots = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    w = torch.rand(T * k, device="cuda")
+    few = Rows(1, 8, dt, offset=1)  # a row of no elements may start off a boundary
+    for p in (None, few):
+        dw = Rows(1, T * k, torch.float32)
+        B.gemm_moe_combine_grad(p, ld, p, ld, rows, slots, w, T, k, 0, code, p, ld, dw)
+        torch.cuda.synchronize()
+        assert not bool(dw.view.view(torch.int32).any())  # +0
+        dw.check_guards()
+    assert bool((few.buf == 77).all())
