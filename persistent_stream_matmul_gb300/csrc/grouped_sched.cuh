@@ -79,7 +79,7 @@ __host__ __device__ __forceinline__ GroupedSplit grouped_split(const GroupedShap
     const int32_t rest = tiles < s.units ? tiles : (s.inner ? 0 : tiles % s.units);
     if (!s.may_split || rest == 0 || (!s.inner && s.kb <= s.least_share)) return p;
     const int32_t total = s.inner ? blocks : rest * s.kb;
-    const int32_t l = (total + s.units - rest - 1) / (s.units - rest);
+    const int32_t l = (int32_t)(((uint32_t)total + (uint32_t)(s.units - rest) - 1u) / (uint32_t)(s.units - rest));
     const int32_t most = l > s.least_share ? l : s.least_share;
     const int32_t shares = s.inner ? 1 : grouped_shares(s.kb, most);
     if (s.inner || shares > 1) p = GroupedSplit{rest, most, shares};
@@ -124,22 +124,23 @@ __host__ __device__ __forceinline__ int32_t grouped_search(int32_t groups, int32
 __host__ __device__ __forceinline__ bool grouped_work(const GroupedShape& s, const GroupedTables& t,
                                                       const GroupedSplit& p, int32_t unit, int32_t step,
                                                       int32_t items, GroupedWork& w) {
-    int32_t at;          // the tile, or for INNER the share
+    uint32_t next;       // the tile, or for INNER the share; below 2^32, as the one before is below 2^31
     int32_t share = 0;
     w.shares = 1;
     if (!s.inner && p.most > 0) {
         const bool has = unit < p.tiles * p.shares;
         if (has && step == 0) {
-            at = unit / p.shares;
-            share = unit - at * p.shares;
+            next = (uint32_t)(unit / p.shares);
+            share = unit - (int32_t)next * p.shares;
             w.shares = p.shares;
         } else {
-            at = p.tiles + unit + (step - has) * s.units;
+            next = (uint32_t)p.tiles + (uint32_t)unit + (uint32_t)(step - has) * (uint32_t)s.units;
         }
     } else {
-        at = unit + step * s.units;
+        next = (uint32_t)unit + (uint32_t)step * (uint32_t)s.units;
     }
-    if (at >= items) return false;
+    if (next >= (uint32_t)items) return false;
+    const int32_t at = (int32_t)next;
     const int32_t g = grouped_search(s.groups, at, t.first);
     w.group = g;
     w.r0 = t.off[g];
@@ -181,7 +182,8 @@ __host__ __device__ __forceinline__ bool grouped_work(const GroupedShape& s, con
         w.n0 = tn * s.tile_n;
         w.valid = s.n_total - w.n0 < s.tile_n ? s.n_total - w.n0 : s.tile_n;
     } else {
-        w.width = ((side == 1 ? n : (n + side - 1) / side) + s.step - 1) & ~(s.step - 1);
+        // the even part, rounded up (n > 0; n + side - 1 may pass 2^31)
+        w.width = ((side == 1 ? n : (n - 1) / side + 1) + s.step - 1) & ~(s.step - 1);
         w.n0 = w.r0 + tn * w.width;
         w.valid = w.r1 - w.n0 < w.width ? w.r1 - w.n0 : w.width;
     }

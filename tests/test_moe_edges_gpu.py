@@ -67,3 +67,28 @@ def test_gradient_of_combine_without_elements(T, k, ld, dtype):
         assert not bool(dw.view.view(torch.int32).any())  # +0
         dw.check_guards()
     assert bool((few.buf == 77).all())
+
+
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_rows_up_to_the_largest_index(ctas):
+    """One group of 2 140 000 000 rows and the rest in another: every row of C,
+    whole numbers, so exactly."""
+    R, N, K = 2 ** 31 - 1024, 8, 8
+    dt, step = torch.bfloat16, 2 ** 25
+    A = torch.empty((R, K), dtype=dt, device="cuda")  # 34 GB, and as much for C
+    for at in range(0, R, step):
+        part = A[at:at + step].view(torch.int16)
+        torch.randint(0, 16, part.shape, out=part, dtype=torch.int16, device="cuda")
+        A[at:at + step] = part.to(dt) - 8
+    Bm = torch.randint(-2, 3, (2, K, N), device="cuda").to(dt)
+    C = torch.full((R, N), 7, dtype=dt, device="cuda")
+    offsets = [3, 2_140_000_000, R]
+    with B.GroupedPlan(B.GEMM_GROUPED_ROWS, 2, R, N, K, B.GEMM_BF16, B.GEMM_ROW_MAJOR, ctas=ctas) as p:
+        ws = torch.empty(max(1, p.workspace_size), dtype=torch.uint8, device="cuda")
+        p.run(A, Bm, C, torch.tensor(offsets, dtype=torch.int32, device="cuda"), ws, torch.cuda.current_stream())
+        assert p.last_status(torch.cuda.current_stream()) == B.GEMM_OK
+    assert not bool(C[:3].view(torch.int16).any())
+    for g in range(2):
+        for at in range(offsets[g], offsets[g + 1], step):
+            end = min(at + step, offsets[g + 1])
+            assert torch.equal(C[at:end], (A[at:end].float() @ Bm[g].float()).to(dt)), at
