@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <mutex>
 
 #include "gemm_moe.h"
 #include "ptx.cuh"
@@ -645,6 +646,30 @@ gemm_status_t combine_grad(const void* dy, int64_t lddy, const void* ys, int64_t
     return fn(dy, lddy, ys, ldys, rows, slots, weights, tokens, topk, hidden, dys, lddys, dweights, stream);
 }
 
+// Allows place_kernel all the shared memory that it may need on the current
+// device, once: the limit is the function's, so a call that set its own size
+// could lower it between another thread's setting and launch.
+template <typename I>
+bool place_memory_allowed() {
+    static std::mutex mu;
+    static bool ready[64];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return false;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+        constexpr int most = 32 * GEMM_MOE_MAX_EXPERTS * (int)sizeof(uint32_t);
+        if (cudaFuncSetAttribute((const void*)place_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        ready[dev] = true;
+    }
+    return true;
+}
+
 template <typename I>
 gemm_status_t sort(const void* ids, int64_t ld, const SortArgs& shape, int32_t* offsets, int32_t* rows,
                    int32_t* slots, void* workspace, gemm_stream_t stream) {
@@ -657,11 +682,7 @@ gemm_status_t sort(const void* ids, int64_t ld, const SortArgs& shape, int32_t* 
     }
     const int threads = a.total > 1024 ? 1024 : 256;
     const size_t smem = (size_t)threads / 32 * a.experts * sizeof(uint32_t);
-    if (smem > 32 * 1024 && cudaFuncSetAttribute((const void*)place_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_CUDA;
-    }
+    if (smem > 32 * 1024 && !place_memory_allowed<I>()) return GEMM_ERR_CUDA;
     return launch(place_kernel<I>, dim3(a.blocks), dim3(threads), smem, stream, static_cast<const I*>(ids), a, table,
                   offsets, rows, slots);
 }

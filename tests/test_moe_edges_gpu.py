@@ -1,11 +1,13 @@
 """GPU tests of the mixture-of-experts operators at their edges."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from persistent_stream_matmul_gb300 import _binding as B
 from tests.gpu_util import ensure_built
-from tests.moe_util import DTYPES, Rows, assert_rounded_sum, normal
+from tests.moe_util import DTYPES, Rows, assert_rounded_sum, normal, routing, sorted_slots
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +94,34 @@ def test_rows_up_to_the_largest_index(ctas):
         for at in range(offsets[g], offsets[g + 1], step):
             end = min(at + step, offsets[g + 1])
             assert torch.equal(C[at:end], (A[at:end].float() @ Bm[g].float()).to(dt)), at
+
+
+def test_sorts_of_two_threads_do_not_disturb_each_other():
+    """Sorts of different numbers of experts, and so of shared memory, on two
+    host threads with a stream each."""
+    T, k = 2000, 2
+    failures = []
+
+    def work(experts, seed, calls):
+        try:
+            ids = routing(T, k, experts, seed)
+            want = sorted_slots(ids, experts)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                dev = torch.from_numpy(ids).cuda()
+                out = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (experts + 1, T * k, T * k)]
+            for _ in range(calls):
+                B.gemm_moe_sort(dev, B.GEMM_INDEX_I64, k, T, k, experts, *out, None, stream)
+            stream.synchronize()
+            for got, w in zip(out, want):
+                assert np.array_equal(got.cpu().numpy(), w)
+        except BaseException as e:
+            failures.append(e)
+
+    assert B.gemm_moe_sort_workspace_size(T, k, 1024) == 0
+    threads = [threading.Thread(target=work, args=(e, e, 5000)) for e in (300, 1024, 400, 1000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures[0]
