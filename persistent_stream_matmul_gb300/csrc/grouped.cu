@@ -371,22 +371,23 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void*
 
     // The maps are encoded for every run: they cost well under a microsecond
     // of host time, and nothing is kept by an operand's address.
-    CUtensorMap tmP, tmC;
-    GroupedQMaps tmQ;
-    bool ok;
+    GroupedMaps<false> tm_rows;
+    GroupedMaps<true> tm_inner;
+    bool ok = true;
     if (inner) {
         const void* P = col ? A : B;  // C's contiguous dimension
         const void* Q = col ? B : A;
-        ok = encode(&tmP, p->dtype, P, 3, p->m_total, p->rows, 1, 64, G_BK) &&
-             encode(&tmQ.m[0], p->dtype, Q, 2, p->shape.n_total, p->rows, 1, 64, G_BK);
-        tmQ.m[1] = tmQ.m[2] = tmQ.m[3] = tmQ.m[0];
+        for (int i = 0; i < 7; ++i)
+            ok = ok && encode(&tm_inner.p[i], p->dtype, P, 2, p->m_total, p->rows, 1, 64, 1u << i) &&
+                 encode(&tm_inner.q[i], p->dtype, Q, 2, p->shape.n_total, p->rows, 1, 64, 1u << i);
+        ok = ok && encode(&tm_inner.c, p->dtype, C, 3, p->m_total, p->shape.n_total, p->groups, 64, 32);
     } else {
-        ok = col ? encode(&tmP, p->dtype, B, 3, p->K, p->N, p->groups, G_BK, 128)
-                 : encode(&tmP, p->dtype, B, 3, p->N, p->K, p->groups, 64, G_BK);
+        ok = col ? encode(&tm_rows.p[0], p->dtype, B, 3, p->K, p->N, p->groups, G_BK, 128)
+                 : encode(&tm_rows.p[0], p->dtype, B, 3, p->N, p->K, p->groups, 64, G_BK);
         for (int i = 0; i < 4; ++i)
-            ok = ok && encode(&tmQ.m[i], p->dtype, A, 2, p->K, p->rows, 1, G_BK, 16u << i);
+            ok = ok && encode(&tm_rows.q[i], p->dtype, A, 2, p->K, p->rows, 1, G_BK, 16u << i);
+        ok = ok && encode(&tm_rows.c, p->dtype, C, 3, p->m_total, p->rows, 1, 64, 32);
     }
-    ok = ok && encode(&tmC, p->dtype, C, 3, p->m_total, inner ? p->shape.n_total : p->rows, inner ? p->groups : 1, 64, 32);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
 
     GroupedParams kp{};
@@ -424,7 +425,7 @@ gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void* A, const void*
     ++na;
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    void* args[4] = {&tmP, &tmQ, &tmC, &kp};
+    void* args[2] = {inner ? (void*)&tm_inner : (void*)&tm_rows, &kp};
     if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;

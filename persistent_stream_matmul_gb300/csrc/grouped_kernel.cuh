@@ -19,16 +19,18 @@
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0     TMA producer, a ring of STAGES stages of 16 KB of P and up to
 //              16 KB of Q (128-byte swizzle), as many rows of Q as the tile has.
+//              INNER: a group's last k-block may end inside a 16-row step of
+//              the MMA.  Its copies then are cut into boxes of 32, 16, 8 .. 1 rows:
+//              the group's rows, then rows past the tensor's end, which read as
+//              zeros, up to the next multiple of 16, where the MMA stops.  Zeros in
+//              both operands, so that whatever a neighbour's rows hold (NaN,
+//              infinity) adds nothing.  All of a block's bytes are counted on its
+//              one barrier, so a pair needs no order between one CTA's writes to
+//              shared memory and the MMA that the other issues.  (Zeros written by
+//              a warp, released at cluster scope: 64 gradients of 2048 x 1536 over
+//              512 rows each 157 us against 143.)
 //   warp 1     one lane issues the MMAs (pair: the first CTA's, for both).
-//   warp 2     allocates tensor memory.  INNER: writes zeros over the rows of a
-//              group's last k-block past its end, up to the next multiple of
-//              16, where the MMA stops: zeros in both operands, so that
-//              whatever a neighbour's rows hold (NaN, infinity) adds nothing.
-//              Only such a block passes through this warp, on barriers of its
-//              own (each CTA's copies complete on its own barrier, then both
-//              CTAs report to the issuing one).  With every block relayed this
-//              way, the gradient of 8 matrices of 14336 x 4096 over 16384 rows
-//              took 2780 us.
+//   warp 2     allocates tensor memory.
 //   warp 3     scheduler: walks this unit's work and hands every piece to the
 //              other warps through a queue of G_QUEUE entries in shared memory.
 //              With the walk (searches and divisions, ~1000 cycles) repeated
@@ -84,12 +86,12 @@ struct GroupedCfg {
     static constexpr int OUT_BYTES = 32 * 256;    // one staged chunk: 32 rows x 128 columns
     static constexpr int TABLE_BYTES = 2 * (G_MAX_GROUPS + 4) * 4;
     static constexpr int QUEUE_BYTES = G_QUEUE * 48;
-    static constexpr int BAR_BYTES = 320;
+    static constexpr int BAR_BYTES = 256;
     static constexpr int TMEM_COLS = 2 * TILE_N;  // two accumulators
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * OUT_BYTES + TABLE_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
     static constexpr int SLOT_FLOATS = 128 * TILE_N;  // a CTA's partial tile
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-    static_assert((4 * STAGES + 5 + 2 * G_QUEUE) * 8 + 16 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 5 + 2 * G_QUEUE) * 8 + 16 <= BAR_BYTES, "barrier area");
 };
 
 struct GroupedParams {
@@ -256,15 +258,17 @@ __device__ __forceinline__ bool grouped_vote_all(bool v) {
     return out != 0;
 }
 
-struct GroupedQMaps {
-    CUtensorMap m[4];  // ROWS: boxes of 16, 32, 64 and 128 rows; INNER: m[0], 64 x 64
+// ROWS: p reads the matrices, q[i] boxes of 16 << i rows of A.  INNER: p[i] and
+// q[i] read boxes of 1 << i rows.
+template <bool INNER>
+struct GroupedMaps {
+    CUtensorMap p[INNER ? 7 : 1], q[INNER ? 7 : 4], c;
 };
 
 // P_MN: P is MN-major (INNER: both operands are).
 template <bool PAIR, bool INNER, bool P_MN, bool OUT_BF16>
 __global__ void __launch_bounds__(G_THREADS, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ GroupedQMaps tmQ,
-                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GroupedParams p) {
+    grouped_kernel(const __grid_constant__ GroupedMaps<INNER> tm, const __grid_constant__ GroupedParams p) {
     using Cf = GroupedCfg<PAIR>;
     static_assert(!INNER || P_MN, "INNER reads both operands MN-major");
     constexpr int STAGES = Cf::STAGES;
@@ -283,16 +287,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const uint32_t bar_base = smem_addr(bar_area);
     auto full_bar = [&](int s) { return bar_base + 8u * s; };
     auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
-    // INNER, a stage that holds a group's ragged last block: its copies into
-    // this CTA, and (first CTA) the CTAs that have written its zeros
-    auto ragged_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
-    auto ready_bar = [&](int s) { return bar_base + 8u * (3 * STAGES + s); };
-    auto tfull_bar = [&](int b) { return bar_base + 8u * (4 * STAGES + b); };
-    auto tempty_bar = [&](int b) { return bar_base + 8u * (4 * STAGES + 2 + b); };
-    const uint32_t done_bar = bar_base + 8u * (4 * STAGES + 4);
-    auto qfull_bar = [&](int s) { return bar_base + 8u * (4 * STAGES + 5 + s); };
-    auto qempty_bar = [&](int s) { return bar_base + 8u * (4 * STAGES + 5 + G_QUEUE + s); };
-    constexpr int BARS = 4 * STAGES + 5 + 2 * G_QUEUE;
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + 2 + b); };
+    const uint32_t done_bar = bar_base + 8u * (2 * STAGES + 4);
+    auto qfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 5 + s); };
+    auto qempty_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 5 + G_QUEUE + s); };
+    constexpr int BARS = 2 * STAGES + 5 + 2 * G_QUEUE;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 8 * BARS + 4);
     volatile int* last_flag = reinterpret_cast<volatile int*>(bar_area + 8 * BARS + 8);
@@ -306,17 +306,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
-            mbar_init(ragged_bar(s), 1);
-            mbar_init(ready_bar(s), Cf::CM);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
             mbar_init(tempty_bar(b), Cf::CM * G_EPI_THREADS / 32);
         }
         mbar_init(done_bar, 1);
-        // readers of the queue: producer, issuer (pair: the first CTA's), INNER's
-        // warp 2 and the epilogue warps
-        const int readers = 1 + (!PAIR || rank == 0) + INNER + G_EPI_THREADS / 32;
+        // readers of the queue: producer, issuer (pair: the first CTA's) and the epilogue warps
+        const int readers = 1 + (!PAIR || rank == 0) + G_EPI_THREADS / 32;
         for (int s = 0; s < G_QUEUE; ++s) {
             mbar_init(qfull_bar(s), 1);
             mbar_init(qempty_bar(s), readers);
@@ -325,8 +322,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmP);
-        tma_prefetch_desc(&tmQ.m[0]);
+        tma_prefetch_desc(&tm.p[INNER ? 6 : 0]);
+        tma_prefetch_desc(&tm.q[INNER ? 6 : 0]);
     }
     if (warp == 2) {
         if constexpr (PAIR) {
@@ -374,15 +371,11 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
         return w.item >= 0;
     };
-    // INNER: whether k-block kb ends inside a 16-row step
-    auto ragged = [&](int kb) { return INNER && kb + 1 == w.kb && ((w.r1 - w.r0) & 15) != 0; };
-
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         int stage = 0;
         uint32_t phase = 0;
         uint32_t filled = 0, fill_parity = 0;
-        uint32_t ragged_used = 0, ragged_parity = 0;  // per stage: parity of the last ragged fill
         bool ok = true;
         const uint32_t full0_c = PAIR ? mapa_shared(full_bar(0), 0) : 0u;
         while (ok && next_work()) {
@@ -392,72 +385,61 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             // ROWS: the smallest box that holds them (a box a bit of their number,
             // which reads fewer rows in more copies, measured the same)
             const int box = rows_q <= 16 ? 0 : rows_q <= 32 ? 1 : rows_q <= 64 ? 2 : 3;
-            const uint32_t q_bytes = INNER ? (uint32_t)Cf::Q_BYTES : (16u << box) * 128u;
+            const uint32_t q_bytes = (16u << box) * 128u;
             for (int kb = w.k0; kb < w.k1; ++kb) {
                 if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.pipe_limit_ns))) {
                     if (lane == 0) fail_pipe();
                     ok = false;
                     break;
                 }
-                if (elect_one()) {
-                    const uint32_t sp = ring + stage * Cf::STAGE_BYTES;
-                    const uint32_t sq = sp + Cf::P_BYTES;
-                    if constexpr (INNER) {
-                        const int k = w.r0 + kb * G_BK;
-                        uint32_t fb = full_bar(stage);
-                        if (ragged(kb)) {
-                            if (rank == 0) mbar_arrive(fb);
-                            fb = ragged_bar(stage);
-                            mbar_arrive_expect_tx(fb, Cf::STAGE_BYTES);
-                        } else if constexpr (PAIR) {
-                            if (rank == 0) mbar_arrive_expect_tx(fb, 2 * Cf::STAGE_BYTES);
-                            fb = full0_c + 8u * (uint32_t)stage;
-                        } else {
-                            mbar_arrive_expect_tx(fb, Cf::STAGE_BYTES);
+                const uint32_t sp = ring + stage * Cf::STAGE_BYTES;
+                const uint32_t sq = sp + Cf::P_BYTES;
+                const uint32_t fb = full_bar(stage), fbc = full0_c + 8u * (uint32_t)stage;
+                auto load_2d = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+                    if constexpr (PAIR) tma_load_2d_pair(dst, map, fbc, x, y, false, 0);
+                    else tma_load_2d(dst, map, fb, x, y, false, 0);
+                };
+                // INNER: rows of the group in this block, and up to the next step of 16
+                const int k_inner = w.r0 + kb * G_BK, rows = min(G_BK, w.r1 - k_inner), zeros = -rows & 15;
+                if (INNER && zeros) {
+                    if (elect_one() && rank == 0) mbar_arrive_expect_tx(fb, Cf::CM * 4 * (rows + zeros) * 128);
+                    // four boxes of 64 columns (two of P, two of Q) by ten pieces: one a
+                    // bit of the rows, from 32 down, and one a bit of the zeros, from 8
+                    for (int i = lane; i < 40; i += 32) {
+                        const int box64 = i & 3, piece = i >> 2;
+                        const bool own = piece < 6;
+                        const int bit = own ? 5 - piece : 9 - piece, all = own ? rows : zeros;
+                        if ((all >> bit) & 1) {
+                            const int at = (own ? 0 : rows) + ((all >> bit >> 1) << bit << 1);
+                            load_2d(sp + box64 * G_CHUNK + at * 128, box64 < 2 ? &tm.p[bit] : &tm.q[bit],
+                                    (box64 < 2 ? m0 : q0) + 64 * (box64 & 1), own ? k_inner + at : p.s.rows);
                         }
-                        if (PAIR && !ragged(kb)) {
+                    }
+                } else if (elect_one()) {
+                    if constexpr (INNER) {
+                        if (rank == 0) mbar_arrive_expect_tx(fb, Cf::CM * Cf::STAGE_BYTES);
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                tma_load_3d_pair(sp + c * G_CHUNK, &tmP, fb, m0 + 64 * c, k, 0);
-                                tma_load_2d_pair(sq + c * G_CHUNK, &tmQ.m[0], fb, q0 + 64 * c, k, false, 0);
-                            }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                tma_load_3d(sp + c * G_CHUNK, &tmP, fb, m0 + 64 * c, k, 0);
-                                tma_load_2d(sq + c * G_CHUNK, &tmQ.m[0], fb, q0 + 64 * c, k, false, 0);
-                            }
+                        for (int c = 0; c < 2; ++c) {
+                            load_2d(sp + c * G_CHUNK, &tm.p[6], m0 + 64 * c, k_inner);
+                            load_2d(sq + c * G_CHUNK, &tm.q[6], q0 + 64 * c, k_inner);
                         }
                     } else {
                         const int k = kb * G_BK;
-                        if constexpr (PAIR) {
-                            const uint32_t fbc = full0_c + 8u * (uint32_t)stage;
-                            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * (Cf::P_BYTES + q_bytes));
-                            if constexpr (P_MN) {
-                                tma_load_3d_pair(sp, &tmP, fbc, m0, k, w.group);
-                                tma_load_3d_pair(sp + G_CHUNK, &tmP, fbc, m0 + 64, k, w.group);
-                            } else {
-                                tma_load_3d_pair(sp, &tmP, fbc, k, m0, w.group);
-                            }
-                            tma_load_2d_pair(sq, &tmQ.m[box], fbc, k, q0, false, 0);
+                        auto load_3d = [&](uint32_t dst, int x, int y) {
+                            if constexpr (PAIR) tma_load_3d_pair(dst, &tm.p[0], fbc, x, y, w.group);
+                            else tma_load_3d(dst, &tm.p[0], fb, x, y, w.group);
+                        };
+                        if (rank == 0) mbar_arrive_expect_tx(fb, Cf::CM * (Cf::P_BYTES + q_bytes));
+                        if constexpr (P_MN) {
+                            load_3d(sp, m0, k);
+                            load_3d(sp + G_CHUNK, m0 + 64, k);
                         } else {
-                            const uint32_t fb = full_bar(stage);
-                            mbar_arrive_expect_tx(fb, Cf::P_BYTES + q_bytes);
-                            if constexpr (P_MN) {
-                                tma_load_3d(sp, &tmP, fb, m0, k, w.group);
-                                tma_load_3d(sp + G_CHUNK, &tmP, fb, m0 + 64, k, w.group);
-                            } else {
-                                tma_load_3d(sp, &tmP, fb, k, m0, w.group);
-                            }
-                            tma_load_2d(sq, &tmQ.m[box], fb, k, q0, false, 0);
+                            load_3d(sp, k, m0);
                         }
+                        load_2d(sq, &tm.q[box], k, q0);
                     }
                 }
                 __syncwarp();
-                if (ragged(kb)) {  // a stage's first ragged fill has parity 0
-                    ragged_parity ^= (ragged_used & (1u << stage));
-                    ragged_used |= 1u << stage;
-                }
                 filled |= 1u << stage;
                 fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == STAGES) {
@@ -471,7 +453,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         for (int s = 0; s < STAGES; ++s)
             if (filled & (1u << s)) {
                 if (!PAIR || rank == 0) mbar_wait(full_bar(s), (fill_parity >> s) & 1u, p.pipe_limit_ns);
-                if (ragged_used & (1u << s)) mbar_wait(ragged_bar(s), (ragged_parity >> s) & 1u, p.pipe_limit_ns);
                 mbar_wait(empty_bar(s), (fill_parity >> s) & 1u, p.pipe_limit_ns);
             }
     } else if (warp == 1) {
@@ -479,7 +460,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         if (!PAIR || rank == 0) {
             int stage = 0;
             uint32_t phase = 0, iter = 0;
-            uint32_t ready_phase = 0;  // INNER: next parity of each stage's ready barrier
             bool ok = true;
             const uint64_t p_desc0 = smem_desc_sw128(ring, P_MN ? G_CHUNK : 16, 1024);
             const uint64_t q_desc0 = smem_desc_sw128(ring + Cf::P_BYTES, INNER ? G_CHUNK : 16, 1024);
@@ -498,13 +478,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 const uint32_t d_tmem = tmem_base + (uint32_t)(buf * Cf::TILE_N);
                 const uint32_t idesc = p.idesc | ((uint32_t)(w.width >> 3) << 17);
                 for (int kb = w.k0; kb < w.k1; ++kb) {
-                    bool got = mbar_wait(full_bar(stage), phase, p.pipe_limit_ns);
-                    if (ragged(kb)) {
-                        got = got && mbar_wait_acq_cluster(ready_bar(stage), (ready_phase >> stage) & 1u,
-                                                           p.pipe_limit_ns);
-                        ready_phase ^= 1u << stage;
-                    }
-                    if (!__all_sync(0xffffffffu, got)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.pipe_limit_ns))) {
                         if (lane == 0) fail_pipe();
                         ok = false;
                         break;
@@ -549,35 +523,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
             __syncwarp();
             mbar_wait(done_bar, 0, p.pipe_limit_ns);
-        }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ INNER: ragged blocks
-        if constexpr (INNER) {
-            int stage = 0;  // of the work's first block
-            uint32_t phases = 0;
-            const uint32_t ready0 = mapa_shared(ready_bar(0), 0);  // the issuing CTA's
-            while (next_work()) {
-                if (w.k1 > w.k0 && ragged(w.k1 - 1)) {
-                    const int st = (stage + (w.k1 - 1 - w.k0)) % STAGES;
-                    if (!__all_sync(0xffffffffu,
-                                    mbar_wait(ragged_bar(st), (phases >> st) & 1u, p.pipe_limit_ns))) {
-                        if (lane == 0) fail_pipe();
-                        break;
-                    }
-                    phases ^= 1u << st;
-                    // four boxes (two of P, two of Q) of 64 k-rows x 128 bytes
-                    const int z0 = w.r1 - w.r0 - (w.kb - 1) * G_BK, zn = 16 - (z0 & 15);
-                    const uint32_t base = ring + st * Cf::STAGE_BYTES;
-                    for (int i = lane; i < zn * 32; i += 32) {
-                        const int box = (i >> 3) & 3, r = z0 + (i >> 5);
-                        st_shared_u4(base + box * G_CHUNK + r * 128 + (i & 7) * 16, 0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_fenced(ready0 + 8u * (uint32_t)st);
-                }
-                stage = (stage + w.k1 - w.k0) % STAGES;
-            }
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ scheduler
@@ -644,8 +589,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             named_bar_sync(G_BAR_HALF + half, 128);
             if (box) {
                 if (et == 0) {
-                    if (col0 < p.m_total) tma_store_3d(&tmC, stage_base, col0, w.n0 + 32 * c, INNER ? w.group : 0);
-                    if (col0 + 64 < p.m_total) tma_store_3d(&tmC, stage_base + 4096, col0 + 64, w.n0 + 32 * c, INNER ? w.group : 0);
+                    if (col0 < p.m_total) tma_store_3d(&tm.c, stage_base, col0, w.n0 + 32 * c, INNER ? w.group : 0);
+                    if (col0 + 64 < p.m_total) tma_store_3d(&tm.c, stage_base + 4096, col0 + 64, w.n0 + 32 * c, INNER ? w.group : 0);
                     bulk_commit_group();
                 }
                 return;

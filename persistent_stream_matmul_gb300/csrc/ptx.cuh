@@ -230,11 +230,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
-// The same arrive with release at CTA scope only: for work that a fence before
-// it has already completed at its place (tensor-memory loads before
-// tcgen05.wait::ld and tcgen05.fence, shared-memory writes before
-// fence.proxy.async).  The cluster-scope release waits for all of the thread's
-// memory operations, about 2000 cycles behind a tile's stores.
+// The same arrive with release at CTA scope only, for an arrival that orders no
+// memory between the CTAs: the pair's tensor memory has been read into registers
+// (tcgen05.wait::ld, then tcgen05.fence) and may be written again.  The
+// cluster-scope release waits for all of the thread's memory operations, about
+// 2000 cycles behind a tile's stores.
 __device__ __forceinline__ void mbar_arrive_cluster_fenced(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

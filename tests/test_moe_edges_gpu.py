@@ -96,6 +96,38 @@ def test_rows_up_to_the_largest_index(ctas):
             assert torch.equal(C[at:end], (A[at:end].float() @ Bm[g].float()).to(dt)), at
 
 
+@pytest.mark.parametrize("layout", [B.GEMM_COL_MAJOR, B.GEMM_ROW_MAJOR])
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_blocks_that_end_inside_a_step(ctas, layout):
+    """Groups of every size from 1 to 63 and beyond, each followed by one of NaN
+    and infinite rows: the rows past a group's end that its last block covers add
+    nothing, in either CTA of a pair, run after run."""
+    counts = [n for i in range(1, 130) for n in (i, 1 + i % 3)]
+    R, G, N, K = sum(counts) + 5, len(counts), 328, 264
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A = torch.randint(-2, 3, (R, K), generator=g, device="cuda").half()
+    D = torch.randint(-2, 3, (R, N), generator=g, device="cuda").half()
+    want = torch.zeros((G, K, N), dtype=torch.float64, device="cuda")
+    for e in range(0, G, 2):
+        at = slice(offsets[e], offsets[e + 1])
+        want[e] = A[at].double().t() @ D[at].double()
+        A[offsets[e + 1]:offsets[e + 2]] = float("nan")
+        D[offsets[e + 1]:offsets[e + 2]] = float("inf")
+    A[offsets[-1]:] = D[offsets[-1]:] = float("nan")
+    want = want[::2].transpose(1, 2) if layout == B.GEMM_COL_MAJOR else want[::2]
+    offs = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    C = torch.empty((G, *want.shape[1:]), dtype=torch.float16, device="cuda")
+    with B.GroupedPlan(B.GEMM_GROUPED_INNER, G, R, N, K, B.GEMM_F16, layout, ctas=ctas) as p:
+        ws = torch.empty(max(1, p.workspace_size), dtype=torch.uint8, device="cuda")
+        for _ in range(10):
+            C.fill_(7)
+            p.run(A, D, C, offs, ws, torch.cuda.current_stream())
+            assert torch.equal(C[::2].double(), want)  # whole numbers, at most 4 * 129
+            assert bool(torch.isnan(C[1::2]).all())
+        assert p.last_status(torch.cuda.current_stream()) == B.GEMM_OK
+
+
 def test_sorts_of_two_threads_do_not_disturb_each_other():
     """Sorts of different numbers of experts, and so of shared memory, on two
     host threads with a stream each."""
