@@ -126,7 +126,11 @@ typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
 enum {
     /* CTAs of a scheduling unit: 1 (tiles of 128 x up to 128), or 2, a cluster
      * that runs pair MMAs (256 x up to 256); 0 (default) lets the plan choose. */
-    GEMM_GROUPED_OPT_CTAS = 1
+    GEMM_GROUPED_OPT_CTAS = 1,
+    /* test hook: the scheduling unit with this index gives up before it writes
+     * its first piece, as if a wait had run out, in every run that starts after
+     * the call, replays of captured ones among them.  -1 (default) = off. */
+    GEMM_GROUPED_OPT_INJECT_GIVE_UP = 3
 };
 
 /* Keys for gemm_grouped_plan_get_info. */
@@ -166,7 +170,8 @@ gemm_status_t gemm_grouped_plan_create_offline(gemm_grouped_plan_t *out, gemm_gr
                                                int num_sms);
 
 /* Set one GEMM_GROUPED_OPT_* option.  On error the plan keeps its options.
- * Errors: INVALID_ARG (NULL plan, unknown key), UNSUPPORTED (value). */
+ * Errors: INVALID_ARG (NULL plan, unknown key), UNSUPPORTED (value), NO_DEVICE
+ * (offline plan) and CUDA (INJECT_GIVE_UP). */
 gemm_status_t gemm_grouped_plan_set_option(gemm_grouped_plan_t plan, int key, int64_t value);
 
 /* Read one GEMM_GROUPED_INFO_* value.  Errors: INVALID_ARG. */
@@ -204,7 +209,9 @@ gemm_status_t gemm_grouped_workspace_size(gemm_grouped_plan_t plan, size_t *byte
 gemm_status_t gemm_grouped_run(gemm_grouped_plan_t plan, const void *A, const void *B, void *C,
                                const int32_t *offsets, void *workspace, gemm_stream_t stream);
 
-/* As gemm_last_status, for a grouped plan. */
+/* As gemm_last_status, for a grouped plan.  After a timeout it waits for the
+ * device; replays of captured runs are right again from then on, and may be
+ * wrong between the timeout and this call. */
 gemm_status_t gemm_grouped_last_status(gemm_grouped_plan_t plan, gemm_stream_t stream);
 
 /* Free the plan.  NULL is accepted.  Always returns GEMM_OK. */

@@ -7,7 +7,8 @@ generator.  Loading the binding's functions fails loudly if the library is
 not built: there is no CPU fallback.
 """
 from ._binding import (  # noqa: F401
-    GEMM_BF16, GEMM_COL_MAJOR, GEMM_GROUPED_INNER, GEMM_GROUPED_OPT_CTAS, GEMM_GROUPED_ROWS, GEMM_INDEX_I32, GEMM_INDEX_I64,
+    GEMM_BF16, GEMM_COL_MAJOR, GEMM_GROUPED_INNER, GEMM_GROUPED_OPT_CTAS,
+    GEMM_GROUPED_OPT_INJECT_GIVE_UP, GEMM_GROUPED_ROWS, GEMM_INDEX_I32, GEMM_INDEX_I64,
     GEMM_MOE_MAX_EXPERTS, GEMM_SCHED_AUTO, GEMM_F16, GEMM_ROW_MAJOR, GEMM_SCHED_DATA_PARALLEL,
     GEMM_SCHED_PERSISTENT, GEMM_SCHED_SPLITK, GEMM_SCHED_STREAMK, GemmError, GroupedPlan, Plan, SCHEDULES,
     gemm_grouped_last_status, gemm_grouped_plan_create, gemm_grouped_plan_create_offline,

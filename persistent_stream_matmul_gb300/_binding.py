@@ -52,7 +52,7 @@ INFO = {
 GEMM_INDEX_I32, GEMM_INDEX_I64 = 0, 1
 GEMM_GROUPED_ROWS, GEMM_GROUPED_INNER = 0, 1
 GEMM_MOE_MAX_EXPERTS = 1024
-GEMM_GROUPED_OPT_CTAS = 1
+GEMM_GROUPED_OPT_CTAS, GEMM_GROUPED_OPT_INJECT_GIVE_UP = 1, 3
 GROUPED_INFO = {"ctas": 1, "units": 2, "tile_m": 3, "tile_n": 4, "stages": 5, "smem_bytes": 6}
 
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3

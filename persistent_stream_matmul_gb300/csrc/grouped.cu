@@ -26,7 +26,8 @@ struct gemm_grouped_plan {
     int64_t m_total;      // C's contiguous extent (the lanes side)
     GroupedShape shape;
     size_t counter_bytes, ws_bytes;
-    int* d_status;
+    int* d_status;        // G_WORDS words
+    int timeouts;         // G_WORD_TIMEOUTS
 };
 
 namespace {
@@ -236,8 +237,8 @@ gemm_status_t make_plan(gemm_grouped_plan_t* out, int kind, int64_t groups, int6
         delete p;
         return st;
     }
-    if (!offline && (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess ||
-                     cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess)) {
+    if (!offline && (cudaMalloc(&p->d_status, G_WORDS * sizeof(int)) != cudaSuccess ||
+                     cudaMemset(p->d_status, 0, G_WORDS * sizeof(int)) != cudaSuccess)) {
         cudaGetLastError();
         if (p->d_status) cudaFree(p->d_status);
         delete p;
@@ -280,7 +281,16 @@ gemm_status_t gemm_grouped_plan_create_offline(gemm_grouped_plan_t* out, gemm_gr
 }
 
 gemm_status_t gemm_grouped_plan_set_option(gemm_grouped_plan_t p, int key, int64_t value) {
-    if (!p || key != GEMM_GROUPED_OPT_CTAS) return GEMM_ERR_INVALID_ARG;
+    if (!p || (key != GEMM_GROUPED_OPT_CTAS && key != GEMM_GROUPED_OPT_INJECT_GIVE_UP)) return GEMM_ERR_INVALID_ARG;
+    if (key == GEMM_GROUPED_OPT_INJECT_GIVE_UP) {
+        if (value < -1 || value >= p->shape.units) return GEMM_ERR_UNSUPPORTED;
+        if (p->offline) return GEMM_ERR_NO_DEVICE;
+        DeviceGuard guard(p->device);
+        const int word = (int)value + 1;
+        return guard.ok && cudaMemcpy(p->d_status + G_WORD_GIVE_UP, &word, sizeof(int), cudaMemcpyHostToDevice) == cudaSuccess
+                   ? GEMM_OK
+                   : GEMM_ERR_CUDA;
+    }
     if (value < 0 || value > 2) return GEMM_ERR_UNSUPPORTED;
     const int saved = p->opt_ctas;
     p->opt_ctas = (int)value;
@@ -440,9 +450,17 @@ gemm_status_t gemm_grouped_last_status(gemm_grouped_plan_t p, gemm_stream_t stre
     if (!guard.ok) return GEMM_ERR_CUDA;
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
     int h = 0;
-    if (cudaMemcpy(&h, p->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (cudaMemcpy(&h, p->d_status + G_WORD_STATUS, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
     if (h == 0) return GEMM_OK;
-    return cudaMemset(p->d_status, 0, sizeof(int)) == cudaSuccess ? GEMM_ERR_TIMEOUT : GEMM_ERR_CUDA;
+    // another tag from here on (grouped_tag), which no run on another stream may
+    // see changing under way
+    static_assert(G_WORD_STATUS == 0 && G_WORD_TIMEOUTS == 1, "both words are written at once");
+    const int words[2] = {0, p->timeouts + 1};
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(p->d_status, words, sizeof(words), cudaMemcpyHostToDevice) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    ++p->timeouts;
+    return GEMM_ERR_TIMEOUT;
 }
 
 gemm_status_t gemm_grouped_plan_destroy(gemm_grouped_plan_t p) {

@@ -74,6 +74,9 @@ constexpr int G_BOX_BLOCKS = 8;
 constexpr uint32_t G_CHUNK = 64 * 128;  // one 64 x 64 MN-major box
 enum : uint32_t { G_BAR_EPI = 1, G_BAR_VOTE = 2, G_BAR_HALF = 3 };  // G_BAR_HALF + half
 enum : int { G_STATUS_PIPE_TIMEOUT = 2 };
+// a plan's device words: the status; how often a timeout has been reported; and,
+// for tests, the unit that gives up, counted from 1
+enum : int { G_WORD_STATUS, G_WORD_TIMEOUTS, G_WORD_GIVE_UP, G_WORDS };
 
 template <bool PAIR>
 struct GroupedCfg {
@@ -102,37 +105,45 @@ struct GroupedParams {
     const int32_t* offsets;
     float* partials;              // a slot a CTA
     unsigned long long* counters; // one a split tile and CTA of the pair
-    uint64_t epoch;               // run number tagged into the counters, 48 bits
-    int* status;
+    uint64_t epoch;               // run number, in the counters' tags, 48 bits
+    int* status;                  // G_WORD_ words of the plan
     uint32_t idesc;               // without N
     uint64_t pipe_limit_ns;
 };
 
-// The counter of a split tile holds (epoch << 16) | count.  A word with another
-// epoch (of another run, or whatever the workspace held) counts as none, so the
+// The counter of a split tile holds (tag << 16) | count.  A word with another
+// tag (of another run, or whatever the workspace held) counts as none, so the
 // workspace needs no clearing, and the last arrival leaves 0, so that a replay
 // of the same launch starts afresh.  The tile's first contributor opens the
 // counter long before anyone arrives; an arrival is then one atomic add.  (With
 // a compare-and-swap an arrival, five contributors took up to 6 us to count.)
 // An arrival that finds it unopened opens it itself.
-__device__ __forceinline__ void grouped_open_counter(unsigned long long* f, uint64_t epoch) {
+//
+// A run whose waits ran out leaves counts behind, and a replay of it has the
+// same run number.  So the tag also counts the plan's reported timeouts: what
+// such a run left then reads as another run's.
+__device__ __forceinline__ uint64_t grouped_tag(uint64_t epoch, const int* words) {
+    return (epoch + (uint64_t)(uint32_t)words[G_WORD_TIMEOUTS] * 0x9e3779b97f4a7c15ull) & 0xffffffffffffull;
+}
+
+__device__ __forceinline__ void grouped_open_counter(unsigned long long* f, uint64_t tag) {
     uint64_t cur = *reinterpret_cast<volatile unsigned long long*>(f);
 #pragma unroll 1
-    for (int tries = 0; tries < (1 << 20) && (cur >> 16) != epoch; ++tries) {
-        const uint64_t prev = atom_cas_acq_rel_u64(f, cur, epoch << 16);
+    for (int tries = 0; tries < (1 << 20) && (cur >> 16) != tag; ++tries) {
+        const uint64_t prev = atom_cas_acq_rel_u64(f, cur, tag << 16);
         if (prev == cur) return;
         cur = prev;
     }
 }
 
 // Count one contribution in; true when it was the last of n.
-__device__ __forceinline__ bool grouped_count_in(unsigned long long* f, uint64_t epoch, uint32_t n) {
+__device__ __forceinline__ bool grouped_count_in(unsigned long long* f, uint64_t tag, uint32_t n) {
     uint64_t have = atom_add_acq_rel_u64(f, 1);
-    if ((have >> 16) != epoch) {
+    if ((have >> 16) != tag) {
         uint64_t cur = have + 1;  // what the add left; it has not counted
 #pragma unroll 1
         for (int tries = 0; tries < (1 << 20); ++tries) {
-            const uint64_t base = (cur >> 16) == epoch ? cur : epoch << 16;
+            const uint64_t base = (cur >> 16) == tag ? cur : tag << 16;
             const uint64_t prev = atom_cas_acq_rel_u64(f, cur, base + 1);
             if (prev == cur) {
                 have = base;
@@ -345,7 +356,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 
     auto fail_pipe = [&]() {
         *abort_flag = 1;
-        atomicCAS(p.status, 0, G_STATUS_PIPE_TIMEOUT);
+        atomicCAS(p.status + G_WORD_STATUS, 0, G_STATUS_PIPE_TIMEOUT);
     };
 
     GroupedWork w{};
@@ -526,6 +537,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ scheduler
+        const uint64_t tag = grouped_tag(p.epoch, p.status);
         const int32_t blocks = grouped_tables(p.s, p.offsets, off, first);
         const GroupedTables tab{off, first};
         const int32_t tiles = first[p.s.groups];
@@ -551,7 +563,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 st_shared_u4(at + 32, w.r1, w.k0, w.k1, w.kb);
                 mbar_arrive(qfull_bar(qslot));
                 if (more && w.shares > 1 && w.item == unit)  // this unit has the first share
-                    grouped_open_counter(p.counters + (size_t)unit * Cf::CM + rank, p.epoch);
+                    grouped_open_counter(p.counters + (size_t)unit * Cf::CM + rank, tag);
             }
             __syncwarp();
             if (++qslot == G_QUEUE) {
@@ -565,6 +577,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int half = (warp - G_EPI_WARP0) >> 2;
         const int et = (threadIdx.x - G_EPI_WARP0 * 32) & 127;  // thread of its half
         const bool lead = threadIdx.x == G_EPI_WARP0 * 32;
+        const uint64_t tag = grouped_tag(p.epoch, p.status);
+        const bool give_up = p.status[G_WORD_GIVE_UP] == unit + 1;
         uint32_t iter = 0;
         int32_t used0 = 0, used1 = p.s.rows;  // the rows of the groups, from the end of the queue
         auto barrier = [&]() { named_bar_sync(G_BAR_EPI, G_EPI_THREADS); };
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const int buf = iter & 1;
             const int chunks = (w.valid + 31) / 32;
             const bool got = more && (empty || (mbar_wait(tfull_bar(buf), (iter >> 1) & 1u, p.pipe_limit_ns) &&
-                                                *abort_flag == 0));
+                                                *abort_flag == 0)) && !give_up;
             if (more && !got && lane == 0) fail_pipe();
             // (a warp that gives up must not leave the others at a barrier)
             if (!grouped_vote_all(got)) {
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 // count, a release and acquire at GPU scope
                 barrier();
                 if (lead)
-                    *last_flag = grouped_count_in(p.counters + (size_t)w.item * Cf::CM + rank, p.epoch,
+                    *last_flag = grouped_count_in(p.counters + (size_t)w.item * Cf::CM + rank, tag,
                                                   (uint32_t)w.shares);
                 barrier();
                 const bool last = *last_flag != 0;

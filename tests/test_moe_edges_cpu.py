@@ -57,3 +57,12 @@ def test_more_units_than_an_index_holds_twice(sms):
     counts = {u: _work(plan, [0, 50, 60, 100], u)[1] for u in (0, 1, 11, 12, sms - 1)}
     assert counts == {0: 1, 1: 1, 11: 1, 12: 0, sms - 1: 0}
     plan.close()
+
+
+def test_give_up_hook_refusals():
+    plan = B.GroupedPlan(B.GEMM_GROUPED_ROWS, 3, 100, 256, 256, B.GEMM_BF16, B.GEMM_ROW_MAJOR, offline_sms=152)
+    for value, status in ((-2, B.GEMM_ERR_UNSUPPORTED), (plan.info("units"), B.GEMM_ERR_UNSUPPORTED), (0, B.GEMM_ERR_NO_DEVICE)):
+        with pytest.raises(B.GemmError) as e:
+            plan.set_option(B.GEMM_GROUPED_OPT_INJECT_GIVE_UP, value)
+        assert e.value.status == status
+    plan.close()

@@ -128,6 +128,52 @@ def test_blocks_that_end_inside_a_step(ctas, layout):
         assert p.last_status(torch.cuda.current_stream()) == B.GEMM_OK
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
+@pytest.mark.parametrize("kind", [B.GEMM_GROUPED_ROWS, B.GEMM_GROUPED_INNER])
+def test_replays_after_a_timeout(kind, ctas):
+    """A captured launch in which one contributor to a split tile gives up: the
+    timeout is reported, and the next replays join what they themselves summed,
+    which leaves every counter (the workspace's first words, one a CTA) at none."""
+    counts, N, K = ([2, 0, 5], 72, 8192) if kind == B.GEMM_GROUPED_ROWS else ([700, 8300, 0], 72, 136)
+    G, R = len(counts), sum(counts)
+    code, dt = DTYPES["bf16"]
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    offs = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    Bm = normal((G, N, K) if kind == B.GEMM_GROUPED_ROWS else (R, N), dt, 2, 0.25)
+    A = torch.empty((R, K), dtype=dt, device="cuda")
+    C = torch.empty((R, N) if kind == B.GEMM_GROUPED_ROWS else (G, N, K), dtype=dt, device="cuda")
+    p = B.GroupedPlan(kind, G, R, N, K, code, B.GEMM_COL_MAJOR, ctas=ctas)
+    work = {u: p.units(offsets, u) for u in range(p.info("units"))}
+    split = [u for u, w in work.items() if w and w[0][0] < 0]
+    assert len(split) > 3 and max(len(w) for w in work.values()) == 1
+    ws = torch.zeros(p.workspace_size, dtype=torch.uint8, device="cuda")
+    counts_in = ws[:8 * p.info("units") * ctas].view(torch.int64)
+    stream = torch.cuda.current_stream()
+    A.copy_(normal((R, K), dt, 1))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run(A, Bm, C, offs, ws, torch.cuda.current_stream())
+    for n, unit in enumerate((split[0], split[-1], split[len(split) // 2])):
+        p.set_option(B.GEMM_GROUPED_OPT_INJECT_GIVE_UP, unit)
+        for _ in range(n):
+            graph.replay()
+        graph.replay()
+        assert p.last_status(stream) == B.GEMM_ERR_TIMEOUT
+        assert p.last_status(stream) == B.GEMM_OK
+        p.set_option(B.GEMM_GROUPED_OPT_INJECT_GIVE_UP, -1)
+        for again in range(3):
+            A.copy_(normal((R, K), dt, 10 * n + again))  # what the run before left is wrong now
+            want = torch.empty_like(C)
+            p.run(A, Bm, want, offs, torch.zeros_like(ws), stream)
+            C.fill_(7)
+            graph.replay()
+            assert p.last_status(stream) == B.GEMM_OK
+            assert torch.equal(C.view(torch.int16), want.view(torch.int16))
+            assert not bool((counts_in & 0xffff).any())
+    p.close()
+
+
 def test_sorts_of_two_threads_do_not_disturb_each_other():
     """Sorts of different numbers of experts, and so of shared memory, on two
     host threads with a stream each."""
