@@ -1,6 +1,8 @@
 """A mixture-of-experts layer on the library's operators, as a program would
 call them: a router, the experts' two products around an activation, and the
-gradients of all of it.
+gradients of the experts' part: to its input, to the choices' weights and to the
+experts' matrices.  The router's own gradient is not here; it starts from that
+of the weights.
 
     python -m persistent_stream_matmul_gb300.moe_layer          # train step and decode, timed
 
@@ -20,19 +22,48 @@ from . import _binding as B
 _DTYPES = {torch.float16: B.GEMM_F16, torch.bfloat16: B.GEMM_BF16}
 
 
+def _check(name, t, shape, dtypes, device):
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device:
+        have = "%s %s on %s" % (t.dtype, tuple(t.shape), t.device) if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError("%s: %s %s on %s needed, not %s" % (name, " or ".join(map(str, dtypes)), shape, device, have))
+
+
+def _contiguous(name, t, shape, dtypes, device):
+    _check(name, t, shape, dtypes, device)
+    if not t.is_contiguous():
+        raise ValueError("%s: a contiguous tensor needed" % name)
+
+
+def _leading(name, t, shape, dtypes, device):
+    """The leading dimension of a matrix whose rows are contiguous."""
+    _check(name, t, shape, dtypes, device)
+    rows, cols = shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError("%s: contiguous rows needed, not strides %s" % (name, t.stride()))
+    return t.stride(0) if rows > 1 else cols
+
+
 class MoELayer:
     """``experts`` experts of ``up`` (hidden -> inner), ReLU, ``down`` (inner -> hidden); each
     token goes to ``topk`` of them.  Weights are in the layout of a linear layer: router
     (experts, hidden), up (experts, inner, hidden), down (experts, hidden, inner).  hidden, inner
     and experts are multiples of 8.  One instance serves one number of tokens, on the current
-    stream; its plans and workspaces are made once."""
+    stream of the device that holds the weights; its plans and workspaces are made once.  Operands
+    of another shape, type or device are refused with a ValueError."""
 
     def __init__(self, tokens, topk, router, up, down):
+        if not isinstance(up, torch.Tensor) or up.dim() != 3 or up.dtype not in _DTYPES or not up.is_cuda:
+            raise ValueError("up: a 16-bit (experts, inner, hidden) tensor on the GPU needed")
         experts, inner, hidden = up.shape
         self.tokens, self.topk, self.experts = tokens, topk, experts
         self.hidden, self.inner = hidden, inner
         self.router, self.up, self.down = router, up, down
         self.dtype, self.code, dev = up.dtype, _DTYPES[up.dtype], up.device
+        self.device, self.saved = dev, None
+        for name, t, shape in (("router", router, (experts, hidden)), ("up", up, tuple(up.shape)),
+                               ("down", down, (experts, hidden, inner))):
+            _contiguous(name, t, shape, (self.dtype,), dev)
+        self._stream()
         slots = tokens * topk
         rows, col, row = B.GEMM_GROUPED_ROWS, B.GEMM_COL_MAJOR, B.GEMM_ROW_MAJOR
         self.router_plan = B.Plan(tokens, experts, hidden, self.code, row, col, "auto")
@@ -54,21 +85,33 @@ class MoELayer:
     def _new(self, *shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.up.device)
 
+    def _stream(self):
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError("the current device is not the layer's, %s" % self.device)
+        return torch.cuda.current_stream()
+
     def route(self, x):
-        """(choices, weights) of every token: top-k of the router's logits, their softmax."""
+        """(choices, weights) of every token: top-k of the router's logits, which the product
+        rounds to the layer's type, and their softmax."""
+        stream = self._stream()
+        _check("x", x, (self.tokens, self.hidden), (self.dtype,), self.device)
         logits = self._new(self.tokens, self.experts)
-        self.router_plan.run(x, self.router, logits, self.router_workspace, torch.cuda.current_stream())
+        self.router_plan.run(x.contiguous(), self.router, logits, self.router_workspace, stream)
         top, ids = torch.topk(logits.float(), self.topk, dim=1)
         return ids, torch.softmax(top, dim=1)
 
     def forward(self, x, ids, weights):
-        """y for x (tokens, hidden), choices (int64; outside the experts: dropped) and fp32 weights;
-        what the gradient needs is kept in ``self.saved``."""
-        T, k, E, H, stream = self.tokens, self.topk, self.experts, self.hidden, torch.cuda.current_stream()
+        """y for x (tokens, hidden), choices (int32 or int64, of any row stride, as x; outside the
+        experts: dropped) and fp32 weights; what the gradient needs is kept in ``self.saved``."""
+        T, k, E, H, stream = self.tokens, self.topk, self.experts, self.hidden, self._stream()
+        ldx = _leading("x", x, (T, H), (self.dtype,), self.device)
+        ld_ids = _leading("ids", ids, (T, k), (torch.int64, torch.int32), self.device)
+        _contiguous("weights", weights, (T, k), (torch.float32,), self.device)
+        index = B.GEMM_INDEX_I64 if ids.dtype == torch.int64 else B.GEMM_INDEX_I32
         offsets, rows, slots = (self._new(n, dtype=torch.int32) for n in (E + 1, T * k, T * k))
-        B.gemm_moe_sort(ids, B.GEMM_INDEX_I64, k, T, k, E, offsets, rows, slots, self.workspace, stream)
+        B.gemm_moe_sort(ids, index, ld_ids, T, k, E, offsets, rows, slots, self.workspace, stream)
         xs = self._new(T * k, H)
-        B.gemm_moe_dispatch(x, H, rows, slots, T, k, H, self.code, xs, H, stream)
+        B.gemm_moe_dispatch(x, ldx, rows, slots, T, k, H, self.code, xs, H, stream)
         a = self._new(T * k, self.inner)
         self.up_plan.run(xs, self.up, a, offsets, self.workspace, stream)
         a.relu_()
@@ -81,10 +124,13 @@ class MoELayer:
 
     def backward(self, dy):
         """(dx, dweights, dup, ddown) of the last forward."""
-        T, k, H, stream = self.tokens, self.topk, self.hidden, torch.cuda.current_stream()
+        if self.saved is None:
+            raise RuntimeError("backward before forward")
+        T, k, H, stream = self.tokens, self.topk, self.hidden, self._stream()
+        lddy = _leading("dy", dy, (T, H), (self.dtype,), self.device)
         offsets, rows, slots, weights, xs, a, ys = self.saved
         dys, dweights = self._new(T * k, H), self._new(T, k, dtype=torch.float32)
-        B.gemm_moe_combine_grad(dy, H, ys, H, rows, slots, weights, T, k, H, self.code, dys, H, dweights, stream)
+        B.gemm_moe_combine_grad(dy, lddy, ys, H, rows, slots, weights, T, k, H, self.code, dys, H, dweights, stream)
         ddown = torch.empty_like(self.down)
         self.down_grad.run(a, dys, ddown, offsets, self.workspace, stream)
         da = self._new(T * k, self.inner)

@@ -66,3 +66,13 @@ def test_give_up_hook_refusals():
             plan.set_option(B.GEMM_GROUPED_OPT_INJECT_GIVE_UP, value)
         assert e.value.status == status
     plan.close()
+
+
+def test_layer_refuses_weights_that_are_not_on_a_gpu():
+    import torch
+
+    from persistent_stream_matmul_gb300.moe_layer import MoELayer
+    w = torch.zeros(8, 16, 24, dtype=torch.float16)
+    for up in (w, w.float(), None):
+        with pytest.raises(ValueError):
+            MoELayer(4, 2, torch.zeros(8, 24, dtype=torch.float16), up, torch.zeros(8, 24, 16, dtype=torch.float16))
