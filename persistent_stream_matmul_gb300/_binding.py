@@ -123,17 +123,25 @@ def load(path: str = LIB_PATH):
 
 
 def _addr(x) -> int | None:
+    if x is None or type(x) is int:
+        return x
     try:
         return x.data_ptr()
     except AttributeError:
-        return x  # an address or None
+        if isinstance(x, int):
+            return x
+        raise  # ctypes would take bytes and str as host pointers
 
 
 def _stream(s) -> int | None:
+    if s is None or type(s) is int:
+        return s
     try:
         return s.cuda_stream
     except AttributeError:
-        return s  # a handle or None
+        if isinstance(s, int):
+            return s
+        raise
 
 
 def _check(st: int, where: str):

@@ -76,3 +76,17 @@ def test_layer_refuses_weights_that_are_not_on_a_gpu():
     for up in (w, w.float(), None):
         with pytest.raises(ValueError):
             MoELayer(4, 2, torch.zeros(8, 24, dtype=torch.float16), up, torch.zeros(8, 24, 16, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("bad", [b"host bytes", "text", 1.5, bytearray(8), ctypes.c_char_p(b"x"), object()])
+def test_operands_that_are_no_addresses_are_refused(bad):
+    """ctypes takes bytes and str as pointers to host memory."""
+    P = 0x1000
+    with pytest.raises((AttributeError, TypeError)):
+        B.gemm_moe_combine(bad, 16, P, P, 0, 2, 16, 1, P, 16)  # no tokens: nothing would be read
+    with pytest.raises((AttributeError, TypeError)):
+        B.gemm_moe_combine(P, 16, P, P, 0, 2, 16, 1, P, 16, bad)
+    plan = B.Plan(0, 8, 8, B.GEMM_BF16, B.GEMM_ROW_MAJOR, B.GEMM_ROW_MAJOR, "dp", offline_sms=152)
+    with pytest.raises((AttributeError, TypeError)):
+        plan.run(P, bad, P)
+    plan.close()
