@@ -140,7 +140,8 @@ enum {
     GEMM_GROUPED_INFO_TILE_M = 3,  /* tile extent along C's contiguous dimension */
     GEMM_GROUPED_INFO_TILE_N = 4,  /* the largest extent along the other one */
     GEMM_GROUPED_INFO_STAGES = 5,  /* depth of the shared-memory ring */
-    GEMM_GROUPED_INFO_SMEM_BYTES = 6
+    GEMM_GROUPED_INFO_SMEM_BYTES = 6,
+    GEMM_GROUPED_INFO_GROUPS = 7
 };
 
 /*

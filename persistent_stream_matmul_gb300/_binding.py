@@ -53,7 +53,7 @@ GEMM_INDEX_I32, GEMM_INDEX_I64 = 0, 1
 GEMM_GROUPED_ROWS, GEMM_GROUPED_INNER = 0, 1
 GEMM_MOE_MAX_EXPERTS = 1024
 GEMM_GROUPED_OPT_CTAS, GEMM_GROUPED_OPT_INJECT_GIVE_UP = 1, 3
-GROUPED_INFO = {"ctas": 1, "units": 2, "tile_m": 3, "tile_n": 4, "stages": 5, "smem_bytes": 6}
+GROUPED_INFO = {"ctas": 1, "units": 2, "tile_m": 3, "tile_n": 4, "stages": 5, "smem_bytes": 6, "groups": 7}
 
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3
 TRACE_STAMPS = 6   # uint64 per CTA written by gemm_plan_set_trace: 4 timer + 2 clock stamps
@@ -371,7 +371,10 @@ def gemm_grouped_plan_get_info(plan, key) -> int:
 
 def gemm_grouped_plan_units(plan, offsets, unit: int):
     """[(tile, group, tile along C's rows, first row, rows, width, k0, k1, k-blocks), ...] of
-    scheduling unit ``unit`` for host offsets."""
+    scheduling unit ``unit`` for host offsets, one more than the plan has groups."""
+    if len(offsets) != gemm_grouped_plan_get_info(plan, "groups") + 1:
+        raise ValueError("gemm_grouped_plan_units: %d offsets for %d groups"
+                         % (len(offsets), gemm_grouped_plan_get_info(plan, "groups")))
     off = (ctypes.c_int32 * len(offsets))(*[int(x) for x in offsets])
     n = ctypes.c_int64()
     _check(load().gemm_grouped_plan_units(plan, off, unit, None, 0, ctypes.byref(n)),

@@ -311,6 +311,7 @@ gemm_status_t gemm_grouped_plan_get_info(gemm_grouped_plan_t p, int key, int64_t
         case GEMM_GROUPED_INFO_TILE_N: *value = p->shape.tile_n; break;
         case GEMM_GROUPED_INFO_STAGES: *value = GroupedCfg<true>::STAGES; break;
         case GEMM_GROUPED_INFO_SMEM_BYTES: *value = smem_of(p->ctas); break;
+        case GEMM_GROUPED_INFO_GROUPS: *value = p->groups; break;
         default: return GEMM_ERR_INVALID_ARG;
     }
     return GEMM_OK;

@@ -90,3 +90,13 @@ def test_operands_that_are_no_addresses_are_refused(bad):
     with pytest.raises((AttributeError, TypeError)):
         plan.run(P, bad, P)
     plan.close()
+
+
+def test_offsets_for_another_number_of_groups_are_refused():
+    """The library reads one offset more than the plan has groups."""
+    plan = B.GroupedPlan(B.GEMM_GROUPED_ROWS, 4, 100, 64, 64, B.GEMM_BF16, B.GEMM_ROW_MAJOR, offline_sms=152)
+    assert plan.info("groups") == 4 and plan.units([0, 1, 2, 3, 4], 0)
+    for offsets in ([], [0], [0, 1, 2, 3], [0, 1, 2, 3, 4, 5]):
+        with pytest.raises(ValueError):
+            plan.units(offsets, 0)
+    plan.close()
