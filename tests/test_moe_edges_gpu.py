@@ -174,6 +174,34 @@ def test_replays_after_a_timeout(kind, ctas):
     p.close()
 
 
+@pytest.mark.parametrize("id_type", [torch.int32, torch.int64])
+@pytest.mark.parametrize("T,k,E", [(131072, 8, 64), (131073, 8, 256), (300001, 5, 1000), (1200003, 1, 3), (2 ** 22 + 1, 4, 1024)])
+def test_sorts_of_more_than_a_million_slots(T, k, E, id_type):
+    """From 1048577 slots on a warp takes its part in several batches, the last
+    block's some in one and some in none."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    n, pad = T * k, 3
+    ids = (torch.rand((T, k + pad), generator=g, device="cuda") ** 3 * E).to(id_type).clamp_(max=E - 1)
+    ids[torch.rand((T, k + pad), generator=g, device="cuda") < 0.1] = -1
+    ids[::7, 0] = E
+    key = ids[:, :k].reshape(-1).long()
+    kept = (key >= 0) & (key < E)
+    order = torch.sort(torch.where(kept, key, E), stable=True).indices
+    total = int(kept.sum())
+    counts = torch.bincount(key[kept], minlength=E)
+    offsets, rows, slots = (Rows(1, m, torch.int32) for m in (E + 1, n, n))
+    ws = torch.randint(0, 256, (B.gemm_moe_sort_workspace_size(T, k, E),), dtype=torch.uint8, device="cuda")
+    B.gemm_moe_sort(ids, B.GEMM_INDEX_I64 if id_type == torch.int64 else B.GEMM_INDEX_I32, k + pad, T, k, E,
+                    offsets, rows, slots, ws, torch.cuda.current_stream())
+    assert torch.equal(offsets.view[0, 1:].long(), counts.cumsum(0)) and int(offsets.view[0, 0]) == 0
+    assert torch.equal(slots.view[0, :total].long(), order[:total]) and bool((slots.view[0, total:] == -1).all())
+    want = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    want[order[:total]] = torch.arange(total, device="cuda")
+    assert torch.equal(rows.view[0].long(), want)
+    for o in (offsets, rows, slots):
+        o.check_guards()
+
+
 def test_sorts_of_two_threads_do_not_disturb_each_other():
     """Sorts of different numbers of experts, and so of shared memory, on two
     host threads with a stream each."""
