@@ -191,8 +191,9 @@ gemm_status_t gemm_grouped_plan_get_info(gemm_grouped_plan_t plan, int key, int6
 gemm_status_t gemm_grouped_plan_units(gemm_grouped_plan_t plan, const int32_t *offsets, int64_t unit,
                                       int32_t *units, int64_t max_units, int64_t *n_units);
 
-/* Bytes of device workspace gemm_grouped_run needs (may be 0).  Its contents
- * need no initialisation; two runs that share it must not overlap in time.
+/* Bytes of device workspace gemm_grouped_run needs (may be 0), with the options
+ * set so far (GEMM_GROUPED_OPT_CTAS changes it).  Its contents need no
+ * initialisation; two runs that share it must not overlap in time.
  * Errors: INVALID_ARG. */
 gemm_status_t gemm_grouped_workspace_size(gemm_grouped_plan_t plan, size_t *bytes);
 

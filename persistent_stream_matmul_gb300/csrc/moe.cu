@@ -233,8 +233,8 @@ SortArgs sort_shape(int64_t tokens, int64_t topk, int64_t experts) {
 // flight an SM, so U and C are weighed against the registers that B allows:
 // the sum of 2 choices of 16384 tokens of 4096 takes 68 us with U, C, B = 2, 1, 4
 // (5.9 TB/s), 71 with 2, 2, 4, 84 with 4, 1, 4 and 115 with 2, 2, 6, whose
-// registers spill (before the streaming stores below, with which the first
-// takes 63).
+// registers spill in the loop (before the streaming stores below, with which the
+// first takes 63).
 //
 // ALIGNED: every row starts at a 16-byte boundary and its length is a multiple
 // of 8.  Otherwise the chunks are cut at the 16-byte boundaries of the row
@@ -608,9 +608,11 @@ template <typename T>
 gemm_status_t gather(const void* src, int64_t lds, const int32_t* rows, const float* weights,
                      int64_t tokens, int64_t topk, int64_t hidden, void* out, int64_t ldo,
                      gemm_stream_t stream) {
-    // (1 choice: 50 us with this, 54 with the next; 4 choices: 108.9 with this, 109.8
-    // with U = 4, and 54.2 against 57.4 on rows of 1024 with C = 1.  Not aligned,
-    // rows of 2047: 19 us, with U = 2 20.)
+    // us for rows of 4096 unless said.  1 choice: 44.5 with this, though 40 registers
+    // spill 90 bytes a thread, 48.2 with B = 4 (6.9 and 6.7 for 4096 rows of 2048) and
+    // 48.8 with the next.  4 choices: 102.4 with this, 103.2 with U, C = 4, 1 and 103.3
+    // with 2, 1; rows of 1024 52.7, 56.0 and 55.2.  Not aligned, rows of 2047: 19.6,
+    // with U = 2 20.6.
     auto* fn = !aligned_rows(hidden, {src, out}, {lds, ldo}) ? gather_v<T, false, 1, 1, 4>
                : topk == 1                                   ? gather_v<T, true, 1, 2, 6>
                : topk == 2                                   ? gather_v<T, true, 2, 1, 4>

@@ -23,7 +23,7 @@ _DTYPES = {torch.float16: B.GEMM_F16, torch.bfloat16: B.GEMM_BF16}
 
 
 def _check(name, t, shape, dtypes, device):
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype not in dtypes or t.device != device:
         have = "%s %s on %s" % (t.dtype, tuple(t.shape), t.device) if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError("%s: %s %s on %s needed, not %s" % (name, " or ".join(map(str, dtypes)), shape, device, have))
 
