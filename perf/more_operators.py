@@ -318,7 +318,8 @@ def work(case):
 def _to_grid(v, type):
     """The nearest values that the 8-bit type holds, ties to an even last digit."""
     digits, least = (3, -6) if type == "e4m3" else (2, -14)
-    step = torch.ldexp(torch.ones_like(v), (torch.frexp(v).exponent - 1).clamp(min=least) - digits)
+    exponent = (torch.frexp(v).exponent.long() - 1).clamp(min=least) - digits
+    step = ((exponent + 1023) << 52).view(torch.float64)  # 2 to that power, exactly
     return torch.round(v / step) * step
 
 
