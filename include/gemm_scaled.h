@@ -1,0 +1,193 @@
+/*
+ * gemm_scaled.h -- C ABI of the 8-bit linear layer: products of 8-bit floating
+ * point operands with a scale for each 128 elements, the quantisation that
+ * makes such operands, and the root-mean-square norm that hands its rows to
+ * a product in that form.
+ *
+ * An 8-bit operand is a matrix of e4m3 or e5m2 values q and fp32 scales s; the
+ * element that it stands for is q * s.  A scale covers, of the summed dimension,
+ * 128 elements (the last group may be shorter), and of the other dimension
+ *
+ *   GEMM_SCALE_VECTOR  one row or column.  The scales of an operand with R rows
+ *                      or columns and K summed elements are ceil(K / 128) x R:
+ *                      that of row r and group g at s[g * R + r].
+ *   GEMM_SCALE_BLOCK   128 of them.  The scales are a matrix of blocks in the
+ *                      order of the stored values: for values stored as S0 rows of
+ *                      S1 contiguous elements, that of (i, j) at
+ *                      s[(i / 128) * ceil(S1 / 128) + j / 128].
+ *
+ * A linear layer y = x * W^T (x: tokens x in, W: out x in) is
+ *
+ *   gemm_rms_norm (or gemm_scaled_quantize, ROWS)  x -> 8 bits
+ *   gemm_scaled_quantize (BLOCKS)                  W -> 8 bits, once a step
+ *   gemm_scaled_run        y = x W^T:   A = x row-major, B = W column-major
+ *   gemm_scaled_quantize_both                      dy -> 8 bits, along rows and columns
+ *   gemm_scaled_run        dx = dy W:   A = dy row-major, B = W row-major
+ *   gemm_scaled_run        dW = dy^T x: A = dy column-major, B = x row-major, both
+ *                          with vectors along the tokens (COLS)
+ *
+ * Conventions, beyond those of gemm.h (status codes, stream semantics and
+ * dependent launches are the same):
+ *  - The functions without a plan run on the current CUDA device, which must
+ *    be the one that holds their operands.
+ *  - Row matrices have a leading dimension in elements, at least the row
+ *    length; scales, weights and sums are contiguous.  Any alignment of the
+ *    element is accepted; rows at 16-byte boundaries (8-bit: 8) are faster.
+ *  - Inputs and outputs must not overlap, but for the cases named below.
+ *  - Results do not depend on timing (no floating-point atomics).
+ *  - NaN and infinity: a NaN becomes a NaN of its own and counts for no scale;
+ *    a group with an infinity has an infinite scale, so all of it stands for
+ *    NaN.
+ */
+#ifndef PSM_GEMM_SCALED_H
+#define PSM_GEMM_SCALED_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* 8-bit floating point: 4 bits of exponent and 3 of mantissa (largest 448, no
+ * infinity), or 5 and 2 (largest 57344). */
+typedef enum { GEMM_E4M3 = 0, GEMM_E5M2 = 1 } gemm_fp8_t;
+typedef enum { GEMM_SCALE_VECTOR = 0, GEMM_SCALE_BLOCK = 1 } gemm_scale_t;
+
+/* Beside GEMM_F16 and GEMM_BF16, an output type of a scaled product. */
+enum { GEMM_F32 = 2 };
+
+/* Elements that share a scale, along the summed dimension. */
+#define GEMM_SCALE_GROUP 128
+
+/* ---------------------------------------------------------------- quantisation */
+
+typedef enum {
+    GEMM_QUANTIZE_ROWS = 0,   /* vectors along the rows: scales ceil(cols / 128) x rows */
+    GEMM_QUANTIZE_COLS = 1,   /* vectors along the columns: scales ceil(rows / 128) x cols */
+    GEMM_QUANTIZE_BLOCKS = 2  /* blocks: scales ceil(rows / 128) x ceil(cols / 128) */
+} gemm_quantize_t;
+
+/*
+ * q, scales = x (rows x cols, 16-bit) in 8 bits.  With L the type's largest value
+ * and m the largest magnitude of a group, at least 2^-100, the group's scale is
+ * m / L (rounded to fp32) and q the 8-bit value nearest to x * L / m, ties to even.
+ * Errors: INVALID_ARG (NULL operand, negative size, a leading dimension below
+ * cols, bad enum), UNSUPPORTED (rows or cols > 2^31 - 1024, an operand not aligned
+ * to its element), LAUNCH.  rows == 0 or cols == 0: nothing is written.
+ */
+gemm_status_t gemm_scaled_quantize(gemm_quantize_t kind, const void *x, int64_t ldx, int64_t rows,
+                                   int64_t cols, gemm_dtype_t dtype, gemm_fp8_t type, void *q,
+                                   int64_t ldq, float *scales, gemm_stream_t stream);
+
+/* ROWS and COLS of one matrix, which is read once.  Errors: as above. */
+gemm_status_t gemm_scaled_quantize_both(const void *x, int64_t ldx, int64_t rows, int64_t cols,
+                                        gemm_dtype_t dtype, gemm_fp8_t type, void *q_rows,
+                                        int64_t ldq_rows, float *scales_rows, void *q_cols,
+                                        int64_t ldq_cols, float *scales_cols, gemm_stream_t stream);
+
+/* ---------------------------------------------------------------- norm */
+
+/*
+ * Root-mean-square norm of each row, after the residual's addition:
+ *
+ *   s = x + residual, rounded to the 16-bit type (x where residual is NULL)
+ *   rstd = 1 / sqrt(mean of s^2 + eps)
+ *   y = s * rstd * weight, in fp32
+ *
+ * x, residual, sum, y: rows x hidden of `dtype`; weight: hidden of `dtype`.
+ * Outputs, each written unless it is NULL (one of y and q at least is needed):
+ * sum = s (may be x or residual, with its leading dimension); y rounded to
+ * `dtype`; q and scales, y in 8 bits as GEMM_QUANTIZE_ROWS makes it from fp32; rstd,
+ * rows of fp32, for the gradient.  q and scales come together.
+ * Errors: INVALID_ARG (NULL x or weight, both y and q NULL, one of q and scales
+ * without the other, sum without residual, negative size, negative or NaN eps, a
+ * leading dimension of a given operand below hidden, bad enum), UNSUPPORTED
+ * (hidden > GEMM_NORM_MAX_HIDDEN, rows > 2^31 - 1024, an operand not aligned to its
+ * element), LAUNCH.  rows == 0 or hidden == 0: nothing is written.
+ */
+#define GEMM_NORM_MAX_HIDDEN 65536
+gemm_status_t gemm_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                            const void *weight, float eps, int64_t rows, int64_t hidden,
+                            gemm_dtype_t dtype, void *sum, int64_t ldsum, void *y, int64_t ldy,
+                            void *q, int64_t ldq, gemm_fp8_t type, float *scales, float *rstd,
+                            gemm_stream_t stream);
+
+/* Bytes of device workspace gemm_rms_norm_grad needs.  Its contents need no
+ * initialisation.  Errors: as gemm_rms_norm for the sizes, INVALID_ARG for a
+ * NULL bytes. */
+gemm_status_t gemm_rms_norm_grad_workspace_size(int64_t rows, int64_t hidden, size_t *bytes);
+
+/*
+ * Gradients of the norm for dy (rows x hidden), with s and rstd as the norm wrote
+ * them and n = s * rstd:
+ *
+ *   dx = rstd * (weight * dy - n * mean(weight * dy * n)) + dsum
+ *   dweight = the sum over the rows of dy * n
+ *
+ * dsum is the gradient that reaches s by the residual stream (NULL: none); dx,
+ * rounded to `dtype`, is the gradient to x and to residual alike, and may be dy or
+ * dsum, with its leading dimension.  dweight: hidden of fp32, written in full; NULL
+ * where it is not wanted.
+ * Errors: as gemm_rms_norm (NULL dy, s, weight, rstd or dx), WORKSPACE (NULL or
+ * not 16-byte aligned while dweight is given).  rows == 0: only dweight is written,
+ * as zeros.  hidden == 0: nothing is written.
+ */
+gemm_status_t gemm_rms_norm_grad(const void *dy, int64_t lddy, const void *s, int64_t lds,
+                                 const void *weight, const float *rstd, const void *dsum,
+                                 int64_t lddsum, int64_t rows, int64_t hidden, gemm_dtype_t dtype,
+                                 void *dx, int64_t lddx, float *dweight, void *workspace,
+                                 gemm_stream_t stream);
+
+/* ---------------------------------------------------------------- scaled products */
+
+typedef struct gemm_scaled_plan *gemm_scaled_plan_t;
+
+/*
+ * Create a plan for C = A * B on the current device, where
+ *
+ *   C[m][n] = the sum over the groups g of k of
+ *             sa(m, g) * sb(n, g) * (the sum over k in g of A[m][k] * B[k][n])
+ *
+ * A is M x K and B is K x N, of the 8-bit types type_a and type_b, in layout_a and
+ * layout_b; each with the kind of scales given.  C is M x N row-major of out_dtype
+ * (GEMM_F16, GEMM_BF16 or GEMM_F32), rounded once.  Sums are in fp32: within a
+ * group by the tensor cores, over the groups in ascending order.
+ * The contiguous dimension of A and of B must be a multiple of 16.  A plan is
+ * not thread-safe.
+ * Errors: INVALID_ARG (NULL out, negative size, bad enum), UNSUPPORTED (a size >
+ * 2^31 - 1024, a contiguous dimension that is no multiple of 16, 2^31 tiles or
+ * more), NO_DEVICE, CUDA.
+ */
+gemm_status_t gemm_scaled_plan_create(gemm_scaled_plan_t *out, int64_t M, int64_t N, int64_t K,
+                                      gemm_fp8_t type_a, gemm_fp8_t type_b, int out_dtype,
+                                      gemm_layout_t layout_a, gemm_layout_t layout_b,
+                                      gemm_scale_t scale_a, gemm_scale_t scale_b);
+
+/* Bytes of device workspace gemm_scaled_run needs (may be 0).  Its contents need no
+ * initialisation; two runs that share it must not overlap in time.
+ * Errors: INVALID_ARG. */
+gemm_status_t gemm_scaled_workspace_size(gemm_scaled_plan_t plan, size_t *bytes);
+
+/*
+ * Run the product on `stream`, asynchronously.  A and B must be 16-byte aligned;
+ * C any alignment of its element (16 bytes and N a multiple of 8, 4 for fp32, are
+ * faster).  K == 0: C is +0.
+ * Errors: INVALID_ARG (NULL plan, or a NULL operand that is not empty),
+ * UNSUPPORTED (alignment), WORKSPACE (NULL or not 16-byte aligned while one is
+ * needed), CUDA, LAUNCH.
+ */
+gemm_status_t gemm_scaled_run(gemm_scaled_plan_t plan, const void *A, const float *scales_a,
+                              const void *B, const float *scales_b, void *C, void *workspace,
+                              gemm_stream_t stream);
+
+/* As gemm_last_status, for a scaled plan. */
+gemm_status_t gemm_scaled_last_status(gemm_scaled_plan_t plan, gemm_stream_t stream);
+
+/* Free the plan.  NULL is accepted.  Always returns GEMM_OK. */
+gemm_status_t gemm_scaled_plan_destroy(gemm_scaled_plan_t plan);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PSM_GEMM_SCALED_H */

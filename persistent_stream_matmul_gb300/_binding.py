@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/gemm.h and include/gemm_moe.h.
+"""ctypes binding of the C ABI in include/gemm.h, gemm_moe.h and gemm_scaled.h.
 
 Argument marshalling only: every step of the product runs in the CUDA
 library.  The functions keep the C names; a non-OK status raises GemmError.
@@ -55,11 +55,19 @@ GEMM_MOE_MAX_EXPERTS = 1024
 GEMM_GROUPED_OPT_CTAS, GEMM_GROUPED_OPT_INJECT_GIVE_UP = 1, 3
 GROUPED_INFO = {"ctas": 1, "units": 2, "tile_m": 3, "tile_n": 4, "stages": 5, "smem_bytes": 6, "groups": 7}
 
+GEMM_E4M3, GEMM_E5M2 = 0, 1
+GEMM_F32 = 2                       # an output type of scaled products only
+GEMM_SCALE_VECTOR, GEMM_SCALE_BLOCK = 0, 1
+GEMM_SCALE_GROUP = 128
+GEMM_QUANTIZE_ROWS, GEMM_QUANTIZE_COLS, GEMM_QUANTIZE_BLOCKS = 0, 1, 2
+GEMM_NORM_MAX_HIDDEN = 65536
+
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3
 TRACE_STAMPS = 6   # uint64 per CTA written by gemm_plan_set_trace: 4 timer + 2 clock stamps
 
 # every entry point of the headers: name -> (restype, argtypes)
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_f32 = ctypes.c_float
 _pp = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = {
     "gemm_plan_create": (_i32, [_pp, _i64, _i64, _i64, _i32, _i32, _i32, _i32]),
@@ -94,6 +102,17 @@ SIGNATURES = {
     "gemm_grouped_run": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "gemm_grouped_last_status": (_i32, [_vp, _vp]),
     "gemm_grouped_plan_destroy": (_i32, [_vp]),
+    "gemm_scaled_quantize": (_i32, [_i32, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp]),
+    "gemm_scaled_quantize_both": (_i32, [_vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
+    "gemm_rms_norm": (_i32, [_vp, _i64, _vp, _i64, _vp, _f32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                             _vp, _vp, _vp]),
+    "gemm_rms_norm_grad_workspace_size": (_i32, [_i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "gemm_rms_norm_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp]),
+    "gemm_scaled_plan_create": (_i32, [_pp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "gemm_scaled_workspace_size": (_i32, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
+    "gemm_scaled_run": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gemm_scaled_last_status": (_i32, [_vp, _vp]),
+    "gemm_scaled_plan_destroy": (_i32, [_vp]),
 }
 
 _lib = None
@@ -441,6 +460,102 @@ class GroupedPlan:
     def close(self):
         if getattr(self, "handle", None):
             gemm_grouped_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def gemm_scaled_quantize(kind, x, ldx, rows, cols, dtype, type, q, ldq, scales, stream=None):
+    _check(load().gemm_scaled_quantize(kind, _addr(x), ldx, rows, cols, dtype, type, _addr(q), ldq, _addr(scales),
+                                       _stream(stream)), "gemm_scaled_quantize")
+
+
+def gemm_scaled_quantize_both(x, ldx, rows, cols, dtype, type, q_rows, ldq_rows, scales_rows, q_cols, ldq_cols,
+                              scales_cols, stream=None):
+    _check(load().gemm_scaled_quantize_both(_addr(x), ldx, rows, cols, dtype, type, _addr(q_rows), ldq_rows,
+                                            _addr(scales_rows), _addr(q_cols), ldq_cols, _addr(scales_cols),
+                                            _stream(stream)), "gemm_scaled_quantize_both")
+
+
+def gemm_rms_norm(x, ldx, residual, ldres, weight, eps, rows, hidden, dtype, sum, ldsum, y, ldy, q, ldq, type, scales,
+                  rstd, stream=None):
+    _check(load().gemm_rms_norm(_addr(x), ldx, _addr(residual), ldres, _addr(weight), eps, rows, hidden, dtype,
+                                _addr(sum), ldsum, _addr(y), ldy, _addr(q), ldq, type, _addr(scales), _addr(rstd),
+                                _stream(stream)), "gemm_rms_norm")
+
+
+def gemm_rms_norm_grad_workspace_size(rows, hidden) -> int:
+    v = ctypes.c_size_t()
+    _check(load().gemm_rms_norm_grad_workspace_size(rows, hidden, ctypes.byref(v)),
+           "gemm_rms_norm_grad_workspace_size")
+    return v.value
+
+
+def gemm_rms_norm_grad(dy, lddy, s, lds, weight, rstd, dsum, lddsum, rows, hidden, dtype, dx, lddx, dweight,
+                       workspace=None, stream=None):
+    _check(load().gemm_rms_norm_grad(_addr(dy), lddy, _addr(s), lds, _addr(weight), _addr(rstd), _addr(dsum), lddsum,
+                                     rows, hidden, dtype, _addr(dx), lddx, _addr(dweight), _addr(workspace),
+                                     _stream(stream)), "gemm_rms_norm_grad")
+
+
+def gemm_scaled_plan_create(M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b) -> int:
+    h = ctypes.c_void_p()
+    _check(load().gemm_scaled_plan_create(ctypes.byref(h), M, N, K, type_a, type_b, out_dtype, layout_a, layout_b,
+                                          scale_a, scale_b), "gemm_scaled_plan_create")
+    return h.value
+
+
+def gemm_scaled_workspace_size(plan) -> int:
+    v = ctypes.c_size_t()
+    _check(load().gemm_scaled_workspace_size(plan, ctypes.byref(v)), "gemm_scaled_workspace_size")
+    return v.value
+
+
+def gemm_scaled_run(plan, A, scales_a, B, scales_b, C, workspace=None, stream=None):
+    _check(load().gemm_scaled_run(plan, _addr(A), _addr(scales_a), _addr(B), _addr(scales_b), _addr(C),
+                                  _addr(workspace), _stream(stream)), "gemm_scaled_run")
+
+
+def gemm_scaled_last_status(plan, stream=None) -> int:
+    """Returns the status code (GEMM_OK or GEMM_ERR_TIMEOUT ...); does not raise."""
+    return int(load().gemm_scaled_last_status(plan, _stream(stream)))
+
+
+def gemm_scaled_plan_destroy(plan):
+    _check(load().gemm_scaled_plan_destroy(plan), "gemm_scaled_plan_destroy")
+
+
+class ScaledPlan:
+    """Owning wrapper around a scaled plan handle (marshalling only)."""
+
+    def __init__(self, M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b):
+        self.M, self.N, self.K = M, N, K
+        self.out_dtype = out_dtype
+        self.handle = gemm_scaled_plan_create(M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b)
+
+    @property
+    def workspace_size(self) -> int:
+        return gemm_scaled_workspace_size(self.handle)
+
+    def run(self, A, scales_a, B, scales_b, C, workspace=None, stream=None):
+        gemm_scaled_run(self.handle, A, scales_a, B, scales_b, C, workspace, stream)
+
+    def last_status(self, stream=None) -> int:
+        return gemm_scaled_last_status(self.handle, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            gemm_scaled_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -1,0 +1,658 @@
+// The 8-bit linear layer's row operators of include/gemm_scaled.h: quantisation
+// and the root-mean-square norm with its gradient.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "gemm_scaled.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+using namespace psm;
+
+namespace {
+
+constexpr int GROUP = GEMM_SCALE_GROUP;
+constexpr float LEAST = 0x1p-100f;  // least magnitude that a scale is made from
+
+// ---------------------------------------------------------------- 8 bits
+template <bool E5M2>
+struct Fp8 {
+    static constexpr float LARGEST = E5M2 ? 57344.f : 448.f;
+    static constexpr __nv_fp8_interpretation_t KIND = E5M2 ? __NV_E5M2 : __NV_E4M3;
+};
+
+// The scale of a group whose largest magnitude is m, and what its elements are
+// multiplied by.
+template <bool E5M2>
+__device__ __forceinline__ float scale_of(float m) { return __fdiv_rn(fmaxf(m, LEAST), Fp8<E5M2>::LARGEST); }
+template <bool E5M2>
+__device__ __forceinline__ float inverse_of(float m) { return __fdiv_rn(Fp8<E5M2>::LARGEST, fmaxf(m, LEAST)); }
+
+// Eight 8-bit values nearest to x * L / m.  x * fl(L / m) is within 2^-23 of
+// that, which could lift a quotient off a border between two 8-bit values or onto
+// the other side, and between 16-bit x and m quotients on a border are common
+// (0.3 % of normal bf16 values).  But those that are not on a border t (5 bits) are
+// 2^-16 away from it at least: x L / m - t is a whole multiple of 1 / m over t
+// of 5 bits and m of 11.  So EXACT rounds the product to 20 bits first, which
+// puts it back on the border it came from and moves no other across.
+template <bool E5M2, bool EXACT>
+__device__ __forceinline__ uint2 quantized(const float (&x)[8], float inverse) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t pair[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[i] = __fmul_rn(x[4 * h + 2 * j + i], inverse);
+                if constexpr (EXACT) {  // the leading part of a splitting by 2^4 + 1
+                    const float c = __fmul_rn(v[i], 17.f);
+                    v[i] = __fsub_rn(c, __fsub_rn(c, v[i]));
+                }
+            }
+            pair[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, Fp8<E5M2>::KIND);
+        }
+        w[h] = pair[0] | (pair[1] << 16);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Elements h .. h + 7 of a row of n to memory; ALIGNED: all of them, at once.
+template <bool ALIGNED>
+__device__ __forceinline__ void store_quantized(uint8_t* row, int h, int n, uint2 q) {
+    if constexpr (ALIGNED) {
+        *reinterpret_cast<uint2*>(row + h) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (h + i < n) row[h + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    }
+}
+
+template <bool ALIGNED>
+__device__ __forceinline__ void store_16bit(uint16_t* row, int h, int n, const Chunk& c) {
+    if constexpr (ALIGNED) {
+        *reinterpret_cast<uint4*>(row + h) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (h + i < n) row[h + i] = (uint16_t)(c.w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// Elements h .. h + 7 of a row of n as fp32, zeros past its end.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void load_row(const uint16_t* row, int h, int n, float (&x)[8]) {
+    unpack<T>(load_chunk<ALIGNED>(row, h, n), x);
+    if constexpr (!ALIGNED)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (h + i >= n) x[i] = 0.f;
+}
+
+__device__ __forceinline__ float magnitude(const float (&x)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    return m;
+}
+
+// The largest over the 16 lanes that share a row's group.
+__device__ __forceinline__ float over_half(float m) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// ---------------------------------------------------------------- quantisation
+struct QuantizeArgs {
+    const uint16_t* x;
+    int64_t ldx, rows;
+    int cols, row_groups;  // row_groups: groups of a row
+    uint8_t* q;            // ROWS, or COLS / BLOCKS alone
+    int64_t ldq;
+    float* scales;
+    uint8_t* q_cols;       // BOTH: the columns' form
+    int64_t ldq_cols;
+    float* scales_cols;
+};
+
+// Vectors along the rows: 16 lanes a group, a block takes R rows and its 16 / R
+// half-warps a row, U groups each.
+template <typename T, bool E5M2, bool ALIGNED, int R, int U>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    constexpr int ACROSS = 16 / R;
+    const int strips = (a.row_groups + ACROSS * U - 1) / (ACROSS * U);
+    const int64_t row = (int64_t)(blockIdx.x / strips) * R + half % R;
+    const int g0 = (blockIdx.x % strips) * ACROSS * U + half / R;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float x[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = (g0 + u * ACROSS) * GROUP + lane * 8;
+        if (row < a.rows && h < a.cols) load_row<T, ALIGNED>(a.x + row * a.ldx, h, a.cols, x[u]);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int g = g0 + u * ACROSS, h = g * GROUP + lane * 8;
+        const float m = over_half(magnitude(x[u]));
+        if (row >= a.rows || h >= a.cols) continue;
+        store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x[u], inverse_of<E5M2>(m)));
+        if (lane == 0) a.scales[(int64_t)g * a.rows + row] = scale_of<E5M2>(m);
+    }
+}
+
+// Tiles of 128 x 128: vectors along the columns, a block, or vectors along both
+// dimensions.  A thread has eight columns of eight rows, 16 apart.
+template <typename T, bool E5M2, bool ALIGNED, int KIND, bool BOTH>
+__global__ void __launch_bounds__(256) quantize_tile_kernel(QuantizeArgs a) {
+    __shared__ float part[8][GROUP];
+    const int lane = threadIdx.x & 15, r = threadIdx.x >> 4, warp = threadIdx.x >> 5;
+    const int64_t tile_row = blockIdx.x / a.row_groups;
+    const int tile_col = blockIdx.x % a.row_groups;
+    const int h = tile_col * GROUP + lane * 8;
+    const int64_t row0 = tile_row * GROUP + r;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    Chunk c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = row0 + 16 * i;
+        if (row < a.rows && h < a.cols) c[i] = load_chunk<ALIGNED>(a.x + row * a.ldx, h, a.cols);
+        else c[i] = Chunk{};
+    }
+    float col[8] = {};  // the largest magnitude of each of this thread's columns
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float x[8];
+        unpack<T>(c[i], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!ALIGNED && h + j >= a.cols) x[j] = 0.f;
+            col[j] = fmaxf(col[j], fabsf(x[j]));
+        }
+        if constexpr (BOTH) {
+            const int64_t row = row0 + 16 * i;
+            const float m = over_half(magnitude(x));
+            if (row < a.rows && h < a.cols) {
+                store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x, inverse_of<E5M2>(m)));
+                if (lane == 0) a.scales[(int64_t)tile_col * a.rows + row] = scale_of<E5M2>(m);
+            }
+        }
+    }
+    if constexpr (KIND == GEMM_QUANTIZE_BLOCKS) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, col[j]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((threadIdx.x & 31) == 0) part[0][warp] = m;
+        __syncthreads();
+        m = part[0][threadIdx.x & 7];
+#pragma unroll
+        for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (threadIdx.x == 0) a.scales[tile_row * a.row_groups + tile_col] = scale_of<E5M2>(m);
+        const float inverse = inverse_of<E5M2>(m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = row0 + 16 * i;
+            float x[8];
+            unpack<T>(c[i], x);
+            if (row < a.rows && h < a.cols) store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x, inverse));
+        }
+    } else {
+        uint8_t* q = BOTH ? a.q_cols : a.q;
+        const int64_t ldq = BOTH ? a.ldq_cols : a.ldq;
+        float* scales = BOTH ? a.scales_cols : a.scales;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            col[j] = fmaxf(col[j], __shfl_xor_sync(0xffffffffu, col[j], 16));
+            if ((threadIdx.x & 16) == 0) part[warp][lane * 8 + j] = col[j];
+        }
+        __syncthreads();
+        if (threadIdx.x < GROUP) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i][threadIdx.x]);
+            const int at = tile_col * GROUP + threadIdx.x;
+            if (at < a.cols) scales[tile_row * a.cols + at] = scale_of<E5M2>(m);
+            part[0][threadIdx.x] = inverse_of<E5M2>(m);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) col[j] = part[0][lane * 8 + j];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = row0 + 16 * i;
+            float x[8];
+            unpack<T>(c[i], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], col[j]);
+            if (row < a.rows && h < a.cols) store_quantized<ALIGNED>(q + row * ldq, h, a.cols, quantized<E5M2, true>(x, 1.f));
+        }
+    }
+}
+
+// Whether rows of 16-bit inputs and 8-bit outputs can be taken in chunks of eight.
+bool whole_chunks(int64_t cols, std::initializer_list<const void*> in, std::initializer_list<int64_t> ld_in,
+                  std::initializer_list<const void*> out, std::initializer_list<int64_t> ld_out) {
+    int64_t bits = cols * 2;
+    for (const void* p : in) bits |= (int64_t)(uintptr_t)p;
+    for (int64_t ld : ld_in) bits |= ld * 2;
+    for (const void* p : out) bits |= (int64_t)(uintptr_t)p * 2;
+    for (int64_t ld : ld_out) bits |= ld * 2;
+    return (bits & 15) == 0;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T, bool E5M2, bool ALIGNED>
+gemm_status_t quantize_v(int kind, bool both, const QuantizeArgs& a, gemm_stream_t stream) {
+    if (kind == GEMM_QUANTIZE_ROWS && !both) {
+        const bool few = a.rows < 8;
+        const int64_t grid = few ? a.rows * cdiv(a.row_groups, 16) : cdiv(a.rows, 8) * cdiv(a.row_groups, 8);
+        if (grid > MAX_INDEX) return GEMM_ERR_UNSUPPORTED;
+        return launch(few ? quantize_rows_kernel<T, E5M2, ALIGNED, 1, 1> : quantize_rows_kernel<T, E5M2, ALIGNED, 8, 4>,
+                      dim3((unsigned)grid), dim3(256), 0, stream, a);
+    }
+    const int64_t grid = cdiv(a.rows, GROUP) * a.row_groups;
+    if (grid > MAX_INDEX) return GEMM_ERR_UNSUPPORTED;
+    auto* fn = both                             ? quantize_tile_kernel<T, E5M2, ALIGNED, GEMM_QUANTIZE_COLS, true>
+               : kind == GEMM_QUANTIZE_COLS     ? quantize_tile_kernel<T, E5M2, ALIGNED, GEMM_QUANTIZE_COLS, false>
+                                                : quantize_tile_kernel<T, E5M2, ALIGNED, GEMM_QUANTIZE_BLOCKS, false>;
+    return launch(fn, dim3((unsigned)grid), dim3(256), 0, stream, a);
+}
+
+template <typename T, bool E5M2>
+gemm_status_t quantize(int kind, bool both, const QuantizeArgs& a, gemm_stream_t stream) {
+    const bool al = both ? whole_chunks(a.cols, {a.x}, {a.ldx}, {a.q, a.q_cols}, {a.ldq, a.ldq_cols})
+                         : whole_chunks(a.cols, {a.x}, {a.ldx}, {a.q}, {a.ldq});
+    return (al ? quantize_v<T, E5M2, true> : quantize_v<T, E5M2, false>)(kind, both, a, stream);
+}
+
+gemm_status_t quantize_any(int kind, bool both, const QuantizeArgs& a, int dtype, int type, gemm_stream_t stream) {
+    auto* fn = dtype == GEMM_BF16 ? (type == GEMM_E5M2 ? quantize<__nv_bfloat16, true> : quantize<__nv_bfloat16, false>)
+                                  : (type == GEMM_E5M2 ? quantize<__half, true> : quantize<__half, false>);
+    return fn(kind, both, a, stream);
+}
+
+bool bad_types(int dtype, int type) {
+    return (dtype != GEMM_F16 && dtype != GEMM_BF16) || (type != GEMM_E4M3 && type != GEMM_E5M2);
+}
+
+// ---------------------------------------------------------------- norm
+struct NormArgs {
+    const uint16_t *x, *residual, *weight;
+    int64_t ldx, ldres, rows;
+    int hidden;
+    float eps;
+    uint16_t *sum, *y;
+    int64_t ldsum, ldy;
+    uint8_t* q;
+    int64_t ldq;
+    float *scales, *rstd;
+};
+
+// Sum over the threads of a row (threadIdx.y); `part` has room for a float a warp
+// of the block.
+__device__ __forceinline__ float over_row(float v, float* part) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.y * warps + warp] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    v = lane < warps ? part[threadIdx.y * warps + lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A row of `blockDim.x` threads, V chunks each, strided by blockDim.x, so that
+// 16 lanes have a group.  The row stays in registers between the sum and the
+// output.
+template <typename T, bool E5M2, bool ALIGNED, int V>
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
+    __shared__ float part[32];
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool in = row < a.rows;
+    const int n = a.hidden;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    Chunk s[V];
+    float square = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int h = (v * blockDim.x + threadIdx.x) * 8;
+        s[v] = Chunk{};
+        if (!in || h >= n) continue;
+        float x[8];
+        load_row<T, ALIGNED>(a.x + row * a.ldx, h, n, x);
+        if (a.residual) {
+            float y[8];
+            load_row<T, ALIGNED>(a.residual + row * a.ldres, h, n, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] += y[i];
+        }
+        s[v] = pack<T>(x);
+        unpack<T>(s[v], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) square = fmaf(x[i], x[i], square);
+    }
+    square = over_row(square, part);
+    const float rstd = __frsqrt_rn(__fdiv_rn(square, (float)n) + a.eps);
+    if (in && threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int h = (v * blockDim.x + threadIdx.x) * 8;
+        const bool here = in && h < n;
+        float x[8], w[8];
+        unpack<T>(s[v], x);
+        if (here) {
+            if (a.sum) store_16bit<ALIGNED>(a.sum + row * a.ldsum, h, n, s[v]);
+            load_row<T, ALIGNED>(a.weight, h, n, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * w[i];
+            if (a.y) store_16bit<ALIGNED>(a.y + row * a.ldy, h, n, pack<T>(x));
+        }
+        if (a.q) {
+            const float m = over_half(here ? magnitude(x) : 0.f);
+            if (here) {
+                store_quantized<ALIGNED>(a.q + row * a.ldq, h, n, quantized<E5M2, false>(x, inverse_of<E5M2>(m)));
+                if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(h / GROUP) * a.rows + row] = scale_of<E5M2>(m);
+            }
+        }
+    }
+}
+
+struct NormGradArgs {
+    const uint16_t *dy, *s, *weight, *dsum;
+    const float* rstd;
+    int64_t lddy, lds, lddsum, rows, lddx;
+    int hidden;
+    uint16_t* dx;
+    float* part;  // gridDim.x x hidden, or null
+};
+
+// As norm_kernel, one row a block and the next gridDim.x further on, so that a
+// thread has the same columns of every row and sums their dweight in registers.
+template <typename T, bool ALIGNED, int V>
+__global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
+    __shared__ float part[2][32];
+    const int n = a.hidden;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float dw[V][8] = {};
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        Chunk dy[V], s[V];
+        const float rstd = a.rstd[row];
+        float dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int h = (v * blockDim.x + threadIdx.x) * 8;
+            dy[v] = s[v] = Chunk{};
+            if (h >= n) continue;
+            float g[8], x[8], w[8];
+            load_row<T, ALIGNED>(a.dy + row * a.lddy, h, n, g);
+            load_row<T, ALIGNED>(a.s + row * a.lds, h, n, x);
+            load_row<T, ALIGNED>(a.weight, h, n, w);
+            dy[v] = pack<T>(g);
+            s[v] = pack<T>(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = g[i] * (x[i] * rstd);
+                dw[v][i] += p;
+                dot = fmaf(p, w[i], dot);
+            }
+        }
+        const float mean = __fdiv_rn(over_row(dot, part[turn]), (float)n);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int h = (v * blockDim.x + threadIdx.x) * 8;
+            if (h >= n) continue;
+            float g[8], x[8], w[8], d[8] = {};
+            unpack<T>(dy[v], g);
+            unpack<T>(s[v], x);
+            load_row<T, ALIGNED>(a.weight, h, n, w);
+            if (a.dsum) load_row<T, ALIGNED>(a.dsum + row * a.lddsum, h, n, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = rstd * (w[i] * g[i] - (x[i] * rstd) * mean) + d[i];
+            store_16bit<ALIGNED>(a.dx + row * a.lddx, h, n, pack<T>(g));
+        }
+    }
+    if (a.part)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int h = (v * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (h + i < n) a.part[(int64_t)blockIdx.x * n + h + i] = dw[v][i];
+        }
+}
+
+// dweight = the sum of the blocks' parts: 32 columns a block, its warps take the
+// parts in turn.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, int blocks, int n, float* dweight) {
+    __shared__ float sums[32][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float sum = 0.f;
+    if (col < n)
+        for (int b = warp; b < blocks; b += 32) sum += part[(int64_t)b * n + col];
+    sums[warp][threadIdx.x & 31] = sum;
+    __syncthreads();
+    if (warp == 0 && col < n) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum += sums[i][threadIdx.x];
+        dweight[col] = sum;
+    }
+}
+
+// Threads of a row with v chunks each, and rows of a block.
+dim3 norm_block(int64_t hidden, int v) {
+    const int64_t chunks = cdiv(hidden, 8);
+    const unsigned width = (unsigned)(cdiv(cdiv(chunks, v), 32) * 32);
+    return dim3(width, width < 256 ? 256 / width : 1, 1);
+}
+
+int norm_chunks(int64_t hidden) {
+    const int64_t chunks = cdiv(hidden, 8);
+    return chunks <= 256 ? 1 : chunks <= 1024 ? 2 : chunks <= 4096 ? 4 : 8;
+}
+
+// Blocks of the gradient, each with a part of dweight.
+constexpr int64_t GRAD_BLOCKS = 456;
+
+template <typename T, bool E5M2>
+gemm_status_t norm(const NormArgs& a, bool aligned, gemm_stream_t stream) {
+    const int v = norm_chunks(a.hidden);
+    const dim3 block = norm_block(a.hidden, v);
+    const int64_t grid = cdiv(a.rows, block.y);
+    void (*fn)(NormArgs);
+    if (aligned)
+        fn = v == 1 ? norm_kernel<T, E5M2, true, 1> : v == 2 ? norm_kernel<T, E5M2, true, 2>
+             : v == 4 ? norm_kernel<T, E5M2, true, 4> : norm_kernel<T, E5M2, true, 8>;
+    else
+        fn = v == 1 ? norm_kernel<T, E5M2, false, 1> : v == 2 ? norm_kernel<T, E5M2, false, 2>
+             : v == 4 ? norm_kernel<T, E5M2, false, 4> : norm_kernel<T, E5M2, false, 8>;
+    return launch(fn, dim3((unsigned)grid), block, 0, stream, a);
+}
+
+template <typename T>
+gemm_status_t norm_grad(const NormGradArgs& a, bool aligned, float* dweight, gemm_stream_t stream) {
+    const int v = norm_chunks(a.hidden);
+    const dim3 block(norm_block(a.hidden, v).x);
+    const int64_t grid = std::min<int64_t>(a.rows, GRAD_BLOCKS);
+    void (*fn)(NormGradArgs);
+    if (aligned)
+        fn = v == 1 ? norm_grad_kernel<T, true, 1> : v == 2 ? norm_grad_kernel<T, true, 2>
+             : v == 4 ? norm_grad_kernel<T, true, 4> : norm_grad_kernel<T, true, 8>;
+    else
+        fn = v == 1 ? norm_grad_kernel<T, false, 1> : v == 2 ? norm_grad_kernel<T, false, 2>
+             : v == 4 ? norm_grad_kernel<T, false, 4> : norm_grad_kernel<T, false, 8>;
+    const gemm_status_t st = launch(fn, dim3((unsigned)grid), block, 0, stream, a);
+    if (st != GEMM_OK || !dweight) return st;
+    return launch(norm_weight_kernel, dim3((unsigned)cdiv(a.hidden, 32)), dim3(1024), 0, stream, a.part, (int)grid, a.hidden, dweight);
+}
+
+gemm_status_t check_norm(int64_t rows, int64_t hidden) {
+    if (rows < 0 || hidden < 0) return GEMM_ERR_INVALID_ARG;
+    return rows > MAX_INDEX || hidden > GEMM_NORM_MAX_HIDDEN ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_scaled_quantize(gemm_quantize_t kind, const void* x, int64_t ldx, int64_t rows,
+                                   int64_t cols, gemm_dtype_t dtype, gemm_fp8_t type, void* q,
+                                   int64_t ldq, float* scales, gemm_stream_t stream) {
+    if ((kind != GEMM_QUANTIZE_ROWS && kind != GEMM_QUANTIZE_COLS && kind != GEMM_QUANTIZE_BLOCKS) ||
+        bad_types(dtype, type) || rows < 0 || cols < 0 || ldx < cols || ldq < cols)
+        return GEMM_ERR_INVALID_ARG;
+    const bool empty = rows == 0 || cols == 0;
+    if (!empty && (!x || !q || !scales)) return GEMM_ERR_INVALID_ARG;
+    if (rows > MAX_INDEX || cols > MAX_INDEX || misaligned(x, 2) || misaligned(scales, 4)) return GEMM_ERR_UNSUPPORTED;
+    if (empty) return GEMM_OK;
+    QuantizeArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.ldx = ldx;
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.row_groups = (int)cdiv(cols, GROUP);
+    a.q = static_cast<uint8_t*>(q);
+    a.ldq = ldq;
+    a.scales = scales;
+    return quantize_any(kind, false, a, dtype, type, stream);
+}
+
+gemm_status_t gemm_scaled_quantize_both(const void* x, int64_t ldx, int64_t rows, int64_t cols,
+                                        gemm_dtype_t dtype, gemm_fp8_t type, void* q_rows,
+                                        int64_t ldq_rows, float* scales_rows, void* q_cols,
+                                        int64_t ldq_cols, float* scales_cols, gemm_stream_t stream) {
+    if (bad_types(dtype, type) || rows < 0 || cols < 0 || ldx < cols || ldq_rows < cols || ldq_cols < cols)
+        return GEMM_ERR_INVALID_ARG;
+    const bool empty = rows == 0 || cols == 0;
+    if (!empty && (!x || !q_rows || !scales_rows || !q_cols || !scales_cols)) return GEMM_ERR_INVALID_ARG;
+    if (rows > MAX_INDEX || cols > MAX_INDEX || misaligned(x, 2) || misaligned(scales_rows, 4) || misaligned(scales_cols, 4))
+        return GEMM_ERR_UNSUPPORTED;
+    if (empty) return GEMM_OK;
+    QuantizeArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.ldx = ldx;
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.row_groups = (int)cdiv(cols, GROUP);
+    a.q = static_cast<uint8_t*>(q_rows);
+    a.ldq = ldq_rows;
+    a.scales = scales_rows;
+    a.q_cols = static_cast<uint8_t*>(q_cols);
+    a.ldq_cols = ldq_cols;
+    a.scales_cols = scales_cols;
+    return quantize_any(GEMM_QUANTIZE_COLS, true, a, dtype, type, stream);
+}
+
+gemm_status_t gemm_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldres,
+                            const void* weight, float eps, int64_t rows, int64_t hidden,
+                            gemm_dtype_t dtype, void* sum, int64_t ldsum, void* y, int64_t ldy,
+                            void* q, int64_t ldq, gemm_fp8_t type, float* scales, float* rstd,
+                            gemm_stream_t stream) {
+    const gemm_status_t st = check_norm(rows, hidden);
+    if (st == GEMM_ERR_INVALID_ARG || bad_types(dtype, type) || !(eps >= 0.f) || ldx < hidden ||
+        (residual && ldres < hidden) || (sum && (ldsum < hidden || !residual)) || (y && ldy < hidden) ||
+        (q && ldq < hidden) || (!q != !scales))
+        return GEMM_ERR_INVALID_ARG;
+    const bool empty = rows == 0 || hidden == 0;
+    if (!empty && (!x || !weight || (!y && !q))) return GEMM_ERR_INVALID_ARG;
+    if (st != GEMM_OK) return st;
+    if (misaligned(x, 2) || misaligned(residual, 2) || misaligned(weight, 2) || misaligned(sum, 2) || misaligned(y, 2) ||
+        misaligned(scales, 4) || misaligned(rstd, 4))
+        return GEMM_ERR_UNSUPPORTED;
+    if (empty) return GEMM_OK;
+    NormArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.ldx = ldx;
+    a.ldres = residual ? ldres : 0;
+    a.rows = rows;
+    a.hidden = (int)hidden;
+    a.eps = eps;
+    a.sum = static_cast<uint16_t*>(sum);
+    a.y = static_cast<uint16_t*>(y);
+    a.ldsum = sum ? ldsum : 0;
+    a.ldy = y ? ldy : 0;
+    a.q = static_cast<uint8_t*>(q);
+    a.ldq = q ? ldq : 0;
+    a.scales = scales;
+    a.rstd = rstd;
+    const bool al = whole_chunks(hidden, {x, residual, weight, sum, y}, {ldx, a.ldres, a.ldsum, a.ldy}, {q}, {a.ldq});
+    auto* fn = dtype == GEMM_BF16 ? (type == GEMM_E5M2 ? norm<__nv_bfloat16, true> : norm<__nv_bfloat16, false>)
+                                  : (type == GEMM_E5M2 ? norm<__half, true> : norm<__half, false>);
+    return fn(a, al, stream);
+}
+
+gemm_status_t gemm_rms_norm_grad_workspace_size(int64_t rows, int64_t hidden, size_t* bytes) {
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = check_norm(rows, hidden);
+    if (st != GEMM_OK) return st;
+    *bytes = (size_t)std::min<int64_t>(rows, GRAD_BLOCKS) * (size_t)hidden * sizeof(float);
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_rms_norm_grad(const void* dy, int64_t lddy, const void* s, int64_t lds,
+                                 const void* weight, const float* rstd, const void* dsum,
+                                 int64_t lddsum, int64_t rows, int64_t hidden, gemm_dtype_t dtype,
+                                 void* dx, int64_t lddx, float* dweight, void* workspace,
+                                 gemm_stream_t stream) {
+    const gemm_status_t st = check_norm(rows, hidden);
+    if (st == GEMM_ERR_INVALID_ARG || bad_types(dtype, GEMM_E4M3) || lddy < hidden || lds < hidden || lddx < hidden ||
+        (dsum && lddsum < hidden))
+        return GEMM_ERR_INVALID_ARG;
+    if (rows > 0 && hidden > 0 && (!dy || !s || !weight || !rstd || !dx)) return GEMM_ERR_INVALID_ARG;
+    if (st != GEMM_OK) return st;
+    if (misaligned(dy, 2) || misaligned(s, 2) || misaligned(weight, 2) || misaligned(rstd, 4) || misaligned(dsum, 2) ||
+        misaligned(dx, 2) || misaligned(dweight, 4))
+        return GEMM_ERR_UNSUPPORTED;
+    if (hidden == 0) return GEMM_OK;
+    if (rows == 0) {
+        if (!dweight) return GEMM_OK;
+        return cudaMemsetAsync(dweight, 0, (size_t)hidden * sizeof(float), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? GEMM_OK
+                   : GEMM_ERR_CUDA;
+    }
+    if (dweight && (!workspace || misaligned(workspace, 16))) return GEMM_ERR_WORKSPACE;
+    NormGradArgs a{};
+    a.dy = static_cast<const uint16_t*>(dy);
+    a.s = static_cast<const uint16_t*>(s);
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.dsum = static_cast<const uint16_t*>(dsum);
+    a.rstd = rstd;
+    a.lddy = lddy;
+    a.lds = lds;
+    a.lddsum = dsum ? lddsum : 0;
+    a.rows = rows;
+    a.lddx = lddx;
+    a.hidden = (int)hidden;
+    a.dx = static_cast<uint16_t*>(dx);
+    a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+    const bool al = whole_chunks(hidden, {dy, s, weight, dsum, dx}, {lddy, lds, a.lddsum, lddx}, {}, {});
+    return (dtype == GEMM_BF16 ? norm_grad<__nv_bfloat16> : norm_grad<__half>)(a, al, dweight, stream);
+}
+
+}  // extern "C"
