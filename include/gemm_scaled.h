@@ -142,6 +142,32 @@ gemm_status_t gemm_rms_norm_grad(const void *dy, int64_t lddy, const void *s, in
 
 typedef struct gemm_scaled_plan *gemm_scaled_plan_t;
 
+/* Options for gemm_scaled_plan_set_option (key, value). */
+enum {
+    /* CTAs of a scheduling unit: 1 (tiles of 128 x up to 128), or 2, a cluster
+     * that runs pair MMAs (256 x 256); 0 (default) lets the plan choose. */
+    GEMM_SCALED_OPT_CTAS = 1,
+    /* 1: B along the tensor memory's lanes and the rows of A along its columns
+     * (one CTA a unit); 0: the other way; -1 (default) lets the plan choose. */
+    GEMM_SCALED_OPT_TURNED = 2,
+    /* test hook: the scheduling unit with this index gives up before it writes
+     * its first tile, as if a wait had run out, in every run that starts after
+     * the call, replays of captured ones among them.  -1 (default) = off. */
+    GEMM_SCALED_OPT_INJECT_GIVE_UP = 3
+};
+
+/* Keys for gemm_scaled_plan_get_info. */
+enum {
+    GEMM_SCALED_INFO_CTAS = 1,        /* CTAs of a scheduling unit (1 or 2) */
+    GEMM_SCALED_INFO_TURNED = 2,      /* 1: the rows of A are the tiles' columns */
+    GEMM_SCALED_INFO_UNITS = 3,       /* scheduling units of a launch */
+    GEMM_SCALED_INFO_TILES = 4,
+    GEMM_SCALED_INFO_TILE_WIDTH = 5,  /* columns of a tile */
+    GEMM_SCALED_INFO_SHARES = 6,      /* parts along k of a tile that is split */
+    GEMM_SCALED_INFO_STAGES = 7,      /* depth of the shared-memory ring */
+    GEMM_SCALED_INFO_SMEM_BYTES = 8
+};
+
 /*
  * Create a plan for C = A * B on the current device, where
  *
@@ -163,7 +189,24 @@ gemm_status_t gemm_scaled_plan_create(gemm_scaled_plan_t *out, int64_t M, int64_
                                       gemm_layout_t layout_a, gemm_layout_t layout_b,
                                       gemm_scale_t scale_a, gemm_scale_t scale_b);
 
-/* Bytes of device workspace gemm_scaled_run needs (may be 0).  Its contents need no
+/* Same, but touches no device: for inspection only, as if the device had
+ * num_sms SMs; gemm_scaled_run returns GEMM_ERR_NO_DEVICE.  Errors: as above,
+ * INVALID_ARG for num_sms < 2. */
+gemm_status_t gemm_scaled_plan_create_offline(gemm_scaled_plan_t *out, int64_t M, int64_t N, int64_t K,
+                                              gemm_fp8_t type_a, gemm_fp8_t type_b, int out_dtype,
+                                              gemm_layout_t layout_a, gemm_layout_t layout_b,
+                                              gemm_scale_t scale_a, gemm_scale_t scale_b, int num_sms);
+
+/* Set one GEMM_SCALED_OPT_* option.  On error the plan keeps its options.
+ * Errors: INVALID_ARG (NULL plan, unknown key), UNSUPPORTED (value, or two options
+ * that exclude each other), NO_DEVICE (offline plan) and CUDA (INJECT_GIVE_UP). */
+gemm_status_t gemm_scaled_plan_set_option(gemm_scaled_plan_t plan, int key, int64_t value);
+
+/* Read one GEMM_SCALED_INFO_* value.  Errors: INVALID_ARG. */
+gemm_status_t gemm_scaled_plan_get_info(gemm_scaled_plan_t plan, int key, int64_t *value);
+
+/* Bytes of device workspace gemm_scaled_run needs (may be 0), with the options set
+ * so far.  Its contents need no
  * initialisation; two runs that share it must not overlap in time.
  * Errors: INVALID_ARG. */
 gemm_status_t gemm_scaled_workspace_size(gemm_scaled_plan_t plan, size_t *bytes);
@@ -174,13 +217,15 @@ gemm_status_t gemm_scaled_workspace_size(gemm_scaled_plan_t plan, size_t *bytes)
  * faster).  K == 0: C is +0.
  * Errors: INVALID_ARG (NULL plan, or a NULL operand that is not empty),
  * UNSUPPORTED (alignment), WORKSPACE (NULL or not 16-byte aligned while one is
- * needed), CUDA, LAUNCH.
+ * needed), NO_DEVICE (offline plan), CUDA, LAUNCH.
  */
 gemm_status_t gemm_scaled_run(gemm_scaled_plan_t plan, const void *A, const float *scales_a,
                               const void *B, const float *scales_b, void *C, void *workspace,
                               gemm_stream_t stream);
 
-/* As gemm_last_status, for a scaled plan. */
+/* As gemm_last_status, for a scaled plan.  After a timeout it waits for the
+ * device; replays of captured runs are right again from then on, and may be
+ * wrong between the timeout and this call. */
 gemm_status_t gemm_scaled_last_status(gemm_scaled_plan_t plan, gemm_stream_t stream);
 
 /* Free the plan.  NULL is accepted.  Always returns GEMM_OK. */

@@ -61,6 +61,8 @@ GEMM_SCALE_VECTOR, GEMM_SCALE_BLOCK = 0, 1
 GEMM_SCALE_GROUP = 128
 GEMM_QUANTIZE_ROWS, GEMM_QUANTIZE_COLS, GEMM_QUANTIZE_BLOCKS = 0, 1, 2
 GEMM_NORM_MAX_HIDDEN = 65536
+GEMM_SCALED_OPT_CTAS, GEMM_SCALED_OPT_TURNED, GEMM_SCALED_OPT_INJECT_GIVE_UP = 1, 2, 3
+SCALED_INFO = {"ctas": 1, "turned": 2, "units": 3, "tiles": 4, "tile_width": 5, "shares": 6, "stages": 7, "smem_bytes": 8}
 
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3
 TRACE_STAMPS = 6   # uint64 per CTA written by gemm_plan_set_trace: 4 timer + 2 clock stamps
@@ -109,6 +111,9 @@ SIGNATURES = {
     "gemm_rms_norm_grad_workspace_size": (_i32, [_i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
     "gemm_rms_norm_grad": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp]),
     "gemm_scaled_plan_create": (_i32, [_pp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "gemm_scaled_plan_create_offline": (_i32, [_pp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "gemm_scaled_plan_set_option": (_i32, [_vp, _i32, _i64]),
+    "gemm_scaled_plan_get_info": (_i32, [_vp, _i32, ctypes.POINTER(_i64)]),
     "gemm_scaled_workspace_size": (_i32, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
     "gemm_scaled_run": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "gemm_scaled_last_status": (_i32, [_vp, _vp]),
@@ -515,6 +520,26 @@ def gemm_scaled_plan_create(M, N, K, type_a, type_b, out_dtype, layout_a, layout
     return h.value
 
 
+def gemm_scaled_plan_create_offline(M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b,
+                                    num_sms) -> int:
+    h = ctypes.c_void_p()
+    _check(load().gemm_scaled_plan_create_offline(ctypes.byref(h), M, N, K, type_a, type_b, out_dtype, layout_a,
+                                                  layout_b, scale_a, scale_b, num_sms),
+           "gemm_scaled_plan_create_offline")
+    return h.value
+
+
+def gemm_scaled_plan_set_option(plan, key, value):
+    _check(load().gemm_scaled_plan_set_option(plan, key, value), "gemm_scaled_plan_set_option")
+
+
+def gemm_scaled_plan_get_info(plan, key) -> int:
+    v = ctypes.c_int64()
+    key = SCALED_INFO[key] if isinstance(key, str) else key
+    _check(load().gemm_scaled_plan_get_info(plan, key, ctypes.byref(v)), "gemm_scaled_plan_get_info")
+    return v.value
+
+
 def gemm_scaled_workspace_size(plan) -> int:
     v = ctypes.c_size_t()
     _check(load().gemm_scaled_workspace_size(plan, ctypes.byref(v)), "gemm_scaled_workspace_size")
@@ -538,10 +563,23 @@ def gemm_scaled_plan_destroy(plan):
 class ScaledPlan:
     """Owning wrapper around a scaled plan handle (marshalling only)."""
 
-    def __init__(self, M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b):
+    def __init__(self, M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b, offline_sms=None,
+                 ctas=None, turned=None):
         self.M, self.N, self.K = M, N, K
         self.out_dtype = out_dtype
-        self.handle = gemm_scaled_plan_create(M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b)
+        args = (M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b)
+        self.handle = (gemm_scaled_plan_create(*args) if offline_sms is None
+                       else gemm_scaled_plan_create_offline(*args, offline_sms))
+        if turned is not None:
+            self.set_option(GEMM_SCALED_OPT_TURNED, int(turned))
+        if ctas is not None:
+            self.set_option(GEMM_SCALED_OPT_CTAS, int(ctas))
+
+    def info(self, key):
+        return gemm_scaled_plan_get_info(self.handle, key)
+
+    def set_option(self, key, value):
+        gemm_scaled_plan_set_option(self.handle, key, value)
 
     @property
     def workspace_size(self) -> int:

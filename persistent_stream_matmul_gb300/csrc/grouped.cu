@@ -4,13 +4,12 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
-#include <chrono>
 #include <mutex>
 #include <new>
 
 #include "gemm_moe.h"
 #include "grouped_kernel.cuh"
+#include "host.cuh"
 
 using namespace psm;
 
@@ -31,54 +30,6 @@ struct gemm_grouped_plan {
 };
 
 namespace {
-
-constexpr int64_t MAX_INDEX = (1ll << 31) - 1024;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// Run numbers tagged into the split tiles' counters, 48 bits, unique in the
-// process and started from the clock, so that what another run or program left
-// in a workspace is not taken for this run's.
-uint64_t next_epoch() {
-    static std::atomic<uint64_t> epoch{
-        (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() << 8};
-    uint64_t e;
-    do e = ++epoch & 0xffffffffffffull;
-    while (e == 0);
-    return e;
-}
-
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Kernels, by [pair][ROWS K-major, ROWS MN-major, INNER][bf16].
 template <bool PAIR>

@@ -8,10 +8,9 @@
 #include <initializer_list>
 
 #include "gemm.h"
+#include "host.cuh"
 
 namespace psm {
-
-constexpr int64_t MAX_INDEX = (1ll << 31) - 1024;
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }

@@ -1,113 +1,242 @@
-// Scaled products of include/gemm_scaled.h: plans, launches and the C entry
-// points.
-#include <cuda_fp8.h>
+// Scaled products of include/gemm_scaled.h: plans, tensor maps, launches and the
+// C entry points.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <mutex>
 #include <new>
 
 #include "gemm_scaled.h"
-#include "ptx.cuh"
-#include "rows.cuh"
+#include "host.cuh"
+#include "scaled_kernel.cuh"
 
 using namespace psm;
 
+static_assert(S_BK == GEMM_SCALE_GROUP, "a k-block is a group");
+
 struct gemm_scaled_plan {
     int64_t M, N, K;
-    int type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b, device;
+    int type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b;
+    int device, num_sms;
+    bool offline;
+    int opt_ctas, opt_turned;
+    // derived
+    int ctas, turned, cols;  // cols: the kernel's COLS
+    int width;               // columns of a tile
+    GroupedShape shape;
+    size_t counter_bytes, ws_bytes;
+    int* d_status;           // G_WORDS words
+    int timeouts;            // G_WORD_TIMEOUTS
 };
 
 namespace {
 
-constexpr int GROUP = GEMM_SCALE_GROUP;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
+// Kernels by form: 0-2 pairs, 3-5 one CTA, 6-7 turned, by COLS.
+struct Kernel {
+    void* fn;
+    int smem, stages;
 };
 
-// One operand: element (r, k) at q[r * row + k * col], its scale at
-// s[(r >> shift) * s_row + (k / 128) * s_group].
-struct Operand {
-    const uint8_t* q;
-    const float* s;
-    int64_t row, col, s_row, s_group, rows;
-    int shift, e5m2;
+template <bool PAIR, bool TURNED, int COLS>
+Kernel kernel_v() {
+    return {(void*)&scaled_kernel<PAIR, TURNED, COLS>, ScaledCfg<PAIR, TURNED, COLS>::SMEM_BYTES, ScaledCfg<PAIR, TURNED, COLS>::STAGES};
+}
+
+Kernel kernel_of(int ctas, int turned, int cols) {
+    if (turned) return cols == 1 ? kernel_v<false, true, 1>() : kernel_v<false, true, 2>();
+    if (ctas == 2) return cols == 0 ? kernel_v<true, false, 0>() : cols == 1 ? kernel_v<true, false, 1>() : kernel_v<true, false, 2>();
+    return cols == 0 ? kernel_v<false, false, 0>() : cols == 1 ? kernel_v<false, false, 1>() : kernel_v<false, false, 2>();
+}
+
+// Whether the kernel may use its shared memory on the current device.
+bool prepared(int ctas, int turned, int cols, int dev) {
+    static std::mutex mu;
+    static bool ready[64][2][2][3];
+    if (dev < 0 || dev >= 64) return false;
+    const Kernel k = kernel_of(ctas, turned, cols);
+    std::lock_guard<std::mutex> lock(mu);
+    bool& r = ready[dev][ctas - 1][turned][cols];
+    if (!r) {
+        if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        r = true;
+    }
+    return true;
+}
+
+// Pairs of CTAs that can be resident at once: a cluster lives inside one GPC,
+// so this can be below #SMs / 2.  0 when unknown.
+int resident_pairs(int dev) {
+    static std::mutex mu;
+    static int cache[64];
+    if (!prepared(2, 0, 0, dev)) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[dev]) return cache[dev];
+    const Kernel k = kernel_of(2, 0, 0);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(S_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)k.smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k.fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return cache[dev] = n;
+}
+
+gemm_status_t derive(gemm_scaled_plan* p) {
+    int turned = p->opt_turned, ctas = p->opt_ctas;
+    if (turned < 0) turned = ctas != 2 && p->M <= 128;
+    if (ctas == 0) ctas = !turned && cdiv(p->M, 256) * cdiv(p->N, 256) >= 64 ? 2 : 1;
+    if (turned && ctas == 2) return GEMM_ERR_UNSUPPORTED;
+    const int64_t lanes = turned ? p->N : p->M, cols = turned ? p->M : p->N;
+    const bool l_block = (turned ? p->scale_b : p->scale_a) == GEMM_SCALE_BLOCK;
+    const int tile = 128 * ctas;
+    GroupedShape s{};
+    s.groups = 1;
+    s.rows = (int32_t)cols;
+    s.tiles_m = (int32_t)cdiv(lanes, tile);
+    s.kb = (int32_t)cdiv(p->K, S_BK);
+    s.tile_n = tile;
+    s.tile_shift = ctas == 2 ? 8 : 7;
+    // straight tiles have one width, so that a half's columns share a block's scale
+    s.step = !turned ? tile : p->layout_a == GEMM_ROW_MAJOR ? 16 : 32;
+    s.band = 8;
+    s.least_share = ctas == 2 ? 16 : turned ? 8 : 12;
+    s.units = p->num_sms / ctas;
+    if (ctas == 2 && !p->offline) {
+        const int n = resident_pairs(p->device);
+        if (n > 0) s.units = std::min(s.units, n);
+    }
+    const int64_t side = std::max<int64_t>(1, cdiv(cols, tile));
+    if (s.tiles_m > 0 && side > MAX_INDEX / s.tiles_m) return GEMM_ERR_UNSUPPORTED;
+    s.may_split = (int64_t)s.units * s.kb < MAX_INDEX;
+    p->ctas = ctas;
+    p->turned = turned;
+    p->cols = !turned && p->scale_b == GEMM_SCALE_BLOCK ? 0 : l_block ? 1 : 2;
+    p->width = (int)(cdiv(std::max<int64_t>(1, cdiv(cols, side)), s.step) * s.step);
+    p->shape = s;
+    p->counter_bytes = p->ws_bytes = 0;
+    if (p->M > 0 && p->N > 0 && p->K > 0 && grouped_split(s, (int32_t)(side * s.tiles_m), 0).most > 0) {
+        const size_t slot = 128 * (size_t)tile * sizeof(float), grid = (size_t)s.units * ctas;
+        p->counter_bytes = (grid * 8 + 255) / 256 * 256;
+        p->ws_bytes = p->counter_bytes + grid * slot;
+    }
+    return GEMM_OK;
+}
+
+bool bad(int v) { return v != 0 && v != 1; }
+
+gemm_status_t make_plan(gemm_scaled_plan_t* out, int64_t M, int64_t N, int64_t K, int type_a, int type_b, int out_dtype,
+                        int layout_a, int layout_b, int scale_a, int scale_b, bool offline, int num_sms) {
+    if (!out || M < 0 || N < 0 || K < 0 || bad(type_a) || bad(type_b) || bad(layout_a) || bad(layout_b) || bad(scale_a) ||
+        bad(scale_b) || (out_dtype != GEMM_F16 && out_dtype != GEMM_BF16 && out_dtype != GEMM_F32) || (offline && num_sms < 2))
+        return GEMM_ERR_INVALID_ARG;
+    if (M > MAX_INDEX || N > MAX_INDEX || K > MAX_INDEX || (layout_a == GEMM_ROW_MAJOR ? K : M) % 16 ||
+        (layout_b == GEMM_COL_MAJOR ? K : N) % 16)
+        return GEMM_ERR_UNSUPPORTED;
+    int dev = -1;
+    if (!offline) {
+        int count = 0, major = 0, minor = 0;
+        if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
+            cudaGetLastError();
+            return GEMM_ERR_NO_DEVICE;
+        }
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        if (major != 10 || minor != 3) return GEMM_ERR_NO_DEVICE;
+    }
+    gemm_scaled_plan* p = new (std::nothrow) gemm_scaled_plan();
+    if (!p) return GEMM_ERR_CUDA;
+    p->M = M;
+    p->N = N;
+    p->K = K;
+    p->type_a = type_a;
+    p->type_b = type_b;
+    p->out_dtype = out_dtype;
+    p->layout_a = layout_a;
+    p->layout_b = layout_b;
+    p->scale_a = scale_a;
+    p->scale_b = scale_b;
+    p->device = dev;
+    p->num_sms = num_sms;
+    p->offline = offline;
+    p->opt_turned = -1;
+    const gemm_status_t st = derive(p);
+    if (st != GEMM_OK) {
+        delete p;
+        return st;
+    }
+    if (!offline && (cudaMalloc(&p->d_status, G_WORDS * sizeof(int)) != cudaSuccess ||
+                     cudaMemset(p->d_status, 0, G_WORDS * sizeof(int)) != cudaSuccess)) {
+        cudaGetLastError();
+        if (p->d_status) cudaFree(p->d_status);
+        delete p;
+        return GEMM_ERR_CUDA;
+    }
+    *out = p;
+    return GEMM_OK;
+}
+
+// 128-byte-swizzled map of a matrix of y rows of x elements.
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, int64_t x, int64_t y, uint32_t box_x, uint32_t box_y) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)x, (cuuint64_t)y};
+    const cuuint64_t strides[1] = {(cuuint64_t)x * (cuuint64_t)size};
+    const cuuint32_t box[2] = {box_x, box_y};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One operand, as the lanes or the columns side sees it: `rows` of K elements.
+struct Side {
+    const void* q;
+    int64_t rows, K;
+    bool mn;
+    ScaledScales s;
 };
 
-__device__ __forceinline__ float value(uint8_t v, int e5m2) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, e5m2 ? __NV_E5M2 : __NV_E4M3)));
-}
-
-// 64 x 64 of C a block, 4 x 4 a thread; a group's sum is scaled and added to the
-// sums before it.
-__global__ void __launch_bounds__(256) scaled_kernel(Operand a, Operand b, int64_t K, void* c, int out_dtype) {
-    __shared__ float as[32][65], bs[32][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
-    grid_dependency_wait();
-    float acc[4][4] = {};
-    for (int64_t g = 0; g * GROUP < K; ++g) {
-        float part[4][4] = {};
-        for (int64_t k0 = g * GROUP; k0 < g * GROUP + GROUP; k0 += 32) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-                const int r = i >> 5, k = i & 31;
-                as[k][r] = m0 + r < a.rows && k0 + k < K ? value(a.q[(m0 + r) * a.row + (k0 + k) * a.col], a.e5m2) : 0.f;
-                bs[k][r] = n0 + r < b.rows && k0 + k < K ? value(b.q[(n0 + r) * b.row + (k0 + k) * b.col], b.e5m2) : 0.f;
-            }
-            __syncthreads();
-            for (int k = 0; k < 32; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) part[i][j] = fmaf(as[k][ty * 4 + i], bs[k][tx * 4 + j], part[i][j]);
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-                if (m < a.rows && n < b.rows)
-                    acc[i][j] = fmaf(part[i][j], a.s[(m >> a.shift) * a.s_row + g * a.s_group] * b.s[(n >> b.shift) * b.s_row + g * b.s_group], acc[i][j]);
-            }
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j, at = m * b.rows + n;
-            if (m >= a.rows || n >= b.rows) continue;
-            if (out_dtype == GEMM_F32) static_cast<float*>(c)[at] = acc[i][j];
-            else if (out_dtype == GEMM_BF16) static_cast<__nv_bfloat16*>(c)[at] = __float2bfloat16_rn(acc[i][j]);
-            else static_cast<__half*>(c)[at] = __float2half_rn(acc[i][j]);
-        }
-}
-
-// k_major: the summed dimension is contiguous.
-Operand operand(const void* q, const float* s, int64_t rows, int64_t K, bool k_major, int scale, int type) {
-    Operand o{};
-    o.q = static_cast<const uint8_t*>(q);
-    o.s = s;
+Side side_of(const void* q, const float* s, int64_t rows, int64_t K, bool k_major, int scale) {
+    Side o{};
+    o.q = q;
     o.rows = rows;
-    o.row = k_major ? K : 1;
-    o.col = k_major ? 1 : rows;
-    o.e5m2 = type == GEMM_E5M2;
+    o.K = K;
+    o.mn = !k_major;
+    o.s.s = s;
+    o.s.rows = (int32_t)rows;
     if (scale == GEMM_SCALE_VECTOR) {
-        o.s_row = 1;
-        o.s_group = rows;
+        o.s.row = 1;
+        o.s.group = rows;
     } else {
-        o.shift = 7;
-        o.s_row = k_major ? cdiv(K, GROUP) : 1;
-        o.s_group = k_major ? 1 : cdiv(rows, GROUP);
+        o.s.shift = 7;
+        o.s.row = k_major ? cdiv(K, S_BK) : 1;
+        o.s.group = k_major ? 1 : cdiv(rows, S_BK);
     }
     return o;
 }
 
-bool bad(int v) { return v != 0 && v != 1; }
+bool encode_side(CUtensorMap* m, const Side& o, uint32_t rows) {
+    return o.mn ? encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, o.rows, o.K, 128, S_BK)
+                : encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, o.K, o.rows, S_BK, rows);
+}
+
+bool misaligned(const void* p, size_t size) { return ((uintptr_t)p & (size - 1)) != 0; }
 
 }  // namespace
 
@@ -117,31 +246,65 @@ gemm_status_t gemm_scaled_plan_create(gemm_scaled_plan_t* out, int64_t M, int64_
                                       gemm_fp8_t type_a, gemm_fp8_t type_b, int out_dtype,
                                       gemm_layout_t layout_a, gemm_layout_t layout_b,
                                       gemm_scale_t scale_a, gemm_scale_t scale_b) {
-    if (!out || M < 0 || N < 0 || K < 0 || bad(type_a) || bad(type_b) || bad(layout_a) || bad(layout_b) || bad(scale_a) ||
-        bad(scale_b) || (out_dtype != GEMM_F16 && out_dtype != GEMM_BF16 && out_dtype != GEMM_F32))
-        return GEMM_ERR_INVALID_ARG;
-    if (M > MAX_INDEX || N > MAX_INDEX || K > MAX_INDEX || (layout_a == GEMM_ROW_MAJOR ? K : M) % 16 ||
-        (layout_b == GEMM_COL_MAJOR ? K : N) % 16 || cdiv(N, 64) > 65535)
-        return GEMM_ERR_UNSUPPORTED;
-    int count = 0, dev = 0, major = 0, minor = 0;
-    if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
-        cudaGetLastError();
-        return GEMM_ERR_NO_DEVICE;
+    return make_plan(out, M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b, false, 0);
+}
+
+gemm_status_t gemm_scaled_plan_create_offline(gemm_scaled_plan_t* out, int64_t M, int64_t N, int64_t K,
+                                              gemm_fp8_t type_a, gemm_fp8_t type_b, int out_dtype,
+                                              gemm_layout_t layout_a, gemm_layout_t layout_b,
+                                              gemm_scale_t scale_a, gemm_scale_t scale_b, int num_sms) {
+    return make_plan(out, M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b, true, num_sms);
+}
+
+gemm_status_t gemm_scaled_plan_set_option(gemm_scaled_plan_t p, int key, int64_t value) {
+    if (!p) return GEMM_ERR_INVALID_ARG;
+    if (key == GEMM_SCALED_OPT_INJECT_GIVE_UP) {
+        if (value < -1 || value >= p->shape.units) return GEMM_ERR_UNSUPPORTED;
+        if (p->offline) return GEMM_ERR_NO_DEVICE;
+        DeviceGuard guard(p->device);
+        const int word = (int)value + 1;
+        return guard.ok && cudaMemcpy(p->d_status + G_WORD_GIVE_UP, &word, sizeof(int), cudaMemcpyHostToDevice) == cudaSuccess
+                   ? GEMM_OK
+                   : GEMM_ERR_CUDA;
     }
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    if (major != 10 || minor != 3) return GEMM_ERR_NO_DEVICE;
-    gemm_scaled_plan* p = new (std::nothrow) gemm_scaled_plan{M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b, dev};
-    if (!p) return GEMM_ERR_CUDA;
-    *out = p;
+    const int saved[2] = {p->opt_ctas, p->opt_turned};
+    if (key == GEMM_SCALED_OPT_CTAS) {
+        if (value < 0 || value > 2) return GEMM_ERR_UNSUPPORTED;
+        p->opt_ctas = (int)value;
+    } else if (key == GEMM_SCALED_OPT_TURNED) {
+        if (value < -1 || value > 1) return GEMM_ERR_UNSUPPORTED;
+        p->opt_turned = (int)value;
+    } else {
+        return GEMM_ERR_INVALID_ARG;
+    }
+    const gemm_status_t st = derive(p);
+    if (st != GEMM_OK) {
+        p->opt_ctas = saved[0];
+        p->opt_turned = saved[1];
+        derive(p);
+    }
+    return st;
+}
+
+gemm_status_t gemm_scaled_plan_get_info(gemm_scaled_plan_t p, int key, int64_t* value) {
+    if (!p || !value) return GEMM_ERR_INVALID_ARG;
+    switch (key) {
+        case GEMM_SCALED_INFO_CTAS: *value = p->ctas; break;
+        case GEMM_SCALED_INFO_TURNED: *value = p->turned; break;
+        case GEMM_SCALED_INFO_UNITS: *value = p->shape.units; break;
+        case GEMM_SCALED_INFO_TILES: *value = grouped_tiles(p->shape, p->shape.rows); break;
+        case GEMM_SCALED_INFO_TILE_WIDTH: *value = p->width; break;
+        case GEMM_SCALED_INFO_SHARES: *value = p->ws_bytes ? grouped_split(p->shape, grouped_tiles(p->shape, p->shape.rows), 0).shares : 1; break;
+        case GEMM_SCALED_INFO_STAGES: *value = kernel_of(p->ctas, p->turned, p->cols).stages; break;
+        case GEMM_SCALED_INFO_SMEM_BYTES: *value = kernel_of(p->ctas, p->turned, p->cols).smem; break;
+        default: return GEMM_ERR_INVALID_ARG;
+    }
     return GEMM_OK;
 }
 
 gemm_status_t gemm_scaled_workspace_size(gemm_scaled_plan_t p, size_t* bytes) {
     if (!p || !bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = 0;
+    *bytes = p->ws_bytes;
     return GEMM_OK;
 }
 
@@ -149,26 +312,106 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
                               const void* B, const float* scales_b, void* C, void* workspace,
                               gemm_stream_t stream) {
     if (!p) return GEMM_ERR_INVALID_ARG;
-    if (p->M == 0 || p->N == 0) return GEMM_OK;
+    if (p->offline) return GEMM_ERR_NO_DEVICE;
+    if (p->M == 0 || p->N == 0) return GEMM_OK;  // C is empty
     if (!C || (p->K > 0 && (!A || !B || !scales_a || !scales_b))) return GEMM_ERR_INVALID_ARG;
-    const size_t size = p->out_dtype == GEMM_F32 ? 4 : 2;
-    if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, size) || misaligned(scales_a, 4) || misaligned(scales_b, 4))
+    const int size = p->out_dtype == GEMM_F32 ? 4 : 2;
+    if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, (size_t)size) || misaligned(scales_a, 4) || misaligned(scales_b, 4))
         return GEMM_ERR_UNSUPPORTED;
+    if (p->ws_bytes > 0 && (!workspace || misaligned(workspace, 16))) return GEMM_ERR_WORKSPACE;
     DeviceGuard guard(p->device);
     if (!guard.ok) return GEMM_ERR_CUDA;
-    const Operand a = operand(A, scales_a, p->M, p->K, p->layout_a == GEMM_ROW_MAJOR, p->scale_a, p->type_a);
-    const Operand b = operand(B, scales_b, p->N, p->K, p->layout_b == GEMM_COL_MAJOR, p->scale_b, p->type_b);
-    return launch(scaled_kernel, dim3((unsigned)cdiv(p->M, 64), (unsigned)cdiv(p->N, 64)), dim3(256), 0, stream, a, b, p->K, C, p->out_dtype);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (p->K == 0)  // empty sums: +0
+        return cudaMemsetAsync(C, 0, (size_t)p->M * (size_t)p->N * (size_t)size, st) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    if (!prepared(p->ctas, p->turned, p->cols, p->device)) return GEMM_ERR_CUDA;
+
+    const Side a = side_of(A, scales_a, p->M, p->K, p->layout_a == GEMM_ROW_MAJOR, p->scale_a);
+    const Side b = side_of(B, scales_b, p->N, p->K, p->layout_b == GEMM_COL_MAJOR, p->scale_b);
+    const Side &l = p->turned ? b : a, &r = p->turned ? a : b;
+    ScaledParams kp{};
+    kp.s = p->shape;
+    kp.l_total = (int32_t)l.rows;
+    kp.l = l.s;
+    kp.r = r.s;
+    kp.out = C;
+    kp.ldc = p->N;
+    kp.out_dtype = p->out_dtype;
+    kp.boxes = !p->turned && !misaligned(C, 16) && p->N * size % 16 == 0;
+    kp.l_mn = l.mn;
+    kp.r_mn = r.mn;
+    // The maps are encoded for every run: they cost well under a microsecond
+    // of host time, and nothing is kept by an operand's address.
+    ScaledMaps tm{};
+    bool ok = encode_side(&tm.l, l, 128) && encode_side(&tm.r, r, (uint32_t)(p->width / p->ctas));
+    if (kp.boxes)
+        ok = ok && encode(&tm.c, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, size, C, p->N, p->M,
+                          (uint32_t)(128 / size), 32);
+    if (!ok) return GEMM_ERR_UNSUPPORTED;
+    if (p->ws_bytes > 0) {
+        kp.counters = reinterpret_cast<unsigned long long*>(workspace);
+        kp.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + p->counter_bytes);
+    } else {
+        kp.s.may_split = 0;
+    }
+    kp.epoch = next_epoch();
+    kp.status = p->d_status;
+    const int l_e5m2 = (p->turned ? p->type_b : p->type_a) == GEMM_E5M2, r_e5m2 = (p->turned ? p->type_a : p->type_b) == GEMM_E5M2;
+    kp.idesc = idesc_f16(0, l.mn, r.mn, 128 * p->ctas, 0) | ((uint32_t)l_e5m2 << 7) | ((uint32_t)r_e5m2 << 10);
+    // a wait may last as long as the longest tile's k-loop
+    kp.pipe_limit_ns = 4000000000ull + 2000ull * (uint64_t)p->shape.kb;
+
+    const Kernel k = kernel_of(p->ctas, p->turned, p->cols);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p->shape.units * p->ctas), 1, 1);
+    cfg.blockDim = dim3(S_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)k.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    if (p->ctas == 2) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = 2;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    void* args[2] = {&tm, &kp};
+    if (cudaLaunchKernelExC(&cfg, k.fn, args) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
 }
 
 gemm_status_t gemm_scaled_last_status(gemm_scaled_plan_t p, gemm_stream_t stream) {
     if (!p) return GEMM_ERR_INVALID_ARG;
+    if (p->offline) return GEMM_ERR_NO_DEVICE;
     DeviceGuard guard(p->device);
     if (!guard.ok) return GEMM_ERR_CUDA;
-    return cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
+    int h = 0;
+    if (cudaMemcpy(&h, p->d_status + G_WORD_STATUS, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (h == 0) return GEMM_OK;
+    // another tag from here on (grouped_tag), which no run on another stream may
+    // see changing under way
+    static_assert(G_WORD_STATUS == 0 && G_WORD_TIMEOUTS == 1, "both words are written at once");
+    const int words[2] = {0, p->timeouts + 1};
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(p->d_status, words, sizeof(words), cudaMemcpyHostToDevice) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    ++p->timeouts;
+    return GEMM_ERR_TIMEOUT;
 }
 
 gemm_status_t gemm_scaled_plan_destroy(gemm_scaled_plan_t p) {
+    if (!p) return GEMM_OK;
+    if (p->d_status) cudaFree(p->d_status);
     delete p;
     return GEMM_OK;
 }

@@ -255,8 +255,6 @@ bool whole_chunks(int64_t cols, std::initializer_list<const void*> in, std::init
     return (bits & 15) == 0;
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 template <typename T, bool E5M2, bool ALIGNED>
 gemm_status_t quantize_v(int kind, bool both, const QuantizeArgs& a, gemm_stream_t stream) {
     if (kind == GEMM_QUANTIZE_ROWS && !both) {

@@ -112,8 +112,35 @@ def test_plan_refusals(status, changes):
     refused(status, B.gemm_scaled_plan_create, *_with(PLAN, **changes))
 
 
+@pytest.mark.parametrize("M,N,K,ctas,turned", [(1, 4096, 4096, 1, 1), (128, 128, 128, 1, 1), (129, 4096, 512, 1, 0), (8192, 8192, 512, 2, 0)])
+def test_offline_plans(M, N, K, ctas, turned):
+    p = B.ScaledPlan(M, N, K, 0, 0, 1, 0, 1, 0, 1, offline_sms=152)
+    assert (p.info("ctas"), p.info("turned")) == (ctas, turned)
+    width = -(-M // 16) * 16 if turned else 128 * ctas
+    assert p.info("tile_width") == width and p.info("units") == 152 // ctas
+    tiles = -(-N // 128) if turned else -(-M // (128 * ctas)) * -(-N // (128 * ctas))
+    assert p.info("tiles") == tiles
+    assert (p.workspace_size > 0) == (p.info("shares") > 1)
+    refused(B.GEMM_ERR_NO_DEVICE, p.run, P, P, P, P, P, P)
+    assert p.last_status() == B.GEMM_ERR_NO_DEVICE
+    for key, value, status in ((1, 3, UNS), (1, -1, UNS), (2, 2, UNS), (2, -2, UNS), (3, -2, UNS), (3, 0, B.GEMM_ERR_NO_DEVICE), (4, 0, INV)):
+        refused(status, p.set_option, key, value)
+    p.set_option(2, 1)
+    p.set_option(1, 1)
+    refused(UNS, p.set_option, 1, 2)  # a turned product has one CTA a unit
+    assert p.info("ctas") == 1
+    refused(INV, p.info, 99)
+    p.close()
+
+
+def test_offline_refusals():
+    refused(INV, B.gemm_scaled_plan_create_offline, *PLAN.values(), 1)
+
+
 def test_null_handles():
     lib = B.load()
+    assert lib.gemm_scaled_plan_set_option(None, 1, 1) == INV
+    assert lib.gemm_scaled_plan_get_info(None, 1, ctypes.byref(ctypes.c_int64())) == INV
     assert lib.gemm_scaled_plan_create(None, 16, 16, 16, 0, 0, 1, 0, 1, 0, 1) == INV
     assert lib.gemm_scaled_workspace_size(None, ctypes.byref(ctypes.c_size_t())) == INV
     assert lib.gemm_scaled_run(None, P, P, P, P, P, P, None) == INV

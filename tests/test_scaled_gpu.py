@@ -189,3 +189,57 @@ def test_quantised_layer_end_to_end():
         p.run(A, sa, Bm, sb, C, ws)
         assert p.last_status() == B.GEMM_OK
         assert_product(C, *product(A, sa, ka, Bm, sb, kb, la == ROW, lb == ROW), K)
+
+
+# every form of the kernel, whatever the plan would choose: (ctas, turned)
+FORMS = [(1, 0), (2, 0), (1, 1)]
+
+
+@pytest.mark.parametrize("ctas,turned", FORMS)
+@pytest.mark.parametrize("layout_a", [ROW, COL])
+@pytest.mark.parametrize("layout_b", [ROW, COL])
+@pytest.mark.parametrize("scale_a,scale_b", [(VEC, BLOCK), (VEC, VEC), (BLOCK, VEC), (BLOCK, BLOCK)])
+@pytest.mark.parametrize("M,N,K", [(16, 144, 272), (304, 528, 784), (528, 272, 4112)])
+def test_forms(M, N, K, layout_a, layout_b, scale_a, scale_b, ctas, turned):
+    kw = dict(layout_a=layout_a, layout_b=layout_b, scale_a=scale_a, scale_b=scale_b, ctas=ctas, turned=turned)
+    for out in ("f32", "bf16"):
+        Case(M, N, K, out=out, seed=M, **kw).check()
+    c = Case(M, N, K, out="f32", integers=True, seed=M, **kw)
+    assert c.plan.info("ctas") == ctas and c.plan.info("turned") == turned
+    # whole sixteenths below 9 * 16 * 4112 < 2^20: 24 bits, exact in any order
+    assert torch.equal(c.run().double(), c.reference()[0])
+
+
+@pytest.mark.parametrize("ctas,turned,M,N,K", [(2, 0, 2048, 2560, 4096), (2, 0, 512, 512, 16384), (1, 0, 1280, 2048, 2304),
+                                               (1, 0, 128, 128, 20000), (1, 1, 48, 512, 8192), (1, 1, 300, 8192, 4096), (1, 1, 1, 128, 65536)])
+@pytest.mark.parametrize("scale_b", [VEC, BLOCK])
+def test_split_tiles(ctas, turned, M, N, K, scale_b):
+    """Tiles left over a whole round of the units, or fewer than one, cut along k and joined."""
+    c = Case(M, N, K, out="f32", integers=False, seed=K, ctas=ctas, turned=turned, scale_b=scale_b)
+    assert c.plan.info("shares") > 1
+    first = c.run().clone()
+    exact, absolute = c.reference()
+    assert_product(first, exact, absolute, K)
+    for _ in range(5):
+        assert torch.equal(c.run(), first)
+
+
+@pytest.mark.parametrize("ctas,turned", FORMS)
+def test_timeout_is_reported_and_replays_recover(ctas, turned):
+    c = Case(96, 1024, 8192, seed=5, ctas=ctas, turned=turned)
+    want = c.run().clone()
+    out, graph, stream = torch.empty_like(want), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        c.plan.run(c.a, c.sa, c.b, c.sb, out, c.ws, stream)
+    with torch.cuda.stream(stream):
+        for unit in (0, 3):
+            c.plan.set_option(B.GEMM_SCALED_OPT_INJECT_GIVE_UP, unit)
+            graph.replay()
+            assert c.plan.last_status(stream) == B.GEMM_ERR_TIMEOUT
+            assert c.plan.last_status(stream) == B.GEMM_OK
+            c.plan.set_option(B.GEMM_SCALED_OPT_INJECT_GIVE_UP, -1)
+            for _ in range(3):
+                out.fill_(7)
+                graph.replay()
+                assert c.plan.last_status(stream) == B.GEMM_OK
+                assert torch.equal(out, want)
