@@ -22,7 +22,7 @@ struct gemm_scaled_plan {
     bool offline;
     int opt_ctas, opt_turned;
     // derived
-    int ctas, turned, cols;  // cols: the kernel's COLS
+    int ctas, turned, col_vector;
     int width;               // columns of a tile
     GroupedShape shape;
     size_t counter_bytes, ws_bytes;
@@ -32,31 +32,31 @@ struct gemm_scaled_plan {
 
 namespace {
 
-// Kernels by form: 0-2 pairs, 3-5 one CTA, 6-7 turned, by COLS.
 struct Kernel {
     void* fn;
     int smem, stages;
 };
 
-template <bool PAIR, bool TURNED, int COLS>
+template <bool PAIR, bool TURNED, bool COL_VECTOR>
 Kernel kernel_v() {
-    return {(void*)&scaled_kernel<PAIR, TURNED, COLS>, ScaledCfg<PAIR, TURNED, COLS>::SMEM_BYTES, ScaledCfg<PAIR, TURNED, COLS>::STAGES};
+    using Cf = ScaledCfg<PAIR, TURNED, COL_VECTOR>;
+    return {(void*)&scaled_kernel<PAIR, TURNED, COL_VECTOR>, Cf::SMEM_BYTES, Cf::STAGES};
 }
 
-Kernel kernel_of(int ctas, int turned, int cols) {
-    if (turned) return cols == 1 ? kernel_v<false, true, 1>() : kernel_v<false, true, 2>();
-    if (ctas == 2) return cols == 0 ? kernel_v<true, false, 0>() : cols == 1 ? kernel_v<true, false, 1>() : kernel_v<true, false, 2>();
-    return cols == 0 ? kernel_v<false, false, 0>() : cols == 1 ? kernel_v<false, false, 1>() : kernel_v<false, false, 2>();
+Kernel kernel_of(int ctas, int turned, int col_vector) {
+    if (turned) return kernel_v<false, true, true>();
+    if (ctas == 2) return col_vector ? kernel_v<true, false, true>() : kernel_v<true, false, false>();
+    return col_vector ? kernel_v<false, false, true>() : kernel_v<false, false, false>();
 }
 
 // Whether the kernel may use its shared memory on the current device.
-bool prepared(int ctas, int turned, int cols, int dev) {
+bool prepared(int ctas, int turned, int col_vector, int dev) {
     static std::mutex mu;
-    static bool ready[64][2][2][3];
+    static bool ready[64][2][2][2];
     if (dev < 0 || dev >= 64) return false;
-    const Kernel k = kernel_of(ctas, turned, cols);
+    const Kernel k = kernel_of(ctas, turned, col_vector);
     std::lock_guard<std::mutex> lock(mu);
-    bool& r = ready[dev][ctas - 1][turned][cols];
+    bool& r = ready[dev][ctas - 1][turned][col_vector];
     if (!r) {
         if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
             cudaGetLastError();
@@ -101,7 +101,6 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     if (ctas == 0) ctas = !turned && cdiv(p->M, 256) * cdiv(p->N, 256) >= 64 ? 2 : 1;
     if (turned && ctas == 2) return GEMM_ERR_UNSUPPORTED;
     const int64_t lanes = turned ? p->N : p->M, cols = turned ? p->M : p->N;
-    const bool l_block = (turned ? p->scale_b : p->scale_a) == GEMM_SCALE_BLOCK;
     const int tile = 128 * ctas;
     GroupedShape s{};
     s.groups = 1;
@@ -124,7 +123,7 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     s.may_split = (int64_t)s.units * s.kb < MAX_INDEX;
     p->ctas = ctas;
     p->turned = turned;
-    p->cols = !turned && p->scale_b == GEMM_SCALE_BLOCK ? 0 : l_block ? 1 : 2;
+    p->col_vector = turned || p->scale_b == GEMM_SCALE_VECTOR;
     p->width = (int)(cdiv(std::max<int64_t>(1, cdiv(cols, side)), s.step) * s.step);
     p->shape = s;
     p->counter_bytes = p->ws_bytes = 0;
@@ -295,8 +294,8 @@ gemm_status_t gemm_scaled_plan_get_info(gemm_scaled_plan_t p, int key, int64_t* 
         case GEMM_SCALED_INFO_TILES: *value = grouped_tiles(p->shape, p->shape.rows); break;
         case GEMM_SCALED_INFO_TILE_WIDTH: *value = p->width; break;
         case GEMM_SCALED_INFO_SHARES: *value = p->ws_bytes ? grouped_split(p->shape, grouped_tiles(p->shape, p->shape.rows), 0).shares : 1; break;
-        case GEMM_SCALED_INFO_STAGES: *value = kernel_of(p->ctas, p->turned, p->cols).stages; break;
-        case GEMM_SCALED_INFO_SMEM_BYTES: *value = kernel_of(p->ctas, p->turned, p->cols).smem; break;
+        case GEMM_SCALED_INFO_STAGES: *value = kernel_of(p->ctas, p->turned, p->col_vector).stages; break;
+        case GEMM_SCALED_INFO_SMEM_BYTES: *value = kernel_of(p->ctas, p->turned, p->col_vector).smem; break;
         default: return GEMM_ERR_INVALID_ARG;
     }
     return GEMM_OK;
@@ -324,7 +323,7 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (p->K == 0)  // empty sums: +0
         return cudaMemsetAsync(C, 0, (size_t)p->M * (size_t)p->N * (size_t)size, st) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
-    if (!prepared(p->ctas, p->turned, p->cols, p->device)) return GEMM_ERR_CUDA;
+    if (!prepared(p->ctas, p->turned, p->col_vector, p->device)) return GEMM_ERR_CUDA;
 
     const Side a = side_of(A, scales_a, p->M, p->K, p->layout_a == GEMM_ROW_MAJOR, p->scale_a);
     const Side b = side_of(B, scales_b, p->N, p->K, p->layout_b == GEMM_COL_MAJOR, p->scale_b);
@@ -337,16 +336,13 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     kp.out = C;
     kp.ldc = p->N;
     kp.out_dtype = p->out_dtype;
-    kp.boxes = !p->turned && !misaligned(C, 16) && p->N * size % 16 == 0;
+    kp.wide = !misaligned(C, 32) && p->N * size % 32 == 0;
     kp.l_mn = l.mn;
     kp.r_mn = r.mn;
     // The maps are encoded for every run: they cost well under a microsecond
     // of host time, and nothing is kept by an operand's address.
     ScaledMaps tm{};
     bool ok = encode_side(&tm.l, l, 128) && encode_side(&tm.r, r, (uint32_t)(p->width / p->ctas));
-    if (kp.boxes)
-        ok = ok && encode(&tm.c, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, size, C, p->N, p->M,
-                          (uint32_t)(128 / size), 32);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
     if (p->ws_bytes > 0) {
         kp.counters = reinterpret_cast<unsigned long long*>(workspace);
@@ -361,7 +357,7 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     // a wait may last as long as the longest tile's k-loop
     kp.pipe_limit_ns = 4000000000ull + 2000ull * (uint64_t)p->shape.kb;
 
-    const Kernel k = kernel_of(p->ctas, p->turned, p->cols);
+    const Kernel k = kernel_of(p->ctas, p->turned, p->col_vector);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p->shape.units * p->ctas), 1, 1);
     cfg.blockDim = dim3(S_THREADS, 1, 1);

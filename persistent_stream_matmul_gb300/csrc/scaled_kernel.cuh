@@ -17,17 +17,20 @@
 //             multiple of 16, so that 16 rows cost 16 columns, and 32 lanes store
 //             32 neighbours of a row of C.
 //
-// COLS, how a column's scale is had:
-//   0  R in blocks: one number for a half tile.
-//   1  a number a column, from shared memory; L's is the same for all lanes of the
-//      tile (blocks) and multiplied in there.
-//   2  as 1, but L has a number a lane: two operations an element.
+// COL_VECTOR: a scale a column (two operations an element) instead of one for 128 of
+// them (one operation, by the product with the lane's).
 //
-// PAIR: the two CTAs of a cluster run one tcgen05.mma.cta_group::2 of 256 x 256;
-// each CTA keeps its 128 lanes' L and half of R.  Without it, 128 x up to 128 a CTA.
+// PAIR: the two CTAs of a cluster run tcgen05.mma.cta_group::2 on a tile of 256 x 256;
+// each CTA keeps its 128 lanes' L and half of R.  A k-block is two products of 256 x
+// 128, one for each half of the epilogue, with their own buffers and barriers, so that
+// the halves run out of step: what one waits for is hidden by the other.  A pair's
+// product has 64 columns of each CTA's half of R, so half h has the tile's columns
+// 64h .. 64h + 63 and 128 + 64h .. 128 + 64h + 63.
+// Without PAIR, 128 x up to 128 a CTA, one product a k-block for both halves.
 //
 // Warp roles (384 threads, one CTA per SM) as in grouped_kernel.cuh: 0 copies, 1
-// issues the MMAs, 2 allocates tensor memory, 3 schedules, 4-11 are the epilogue,
+// issues the MMAs, 2 allocates tensor memory and then copies the scales of the k-blocks
+// ahead into a ring of their own, 3 schedules, 4-11 are the epilogue,
 // whose two halves have the two halves of a tile's columns.  Split tiles likewise:
 // partials in the workspace, the last contributor adds them in ascending k.
 //
@@ -42,30 +45,78 @@
 
 namespace psm {
 
-constexpr int S_THREADS = 384;
+#ifndef S_EPI_WARPS
+#define S_EPI_WARPS 8
+#endif
+#ifndef S_G
+#define S_G 8
+#endif
+constexpr int S_THREADS = 128 + 32 * S_EPI_WARPS;
 constexpr int S_BK = 128;
 constexpr int S_EPI_WARP0 = 4;
-constexpr int S_EPI_THREADS = 256;
+constexpr int S_EPI_THREADS = 32 * S_EPI_WARPS;
 constexpr int S_QUEUE = 4;
+constexpr int S_SLOTS = 2;       // of scales, S_G k-blocks each
+constexpr int S_COL_SCALES = 128 * 4;  // a k-block's: the lanes' scales, then the columns'
+#ifndef S_FMA
+#define S_FMA 1
+#endif
+#if S_FMA == 1
+#define S_ADD4(a, v, f, factor)                                                                                   \
+    {                                                                                                             \
+        uint64_t p0 = pack_f32x2((v)[0], (v)[1]), p1 = pack_f32x2((v)[2], (v)[3]);                                \
+        const uint64_t f0 = pack_f32x2((f).x, (f).y), f1 = pack_f32x2((f).z, (f).w), ff = pack_f32x2(factor, factor); \
+        uint64_t a0 = pack_f32x2((a)[0], (a)[1]), a1 = pack_f32x2((a)[2], (a)[3]);                                \
+        if constexpr (COL_VECTOR) {                                                                               \
+            a0 = fma_f32x2(mul_f32x2(p0, f0), ff, a0);                                                            \
+            a1 = fma_f32x2(mul_f32x2(p1, f1), ff, a1);                                                            \
+        } else {                                                                                                  \
+            a0 = fma_f32x2(p0, f0, a0);                                                                           \
+            a1 = fma_f32x2(p1, f1, a1);                                                                           \
+        }                                                                                                         \
+        const float2 x0 = unpack_f32x2(a0), x1 = unpack_f32x2(a1);                                                \
+        (a)[0] = x0.x; (a)[1] = x0.y; (a)[2] = x1.x; (a)[3] = x1.y;                                               \
+    }
+#else
+#define S_ADD4(a, v, f, factor)                                                                                   \
+    if constexpr (COL_VECTOR) {                                                                                   \
+        (a)[0] = fmaf(__uint_as_float((v)[0]) * (f).x, factor, (a)[0]);                                           \
+        (a)[1] = fmaf(__uint_as_float((v)[1]) * (f).y, factor, (a)[1]);                                           \
+        (a)[2] = fmaf(__uint_as_float((v)[2]) * (f).z, factor, (a)[2]);                                           \
+        (a)[3] = fmaf(__uint_as_float((v)[3]) * (f).w, factor, (a)[3]);                                           \
+    } else {                                                                                                      \
+        (a)[0] = fmaf(__uint_as_float((v)[0]), factor, (a)[0]);                                                   \
+        (a)[1] = fmaf(__uint_as_float((v)[1]), factor, (a)[1]);                                                   \
+        (a)[2] = fmaf(__uint_as_float((v)[2]), factor, (a)[2]);                                                   \
+        (a)[3] = fmaf(__uint_as_float((v)[3]), factor, (a)[3]);                                                   \
+    }
+#endif
+#ifndef S_CHUNK_V
+#define S_CHUNK_V 16
+#endif
+#ifndef S_CHUNK
+#define S_CHUNK 64
+#endif
 enum : uint32_t { S_BAR_EPI = 1, S_BAR_VOTE = 2 };
 
-template <bool PAIR, bool TURNED, int COLS>
+template <bool PAIR, bool TURNED, bool COL_VECTOR>
 struct ScaledCfg {
     static constexpr int CM = PAIR ? 2 : 1;
     static constexpr int TILE_N = 128 * CM;
-    static constexpr int HALF = TILE_N / 2;       // columns of an epilogue half at most
+    static constexpr int PART = TILE_N * 4 / S_EPI_WARPS;  // columns of an epilogue warp at most
     static constexpr int L_BYTES = 128 * S_BK;
     static constexpr int R_BYTES = 128 * S_BK;    // this CTA's columns
     static constexpr int STAGE_BYTES = L_BYTES + R_BYTES;
-    static constexpr int STAGES = COLS == 0 || TURNED ? 6 : 5;
-    static constexpr int BUFFERS = 512 / TILE_N;  // products in tensor memory
-    static constexpr int BOX_BYTES = TURNED ? 0 : 8 * 4096;              // a staged box a warp
-    static constexpr int SCALE_BYTES = COLS == 0 ? 0 : 8 * 2 * HALF * 4; // two k-blocks' a warp
+    static constexpr int STAGES = 6;
+    static constexpr int PRODUCTS = CM;           // products a k-block
+    static constexpr int BUFFERS = 4 / PRODUCTS;  // of each, 128 columns of tensor memory
+    static constexpr int SCALE_BYTES = S_COL_SCALES + (COL_VECTOR ? TILE_N * 4 : 16);  // of a k-block
+    static constexpr int SLOT_BYTES = S_G * SCALE_BYTES;
     static constexpr int QUEUE_BYTES = S_QUEUE * 48;
-    static constexpr int BAR_BYTES = 320;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BOX_BYTES + SCALE_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
+    static constexpr int BAR_BYTES = 384;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + S_SLOTS * SLOT_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
     static constexpr int SLOT_FLOATS = 128 * TILE_N;
-    static constexpr int BARS = 2 * STAGES + 2 * BUFFERS + 1 + 2 * S_QUEUE;
+    static constexpr int BARS = 2 * STAGES + 8 + 1 + 2 * S_QUEUE + 2 * S_SLOTS;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(BARS * 8 + 32 <= BAR_BYTES, "barrier area");
 };
@@ -85,7 +136,7 @@ struct ScaledParams {
     void* out;
     int64_t ldc;                  // elements of a row of C
     int32_t out_dtype;            // 0 f16, 1 bf16, 2 f32
-    int32_t boxes;                // straight: C is written by tensor copies
+    int32_t wide;                 // straight: every row of C starts at a 32-byte boundary
     int32_t l_mn, r_mn;           // operand is MN-major (the summed dimension is strided)
     float* partials;              // a slot a CTA
     unsigned long long* counters; // one a split tile and CTA of the pair
@@ -96,7 +147,7 @@ struct ScaledParams {
 };
 
 struct ScaledMaps {
-    CUtensorMap l, r, c;
+    CUtensorMap l, r;
 };
 
 // ---------------------------------------------------------------- instructions
@@ -118,8 +169,9 @@ __device__ __forceinline__ void mma_f8_ss_pair(uint32_t d_tmem, uint64_t a_desc,
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
-// 32 lanes x 16 columns, without the wait.
-__device__ __forceinline__ void tmem_ld_x16_async(uint32_t taddr, uint32_t (&r)[16]) {
+// 32 lanes x as many columns as there are registers: the load, and the wait for this
+// warp's loads, before which no use of the registers can be scheduled.
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -127,12 +179,103 @@ __device__ __forceinline__ void tmem_ld_x16_async(uint32_t taddr, uint32_t (&r)[
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-
-// Wait for this warp's loads; no use of the registers can be scheduled before it.
-__device__ __forceinline__ void tmem_wait_x16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+                   "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+                   "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+                   "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+                   "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63]));
+}
+
+// Four bytes global -> shared, asynchronously; and an arrival on a barrier (counted in
+// its expected ones) when all of this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// 32 bytes to global memory, a whole sector.
+__device__ __forceinline__ void st_u8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                      uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+                 "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
+// mbar_wait that also gives up once `stop` is set.
+__device__ __forceinline__ bool mbar_wait_unless(uint32_t bar, uint32_t parity, uint64_t limit_ns, const volatile int* stop) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*stop != 0 || globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 // Two fp32 values in a register pair, and their operations (each rounds to nearest).
@@ -197,30 +340,32 @@ __device__ __forceinline__ bool scaled_vote_all(bool v) {
     return out != 0;
 }
 
-template <bool PAIR, bool TURNED, int COLS>
+template <bool PAIR, bool TURNED, bool COL_VECTOR>
 __global__ void __launch_bounds__(S_THREADS, 1)
     scaled_kernel(const __grid_constant__ ScaledMaps tm, const __grid_constant__ ScaledParams p) {
-    using Cf = ScaledCfg<PAIR, TURNED, COLS>;
-    static_assert(!TURNED || (!PAIR && COLS > 0), "a turned tile's columns start anywhere");
-    constexpr int STAGES = Cf::STAGES, BUFFERS = Cf::BUFFERS, HALF = Cf::HALF;
+    using Cf = ScaledCfg<PAIR, TURNED, COL_VECTOR>;
+    static_assert(!TURNED || (!PAIR && COL_VECTOR), "a turned tile's columns start anywhere");
+    constexpr int STAGES = Cf::STAGES, BUFFERS = Cf::BUFFERS, PART = Cf::PART;
     constexpr uint16_t PAIR_MASK = 0x3;
     extern __shared__ uint8_t smem_raw[];
 
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
     const uint32_t ring = raw + pad;
-    const uint32_t boxes = ring + STAGES * Cf::STAGE_BYTES;
-    const uint32_t col_scales = boxes + Cf::BOX_BYTES;
-    const uint32_t queue = col_scales + Cf::SCALE_BYTES;
+    const uint32_t slots = ring + STAGES * Cf::STAGE_BYTES;
+    const uint32_t queue = slots + S_SLOTS * Cf::SLOT_BYTES;
     uint8_t* bar_area = smem_raw + (queue + Cf::QUEUE_BYTES - raw);
     const uint32_t bar_base = smem_addr(bar_area);
     auto full_bar = [&](int s) { return bar_base + 8u * s; };
     auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+    // buffer b of product h is number h * BUFFERS + b of the four
     auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
-    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + BUFFERS + b); };
-    const uint32_t done_bar = bar_base + 8u * (2 * STAGES + 2 * BUFFERS);
-    auto qfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 2 * BUFFERS + 1 + s); };
-    auto qempty_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 2 * BUFFERS + 1 + S_QUEUE + s); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + 4 + b); };
+    const uint32_t done_bar = bar_base + 8u * (2 * STAGES + 8);
+    auto qfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 9 + s); };
+    auto qempty_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 9 + S_QUEUE + s); };
+    auto sfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 9 + 2 * S_QUEUE + s); };
+    auto sempty_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 9 + 2 * S_QUEUE + S_SLOTS + s); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * Cf::BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 8 * Cf::BARS + 4);
     volatile int* last_flag = reinterpret_cast<volatile int*>(bar_area + 8 * Cf::BARS + 8);
@@ -236,13 +381,18 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        for (int b = 0; b < BUFFERS; ++b) {
+        for (int b = 0; b < 4; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), Cf::CM * S_EPI_THREADS / 32);
+            mbar_init(tempty_bar(b), Cf::CM / Cf::PRODUCTS * S_EPI_THREADS / 32);
         }
         mbar_init(done_bar, 1);
-        // readers of the queue: producer, issuer (pair: the first CTA's) and the epilogue warps
-        const int readers = 1 + (!PAIR || rank == 0) + S_EPI_THREADS / 32;
+        for (int s = 0; s < S_SLOTS; ++s) {
+            mbar_init(sfull_bar(s), 32);
+            mbar_init(sempty_bar(s), S_EPI_THREADS / 32);
+        }
+        // readers of the queue: producer, copier of the scales, issuer (pair: the first
+        // CTA's) and the epilogue warps
+        const int readers = 2 + (!PAIR || rank == 0) + S_EPI_THREADS / 32;
         for (int s = 0; s < S_QUEUE; ++s) {
             mbar_init(qfull_bar(s), 1);
             mbar_init(qempty_bar(s), readers);
@@ -280,13 +430,14 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         atomicCAS(p.status + G_WORD_STATUS, 0, G_STATUS_PIPE_TIMEOUT);
     };
 
+    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, p.pipe_limit_ns, abort_flag); };
     GroupedWork w{};
     int qslot = 0;
     uint32_t qphase = 0;
     // The next piece of work, for a whole warp; false at the end or after a
     // wait that ran out.
     auto next_work = [&]() {
-        const bool got = mbar_wait(qfull_bar(qslot), qphase, p.pipe_limit_ns);
+        const bool got = wait(qfull_bar(qslot), qphase);
         if (!__all_sync(0xffffffffu, got && *abort_flag == 0)) {
             if (lane == 0) fail_pipe();
             return false;
@@ -305,7 +456,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     };
 
     if (warp < S_EPI_WARP0) {
-        if constexpr (PAIR) registers_fewer<72>();
+        if constexpr (PAIR) registers_fewer<(S_EPI_WARPS == 16 ? 64 : 72)>();
         if (warp == 0) {
             // -------------------------------------------------------- producer
             int stage = 0;
@@ -319,7 +470,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 const int r0 = w.n0 + rank * cols;
                 const uint32_t r_bytes = p.r_mn ? (uint32_t)Cf::R_BYTES : (uint32_t)cols * S_BK;
                 for (int kb = w.k0; kb < w.k1; ++kb) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.pipe_limit_ns))) {
+                    if (!__all_sync(0xffffffffu, wait(empty_bar(stage), phase ^ 1u))) {
                         if (lane == 0) fail_pipe();
                         ok = false;
                         break;
@@ -364,36 +515,46 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 // 32 elements of the summed dimension: bytes of a row, or 32 rows of 128 bytes
                 const uint64_t l_step = p.l_mn ? (32 * 128) >> 4 : 32 >> 4;
                 const uint64_t r_step = p.r_mn ? (32 * 128) >> 4 : 32 >> 4;
+                // 64 columns: of 128 bytes a row, or rows of 128 bytes
+                const uint64_t r_part = p.r_mn ? 64 >> 4 : (64 * 128) >> 4;
                 while (ok && next_work()) {
-                    const uint32_t idesc = p.idesc | ((uint32_t)(w.width >> 3) << 17);
+                    const uint32_t idesc = p.idesc | ((uint32_t)(w.width / Cf::PRODUCTS >> 3) << 17);
                     for (int kb = w.k0; kb < w.k1; ++kb) {
-                        const bool got = mbar_wait(tempty_bar(buf), tphase ^ 1u, p.pipe_limit_ns) &&
-                                         mbar_wait(full_bar(stage), phase, p.pipe_limit_ns) && *abort_flag == 0;
-                        if (!__all_sync(0xffffffffu, got)) {
-                            if (lane == 0) fail_pipe();
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after_sync();
-                        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * Cf::TILE_N);
-                        if (elect_one()) {
-                            const uint64_t at = (uint64_t)((uint32_t)(stage * Cf::STAGE_BYTES) >> 4);
+                        // the barriers' states are asked for together, as each answer takes
+                        // some hundred cycles, and waited for where one is not ready
+                        bool here = mbar_test(full_bar(stage), phase);
+                        bool free[Cf::PRODUCTS];
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const uint64_t ld = l_desc0 + at + (uint64_t)kk * l_step;
-                                const uint64_t rd = r_desc0 + at + (uint64_t)kk * r_step;
-                                if constexpr (PAIR) mma_f8_ss_pair(d_tmem, ld, rd, idesc, kk > 0);
-                                else mma_f8_ss(d_tmem, ld, rd, idesc, kk > 0);
+                        for (int h = 0; h < Cf::PRODUCTS; ++h) free[h] = mbar_test(tempty_bar(h * BUFFERS + buf), tphase ^ 1u);
+                        if (!here) here = wait(full_bar(stage), phase);
+                        const uint64_t at = (uint64_t)((uint32_t)(stage * Cf::STAGE_BYTES) >> 4);
+#pragma unroll
+                        for (int h = 0; h < Cf::PRODUCTS; ++h) {
+                            const int b = h * BUFFERS + buf;
+                            if (!free[h]) here = here && wait(tempty_bar(b), tphase ^ 1u);
+                            ok = ok && __all_sync(0xffffffffu, here);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            if (elect_one()) {
+                                const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    const uint64_t ld = l_desc0 + at + (uint64_t)kk * l_step;
+                                    const uint64_t rd = r_desc0 + at + (uint64_t)h * r_part + (uint64_t)kk * r_step;
+                                    if constexpr (PAIR) mma_f8_ss_pair(d_tmem, ld, rd, idesc, kk > 0);
+                                    else mma_f8_ss(d_tmem, ld, rd, idesc, kk > 0);
+                                }
+                                if constexpr (PAIR) {
+                                    mma_commit_pair_multicast(tfull_bar(b), PAIR_MASK);
+                                    if (h == Cf::PRODUCTS - 1) mma_commit_pair_multicast(empty_bar(stage), PAIR_MASK);
+                                } else {
+                                    mma_commit(tfull_bar(b));
+                                    mma_commit(empty_bar(stage));
+                                }
                             }
-                            if constexpr (PAIR) {
-                                mma_commit_pair_multicast(empty_bar(stage), PAIR_MASK);
-                                mma_commit_pair_multicast(tfull_bar(buf), PAIR_MASK);
-                            } else {
-                                mma_commit(empty_bar(stage));
-                                mma_commit(tfull_bar(buf));
-                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (!ok) break;
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -403,6 +564,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                             tphase ^= 1u;
                         }
                     }
+                    if (!ok && lane == 0) fail_pipe();
                 }
                 // all MMAs are complete before tensor memory is freed
                 __syncwarp();
@@ -413,6 +575,56 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 __syncwarp();
                 mbar_wait(done_bar, 0, p.pipe_limit_ns);
             }
+        } else if (warp == 2) {
+            // -------------------------------------------------------- scales
+            // four bytes a copy: rows of scales start anywhere
+            int slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            constexpr int PER = COL_VECTOR ? Cf::TILE_N / 32 : 1;
+            while (ok && next_work()) {
+                const float* ls[4];
+                const float* rs[PER];
+                // rows and columns past the end read the last one's
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int l = min((w.tm * Cf::CM + rank) * 128 + i * 32 + lane, p.l.rows - 1);
+                    ls[i] = p.l.s + (int64_t)(l >> p.l.shift) * p.l.row + (int64_t)w.k0 * p.l.group;
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int c = min(w.n0 + (COL_VECTOR ? i * 32 + lane : (lane & (Cf::CM - 1)) * 128), p.r.rows - 1);
+                    rs[i] = p.r.s + (int64_t)(c >> p.r.shift) * p.r.row + (int64_t)w.k0 * p.r.group;
+                }
+                for (int kb0 = w.k0; kb0 < w.k1; kb0 += S_G) {
+                    if (!__all_sync(0xffffffffu, wait(sempty_bar(slot), phase ^ 1u))) {
+                        if (lane == 0) fail_pipe();
+                        ok = false;
+                        break;
+                    }
+                    uint32_t at = slots + (uint32_t)(slot * Cf::SLOT_BYTES) + (uint32_t)lane * 4;
+#pragma unroll 1
+                    for (int kb = kb0; kb < min(kb0 + S_G, w.k1); ++kb) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            cp_async_4(at + i * 128, ls[i]);
+                            ls[i] += p.l.group;
+                        }
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            if (COL_VECTOR ? i * 32 < w.width : lane < Cf::CM) cp_async_4(at + S_COL_SCALES + i * 128, rs[i]);
+                            rs[i] += p.r.group;
+                        }
+                        at += Cf::SCALE_BYTES;
+                    }
+                    cp_async_arrive(sfull_bar(slot));
+                    if (++slot == S_SLOTS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            cp_async_wait_all();  // the copies are complete before the CTA ends
         } else if (warp == 3) {
             // -------------------------------------------------------- scheduler
             const uint64_t tag = grouped_tag(p.epoch, p.status);
@@ -423,7 +635,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             for (int32_t step = 0; more; ++step) {
                 more = grouped_work(p.s, tab, split, unit, step, items, w);
                 if (!more) w.item = -1;
-                if (!__all_sync(0xffffffffu, mbar_wait(qempty_bar(qslot), qphase ^ 1u, p.pipe_limit_ns))) {
+                if (!__all_sync(0xffffffffu, wait(qempty_bar(qslot), qphase ^ 1u))) {
                     if (lane == 0) fail_pipe();
                     break;
                 }
@@ -445,127 +657,110 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if constexpr (PAIR) registers_more<216>();
+        if constexpr (PAIR) registers_more<(S_EPI_WARPS == 16 ? 104 : 216)>();
         const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
-        const int half = (warp - S_EPI_WARP0) >> 2;
+        const int part = (warp - S_EPI_WARP0) >> 2;
         const int et = threadIdx.x - S_EPI_WARP0 * 32;
         const uint64_t tag = grouped_tag(p.epoch, p.status);
         const bool give_up = p.status[G_WORD_GIVE_UP] == unit + 1;
-        const uint32_t my_scales = col_scales + (uint32_t)(warp - S_EPI_WARP0) * (2 * HALF * 4);
-        const uint32_t my_box = boxes + (uint32_t)(warp - S_EPI_WARP0) * 4096u;
-        const uint32_t release0 = PAIR ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
-        constexpr int PER = HALF / 32;  // column scales a lane fetches
-        constexpr int VALUES = COLS == 0 ? 2 : 1 + PER;
-        int buf = 0;
-        uint32_t tphase = 0;
+        constexpr int PARTS = S_EPI_WARPS / 4;
+        constexpr bool WHOLE = PAIR && PARTS == 2;  // a part reads a product, else half of one
+        const int first_buf = PAIR ? (WHOLE ? part : part >> 1) * BUFFERS : 0;
+        const uint32_t full0 = tfull_bar(first_buf);
+        const uint32_t release0 = PAIR ? mapa_shared(tempty_bar(first_buf), 0) : tempty_bar(0);
+        constexpr int CHUNK = !PAIR ? 16 : COL_VECTOR ? S_CHUNK_V : S_CHUNK;  // columns a load from tensor memory
+        int buf = 0, slot = 0;
+        uint32_t tphase = 0, sphase = 0;
         while (next_work()) {
-            // this half's columns: c0 .. c0 + 16 * chunks - 1 of the tile
-            const int half_width = PAIR ? HALF : ((w.width >> 1) + 15) & ~15;
-            const int c0 = half * half_width;
-            const int chunks = PAIR ? HALF / 16 : max(0, min(w.width - c0, half_width)) >> 4;
+            // this warp's columns: c0 .. c0 + CHUNK * chunks - 1 of the tile, from t0 on of
+            // a product's in tensor memory
+            const int wide = PAIR ? PART : (w.width / PARTS + 15) & ~15;
+            const int c0 = WHOLE ? part * 64 : PAIR ? (part >> 1) * 64 + (part & 1) * 128 : part * wide;
+            const int t0 = WHOLE ? 0 : PAIR ? (part & 1) * 64 : c0;
+            const int chunks = PAIR ? PART / CHUNK : max(0, min(w.width - c0, wide)) >> 4;
             const int l = (w.tm * Cf::CM + rank) * 128 + q * 32 + lane;
-            // the scales' addresses; rows and columns past the end read the last one's
-            const float* ls = p.l.s + (int64_t)(min(l, p.l.rows - 1) >> p.l.shift) * p.l.row;
-            const float* rs[COLS == 0 ? 1 : PER];
-            if constexpr (COLS == 0) {
-                rs[0] = p.r.s + (int64_t)(min(w.n0 + c0, p.r.rows - 1) >> p.r.shift) * p.r.row;
-            } else {
+            float acc[PART];
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    rs[i] = p.r.s + (int64_t)(min(w.n0 + c0 + lane * PER + i, p.r.rows - 1) >> p.r.shift) * p.r.row;
-            }
-            // fetched two k-blocks ahead
-            float now[VALUES], next[VALUES], after[VALUES];
-            auto fetch = [&](int kb, float (&v)[VALUES]) {
-                const int64_t g = min(kb, w.k1 - 1);
-                v[0] = ls[g * p.l.group];
-#pragma unroll
-                for (int i = 0; i < VALUES - 1; ++i) v[1 + i] = rs[i][g * p.r.group];
-            };
-            uint64_t acc[HALF / 2];
-#pragma unroll
-            for (int i = 0; i < HALF / 2; ++i) acc[i] = 0;
-            fetch(w.k0, now);
-            fetch(w.k0 + 1, next);
+            for (int i = 0; i < PART; ++i) acc[i] = 0.f;
             bool ok = !give_up;
+            int turn = 0;  // the k-block's place in its slot of scales
+            // the answer whether a product is there is asked for before the sums of the one
+            // before, as it takes some hundred cycles
+            bool here = mbar_test(full0 + 8u * (uint32_t)buf, tphase);
+            uint32_t my_scales = 0;
 #pragma unroll 1
             for (int kb = w.k0; kb < w.k1; ++kb) {
-                fetch(kb + 2, after);
-                uint64_t factor;
-                const uint32_t scales_at = my_scales + (uint32_t)(kb & 1) * (HALF * 4);
-                if constexpr (COLS == 0) {
-                    const float f = now[0] * now[1];
-                    factor = pack_f32x2(f, f);
-                } else {
-                    factor = pack_f32x2(now[0], now[0]);
-                    const float with = COLS == 1 ? now[0] : 1.f;
-#pragma unroll
-                    for (int i = 0; i < PER; i += 2)
-                        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(scales_at + (uint32_t)(lane * PER + i) * 4),
-                                     "f"(now[1 + i] * with), "f"(now[2 + i] * with)
-                                     : "memory");
-                    __syncwarp();
+                if (turn == 0) {
+                    ok = ok && wait(sfull_bar(slot), sphase);
+                    my_scales = slots + (uint32_t)(slot * Cf::SLOT_BYTES);
                 }
-                const bool got = mbar_wait(tfull_bar(buf), tphase, p.pipe_limit_ns) && *abort_flag == 0;
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
+                if (!here) ok = ok && wait(full0 + 8u * (uint32_t)buf, tphase);
+                __syncwarp();
                 tc_fence_after_sync();
-                const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * Cf::TILE_N + c0);
-                // two chunks of 16 columns in turn: one is loaded while the other is added
-                uint32_t v[2][16];
-                if (chunks > 0) tmem_ld_x16_async(tbase, v[0]);
+                const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((first_buf + buf) * 128 + t0);
+                // the lane's scale, or its products with those of the columns
+                const uint32_t my_cols = my_scales + S_COL_SCALES + (uint32_t)c0 * 4;
+                float factors[WHOLE ? 2 : 1];
+                auto release = [&]() {  // the product has been read
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) mbar_arrive_cluster_fenced(release0 + 8u * (uint32_t)buf);
+                        else mbar_arrive(release0 + 8u * (uint32_t)buf);
+                    }
+                    if (++buf == BUFFERS) {
+                        buf = 0;
+                        tphase ^= 1u;
+                    }
+                    here = mbar_test(full0 + 8u * (uint32_t)buf, tphase);
+                };
 #pragma unroll
-                for (int c = 0; c < HALF / 16; ++c) {
+                for (int c = 0; c < PART / CHUNK; ++c) {
                     if (c < chunks) {
-                        tmem_wait_x16(v[c & 1]);
-                        if (c + 1 < HALF / 16 && c + 1 < chunks) tmem_ld_x16_async(tbase + (c + 1) * 16, v[(c + 1) & 1]);
+                        uint32_t v[CHUNK];
+                        tmem_ld_async(tbase + c * CHUNK, v);
+                        if (c == 0) {
+                            const float mine = ld_shared_f1(my_scales + (uint32_t)(q * 32 + lane) * 4);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint64_t f[2] = {factor, factor};
-                            if constexpr (COLS > 0) {
-                                const float4 s = ld_shared_f4(scales_at + (uint32_t)(c * 16 + i * 4) * 4);
-                                f[0] = pack_f32x2(s.x, s.y);
-                                f[1] = pack_f32x2(s.z, s.w);
+                            for (int i = 0; i < (WHOLE ? 2 : 1); ++i) {
+                                factors[i] = mine;
+                                if constexpr (!COL_VECTOR) factors[i] *= ld_shared_f1(my_scales + S_COL_SCALES + (uint32_t)((c0 >> 7) + i) * 4);
                             }
+                        }
+                        tmem_wait(v);
+                        if (PAIR && c == PART / CHUNK - 1) release();
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                uint64_t& a = acc[c * 8 + i * 2 + j];
-                                const uint64_t product = pack_f32x2(v[c & 1][i * 4 + j * 2], v[c & 1][i * 4 + j * 2 + 1]);
-                                if constexpr (COLS == 2) a = fma_f32x2(mul_f32x2(product, f[j]), factor, a);
-                                else a = fma_f32x2(product, f[j], a);
-                            }
+                        for (int i = 0; i < CHUNK; i += 4) {
+                            const int at = c * CHUNK + i;
+                            const float factor = factors[WHOLE && at >= 64 ? 1 : 0];
+                            float4 f = make_float4(factor, factor, factor, factor);
+                            if constexpr (COL_VECTOR) f = ld_shared_f4(my_cols + (uint32_t)(at + (WHOLE && at >= 64 ? 64 : 0)) * 4);
+                            float* a = acc + c * CHUNK + i;
+                            S_ADD4(a, v + i, f, factor);
                         }
                     }
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_cluster_fenced(release0 + 8u * (uint32_t)buf);
-                    else mbar_arrive(release0 + 8u * (uint32_t)buf);
-                }
-                if (++buf == BUFFERS) {
-                    buf = 0;
-                    tphase ^= 1u;
-                }
-#pragma unroll
-                for (int i = 0; i < VALUES; ++i) {
-                    now[i] = next[i];
-                    next[i] = after[i];
+                if (!PAIR) release();
+                my_scales += Cf::SCALE_BYTES;
+                if (++turn == S_G || kb == w.k1 - 1) {
+                    turn = 0;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty_bar(slot));
+                    if (++slot == S_SLOTS) {
+                        slot = 0;
+                        sphase ^= 1u;
+                    }
                 }
             }
             if (!ok && lane == 0) fail_pipe();
             // (a warp that gives up must not leave the others at a barrier)
             if (!scaled_vote_all(ok)) break;
             if (w.shares > 1) {
-                float4* slot = reinterpret_cast<float4*>(p.partials + (size_t)blockIdx.x * Cf::SLOT_FLOATS);
+                float4* mine = reinterpret_cast<float4*>(p.partials + (size_t)blockIdx.x * Cf::SLOT_FLOATS) + et;
 #pragma unroll
-                for (int i = 0; i < HALF / 4; ++i)
-                    if (i < chunks * 4) {
-                        const float2 a = unpack_f32x2(acc[2 * i]), b = unpack_f32x2(acc[2 * i + 1]);
-                        st_f4(slot + i * S_EPI_THREADS + et, make_float4(a.x, a.y, b.x, b.y));
-                    }
+                for (int i = 0; i < PART / 4; ++i)
+                    if (i < chunks * (CHUNK / 4))
+                        st_f4(mine + i * S_EPI_THREADS, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
                 // the barrier orders the partial's stores before the count, a release
                 // and acquire at GPU scope
                 named_bar_sync(S_BAR_EPI, S_EPI_THREADS);
@@ -576,94 +771,70 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 named_bar_sync(S_BAR_EPI, S_EPI_THREADS);
                 if (!last) continue;
 #pragma unroll
-                for (int i = 0; i < HALF / 2; ++i) acc[i] = 0;
+                for (int i = 0; i < PART; ++i) acc[i] = 0.f;
 #pragma unroll 1
                 for (int x = 0; x < w.shares; ++x) {
                     // share x was run by unit w.item + x
                     const float4* from = reinterpret_cast<const float4*>(
                         p.partials + (size_t)((w.item + x) * Cf::CM + rank) * Cf::SLOT_FLOATS) + et;
-                    const uint64_t one = pack_f32x2(1.f, 1.f);
 #pragma unroll
-                    for (int i = 0; i < HALF / 4; ++i)
-                        if (i < chunks * 4) {
+                    for (int i = 0; i < PART / 4; ++i)
+                        if (i < chunks * (CHUNK / 4)) {
                             const float4 y = ld_cg_f4(from + i * S_EPI_THREADS);
-                            acc[2 * i] = fma_f32x2(pack_f32x2(y.x, y.y), one, acc[2 * i]);
-                            acc[2 * i + 1] = fma_f32x2(pack_f32x2(y.z, y.w), one, acc[2 * i + 1]);
+                            acc[4 * i] += y.x;
+                            acc[4 * i + 1] += y.y;
+                            acc[4 * i + 2] += y.z;
+                            acc[4 * i + 3] += y.w;
                         }
                 }
             }
             // ---- the tile to C
-            const int row0 = l - lane;
+            if (l >= p.l_total) continue;
             if constexpr (TURNED) {
-                const int count = min(w.valid - c0, chunks * 16);  // columns with a row of C
-                if (l < p.l_total) {
-                    const int64_t at = (int64_t)(w.n0 + c0) * p.ldc + l;
+                const int count = min(w.valid - c0, chunks * CHUNK);  // columns with a row of C
+                const int64_t at = (int64_t)(w.n0 + c0) * p.ldc + l;
 #pragma unroll
-                    for (int i = 0; i < HALF / 2; ++i) {
-                        const float2 x = unpack_f32x2(acc[i]);
-                        if (2 * i < count) scaled_store(p.out, p.out_dtype, at + (int64_t)(2 * i) * p.ldc, x.x);
-                        if (2 * i + 1 < count) scaled_store(p.out, p.out_dtype, at + (int64_t)(2 * i + 1) * p.ldc, x.y);
-                    }
-                }
-            } else if (p.boxes) {
-                // boxes of 32 rows x 128 bytes, 16-byte units swizzled by row
-                const uint32_t my_row = my_box + (uint32_t)lane * 128u;
-                const int col = w.n0 + c0;
-                auto send = [&](int x) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (x < (int)p.ldc && row0 < p.l_total) tma_store_2d(&tm.c, my_box, x, row0);
-                        bulk_commit_group();
-                    }
-                };
-                auto free_box = [&]() {
-                    if (lane == 0) bulk_wait_group_read_0();
-                    __syncwarp();
-                };
+                for (int i = 0; i < PART; ++i)
+                    if (i < count) scaled_store(p.out, p.out_dtype, at + (int64_t)i * p.ldc, acc[i]);
+            } else {
+                const int64_t at = (int64_t)l * p.ldc + w.n0 + c0;
                 if (p.out_dtype == 2) {
+                    float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
-                    for (int b = 0; b < HALF / 32; ++b) {
-                        free_box();
+                    for (int i = 0; i < PART; i += 8) {
+                        const int c = i + (WHOLE && i >= 64 ? 64 : 0);
+                        const int count = w.valid - c0 - c;
+                        if (p.wide && count >= 8) {
+                            st_u8(out + c, __float_as_uint(acc[i]), __float_as_uint(acc[i + 1]), __float_as_uint(acc[i + 2]),
+                                  __float_as_uint(acc[i + 3]), __float_as_uint(acc[i + 4]), __float_as_uint(acc[i + 5]),
+                                  __float_as_uint(acc[i + 6]), __float_as_uint(acc[i + 7]));
+                        } else {
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const float2 x = unpack_f32x2(acc[b * 16 + 2 * u]), y = unpack_f32x2(acc[b * 16 + 2 * u + 1]);
-                            st_shared_u4(my_row + (uint32_t)((u ^ (lane & 7)) * 16), __float_as_uint(x.x), __float_as_uint(x.y),
-                                         __float_as_uint(y.x), __float_as_uint(y.y));
+                            for (int j = 0; j < 8; ++j)
+                                if (j < count) out[c + j] = acc[i + j];
                         }
-                        send(col + b * 32);
                     }
                 } else {
                     const bool bf16 = p.out_dtype == 1;
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
 #pragma unroll
-                    for (int b = 0; b < HALF / 64; ++b) {
-                        free_box();
+                    for (int i = 0; i < PART; i += 16) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            uint32_t o[4];
+                        for (int j = 0; j < 8; ++j) o[j] = scaled_pack2(bf16, acc[i + 2 * j], acc[i + 2 * j + 1]);
+                        const int c = i + (WHOLE && i >= 64 ? 64 : 0);
+                        const int count = w.valid - c0 - c;
+                        if (p.wide && count >= 16) {
+                            st_u8(out + c, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+                        } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 x = unpack_f32x2(acc[b * 32 + 4 * u + i]);
-                                o[i] = scaled_pack2(bf16, x.x, x.y);
-                            }
-                            st_shared_u4(my_row + (uint32_t)((u ^ (lane & 7)) * 16), o[0], o[1], o[2], o[3]);
+                            for (int j = 0; j < 16; ++j)
+                                if (j < count) out[c + j] = (uint16_t)(o[j / 2] >> (16 * (j & 1)));
                         }
-                        send(col + b * 64);
                     }
-                }
-            } else if (l < p.l_total) {
-                // rows of C that tensor copies cannot address: element by element
-                const int64_t at = (int64_t)l * p.ldc + w.n0 + c0;
-                const int64_t count = p.ldc - (w.n0 + c0);
-#pragma unroll
-                for (int i = 0; i < HALF / 2; ++i) {
-                    const float2 x = unpack_f32x2(acc[i]);
-                    if (2 * i < count) scaled_store(p.out, p.out_dtype, at + 2 * i, x.x);
-                    if (2 * i + 1 < count) scaled_store(p.out, p.out_dtype, at + 2 * i + 1, x.y);
                 }
             }
         }
-        if (lane == 0) bulk_wait_group_0();  // the copies are complete before the CTA ends
     }
 
     tc_fence_before_sync();
