@@ -91,6 +91,12 @@ constexpr int S_COL_SCALES = 128 * 4;  // a k-block's: the lanes' scales, then t
         (a)[3] = fmaf(__uint_as_float((v)[3]), factor, (a)[3]);                                                   \
     }
 #endif
+#ifndef S_EPI_REGS
+#define S_EPI_REGS 216
+#endif
+#ifndef S_UNROLL
+#define S_UNROLL 1
+#endif
 #ifndef S_CHUNK_V
 #define S_CHUNK_V 16
 #endif
@@ -278,6 +284,15 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// Arrivals by one lane without a branch, where the warp has run into them together.
+__device__ __forceinline__ void mbar_arrive_if(bool one, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"((uint32_t)one), "r"(bar) : "memory");
+}
+// (As mbar_arrive_cluster_fenced.)
+__device__ __forceinline__ void mbar_arrive_cluster_if(bool one, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%1];\n\t}" ::"r"((uint32_t)one), "r"(bar) : "memory");
+}
+
 // Two fp32 values in a register pair, and their operations (each rounds to nearest).
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
     uint64_t v;
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     };
 
     if (warp < S_EPI_WARP0) {
-        if constexpr (PAIR) registers_fewer<(S_EPI_WARPS == 16 ? 64 : 72)>();
+        if constexpr (PAIR) registers_fewer<(S_EPI_WARPS == 16 ? 64 : 504 - 2 * S_EPI_REGS)>();
         if (warp == 0) {
             // -------------------------------------------------------- producer
             int stage = 0;
@@ -528,33 +543,42 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                         for (int h = 0; h < Cf::PRODUCTS; ++h) free[h] = mbar_test(tempty_bar(h * BUFFERS + buf), tphase ^ 1u);
                         if (!here) here = wait(full_bar(stage), phase);
                         const uint64_t at = (uint64_t)((uint32_t)(stage * Cf::STAGE_BYTES) >> 4);
-#pragma unroll
-                        for (int h = 0; h < Cf::PRODUCTS; ++h) {
+                        auto issue = [&](int h) {  // one lane
                             const int b = h * BUFFERS + buf;
-                            if (!free[h]) here = here && wait(tempty_bar(b), tphase ^ 1u);
-                            ok = ok && __all_sync(0xffffffffu, here);
+                            const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint64_t ld = l_desc0 + at + (uint64_t)kk * l_step;
+                                const uint64_t rd = r_desc0 + at + (uint64_t)h * r_part + (uint64_t)kk * r_step;
+                                if constexpr (PAIR) mma_f8_ss_pair(d_tmem, ld, rd, idesc, kk > 0);
+                                else mma_f8_ss(d_tmem, ld, rd, idesc, kk > 0);
+                            }
+                            if constexpr (PAIR) {
+                                mma_commit_pair_multicast(tfull_bar(b), PAIR_MASK);
+                                if (h == Cf::PRODUCTS - 1) mma_commit_pair_multicast(empty_bar(stage), PAIR_MASK);
+                            } else {
+                                mma_commit(tfull_bar(b));
+                                mma_commit(empty_bar(stage));
+                            }
+                        };
+                        if (!free[0]) here = here && wait(tempty_bar(buf), tphase ^ 1u);
+                        const bool both = PAIR && free[Cf::PRODUCTS - 1];
+                        ok = __all_sync(0xffffffffu, here);
+                        if (!ok) break;
+                        const bool at_once = __all_sync(0xffffffffu, both);
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            issue(0);
+                            if (PAIR && at_once) issue(Cf::PRODUCTS - 1);
+                        }
+                        __syncwarp();
+                        if (PAIR && !at_once) {
+                            ok = __all_sync(0xffffffffu, wait(tempty_bar((Cf::PRODUCTS - 1) * BUFFERS + buf), tphase ^ 1u));
                             if (!ok) break;
                             tc_fence_after_sync();
-                            if (elect_one()) {
-                                const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    const uint64_t ld = l_desc0 + at + (uint64_t)kk * l_step;
-                                    const uint64_t rd = r_desc0 + at + (uint64_t)h * r_part + (uint64_t)kk * r_step;
-                                    if constexpr (PAIR) mma_f8_ss_pair(d_tmem, ld, rd, idesc, kk > 0);
-                                    else mma_f8_ss(d_tmem, ld, rd, idesc, kk > 0);
-                                }
-                                if constexpr (PAIR) {
-                                    mma_commit_pair_multicast(tfull_bar(b), PAIR_MASK);
-                                    if (h == Cf::PRODUCTS - 1) mma_commit_pair_multicast(empty_bar(stage), PAIR_MASK);
-                                } else {
-                                    mma_commit(tfull_bar(b));
-                                    mma_commit(empty_bar(stage));
-                                }
-                            }
+                            if (elect_one()) issue(Cf::PRODUCTS - 1);
                             __syncwarp();
                         }
-                        if (!ok) break;
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -657,7 +681,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if constexpr (PAIR) registers_more<(S_EPI_WARPS == 16 ? 104 : 216)>();
+        if constexpr (PAIR) registers_more<(S_EPI_WARPS == 16 ? 104 : S_EPI_REGS)>();
         const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
         const int part = (warp - S_EPI_WARP0) >> 2;
         const int et = threadIdx.x - S_EPI_WARP0 * 32;
@@ -683,31 +707,22 @@ __global__ void __launch_bounds__(S_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < PART; ++i) acc[i] = 0.f;
             bool ok = !give_up;
-            int turn = 0;  // the k-block's place in its slot of scales
+            const uint32_t tmem_lanes = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(first_buf * 128 + t0);
             // the answer whether a product is there is asked for before the sums of the one
             // before, as it takes some hundred cycles
             bool here = mbar_test(full0 + 8u * (uint32_t)buf, tphase);
-            uint32_t my_scales = 0;
-#pragma unroll 1
-            for (int kb = w.k0; kb < w.k1; ++kb) {
-                if (turn == 0) {
-                    ok = ok && wait(sfull_bar(slot), sphase);
-                    my_scales = slots + (uint32_t)(slot * Cf::SLOT_BYTES);
-                }
+            auto block = [&](uint32_t my_scales) {
                 if (!here) ok = ok && wait(full0 + 8u * (uint32_t)buf, tphase);
                 __syncwarp();
                 tc_fence_after_sync();
-                const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((first_buf + buf) * 128 + t0);
+                const uint32_t tbase = tmem_lanes + (uint32_t)(buf * 128);
                 // the lane's scale, or its products with those of the columns
                 const uint32_t my_cols = my_scales + S_COL_SCALES + (uint32_t)c0 * 4;
                 float factors[WHOLE ? 2 : 1];
-                auto release = [&]() {  // the product has been read
+                auto release = [&]() {  // the product has been read, by all lanes (wait::ld is the warp's)
                     tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR) mbar_arrive_cluster_fenced(release0 + 8u * (uint32_t)buf);
-                        else mbar_arrive(release0 + 8u * (uint32_t)buf);
-                    }
+                    if constexpr (PAIR) mbar_arrive_cluster_if(lane == 0, release0 + 8u * (uint32_t)buf);
+                    else mbar_arrive_if(lane == 0, release0 + 8u * (uint32_t)buf);
                     if (++buf == BUFFERS) {
                         buf = 0;
                         tphase ^= 1u;
@@ -741,15 +756,28 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     }
                 }
                 if (!PAIR) release();
-                my_scales += Cf::SCALE_BYTES;
-                if (++turn == S_G || kb == w.k1 - 1) {
-                    turn = 0;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sempty_bar(slot));
-                    if (++slot == S_SLOTS) {
-                        slot = 0;
-                        sphase ^= 1u;
+            };
+#pragma unroll 1
+            for (int kb0 = w.k0; kb0 < w.k1; kb0 += S_G) {
+                ok = ok && wait(sfull_bar(slot), sphase);
+                uint32_t my_scales = slots + (uint32_t)(slot * Cf::SLOT_BYTES);
+                const int n = min(S_G, w.k1 - kb0);
+                if (S_UNROLL > 1 && n == S_G) {
+#pragma unroll 1
+                    for (int i = 0; i < S_G; i += S_UNROLL) {
+#pragma unroll
+                        for (int u = 0; u < S_UNROLL; ++u) block(my_scales + u * Cf::SCALE_BYTES);
+                        my_scales += S_UNROLL * Cf::SCALE_BYTES;
                     }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i, my_scales += Cf::SCALE_BYTES) block(my_scales);
+                }
+                __syncwarp();
+                mbar_arrive_if(lane == 0, sempty_bar(slot));
+                if (++slot == S_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1u;
                 }
             }
             if (!ok && lane == 0) fail_pipe();
