@@ -191,8 +191,9 @@ gemm_status_t make_plan(gemm_scaled_plan_t* out, int64_t M, int64_t N, int64_t K
     return GEMM_OK;
 }
 
-// 128-byte-swizzled map of a matrix of y rows of x elements.
-bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, int64_t x, int64_t y, uint32_t box_x, uint32_t box_y) {
+// Map of a matrix of y rows of x elements.
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, int64_t x, int64_t y, uint32_t box_x, uint32_t box_y,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)x, (cuuint64_t)y};
@@ -200,7 +201,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base
     const cuuint32_t box[2] = {box_x, box_y};
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // One operand, as the lanes or the columns side sees it: `rows` of K elements.
@@ -336,13 +337,16 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     kp.out = C;
     kp.ldc = p->N;
     kp.out_dtype = p->out_dtype;
-    kp.wide = !misaligned(C, 32) && p->N * size % 32 == 0;
+    kp.boxes = !p->turned && !misaligned(C, 16) && p->N * size % 16 == 0;
     kp.l_mn = l.mn;
     kp.r_mn = r.mn;
     // The maps are encoded for every run: they cost well under a microsecond
     // of host time, and nothing is kept by an operand's address.
     ScaledMaps tm{};
     bool ok = encode_side(&tm.l, l, 128) && encode_side(&tm.r, r, (uint32_t)(p->width / p->ctas));
+    if (kp.boxes)
+        ok = ok && encode(&tm.c, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, size, C, p->N, p->M,
+                          (uint32_t)(64 / size), 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
     if (p->ws_bytes > 0) {
         kp.counters = reinterpret_cast<unsigned long long*>(workspace);

@@ -48,15 +48,12 @@ namespace psm {
 #ifndef S_EPI_WARPS
 #define S_EPI_WARPS 8
 #endif
-#ifndef S_G
-#define S_G 8
-#endif
 constexpr int S_THREADS = 128 + 32 * S_EPI_WARPS;
 constexpr int S_BK = 128;
 constexpr int S_EPI_WARP0 = 4;
 constexpr int S_EPI_THREADS = 32 * S_EPI_WARPS;
 constexpr int S_QUEUE = 4;
-constexpr int S_SLOTS = 2;       // of scales, S_G k-blocks each
+constexpr int S_SLOTS = 2;       // of scales, GROUPS k-blocks each
 constexpr int S_COL_SCALES = 128 * 4;  // a k-block's: the lanes' scales, then the columns'
 #ifndef S_FMA
 #define S_FMA 1
@@ -101,7 +98,7 @@ constexpr int S_COL_SCALES = 128 * 4;  // a k-block's: the lanes' scales, then t
 #define S_CHUNK_V 16
 #endif
 #ifndef S_CHUNK
-#define S_CHUNK 64
+#define S_CHUNK 32
 #endif
 enum : uint32_t { S_BAR_EPI = 1, S_BAR_VOTE = 2 };
 
@@ -113,14 +110,16 @@ struct ScaledCfg {
     static constexpr int L_BYTES = 128 * S_BK;
     static constexpr int R_BYTES = 128 * S_BK;    // this CTA's columns
     static constexpr int STAGE_BYTES = L_BYTES + R_BYTES;
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = TURNED ? 6 : 5;
+    static constexpr int GROUPS = COL_VECTOR && PAIR ? 4 : 8;  // k-blocks of a slot of scales
+    static constexpr int BOXES = TURNED ? 0 : 3;  // staged boxes of a warp, 32 rows x 64 bytes
     static constexpr int PRODUCTS = CM;           // products a k-block
     static constexpr int BUFFERS = 4 / PRODUCTS;  // of each, 128 columns of tensor memory
     static constexpr int SCALE_BYTES = S_COL_SCALES + (COL_VECTOR ? TILE_N * 4 : 16);  // of a k-block
-    static constexpr int SLOT_BYTES = S_G * SCALE_BYTES;
+    static constexpr int SLOT_BYTES = GROUPS * SCALE_BYTES;
     static constexpr int QUEUE_BYTES = S_QUEUE * 48;
     static constexpr int BAR_BYTES = 384;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + S_SLOTS * SLOT_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + S_EPI_WARPS * BOXES * 2048 + S_SLOTS * SLOT_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
     static constexpr int SLOT_FLOATS = 128 * TILE_N;
     static constexpr int BARS = 2 * STAGES + 8 + 1 + 2 * S_QUEUE + 2 * S_SLOTS;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
@@ -142,7 +141,7 @@ struct ScaledParams {
     void* out;
     int64_t ldc;                  // elements of a row of C
     int32_t out_dtype;            // 0 f16, 1 bf16, 2 f32
-    int32_t wide;                 // straight: every row of C starts at a 32-byte boundary
+    int32_t boxes;                // straight: C is written by tensor copies
     int32_t l_mn, r_mn;           // operand is MN-major (the summed dimension is strided)
     float* partials;              // a slot a CTA
     unsigned long long* counters; // one a split tile and CTA of the pair
@@ -153,7 +152,7 @@ struct ScaledParams {
 };
 
 struct ScaledMaps {
-    CUtensorMap l, r;
+    CUtensorMap l, r, c;
 };
 
 // ---------------------------------------------------------------- instructions
@@ -251,12 +250,11 @@ __device__ __forceinline__ float ld_shared_f1(uint32_t addr) {
     return v;
 }
 
-// 32 bytes to global memory, a whole sector.
-__device__ __forceinline__ void st_u8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
-                                      uint32_t g, uint32_t h) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
-                 "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
+// Wait until at most N of this thread's bulk groups have not finished reading their
+// shared-memory source.
+template <int N>
+__device__ __forceinline__ void bulk_wait_group_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // mbar_wait that also gives up once `stop` is set.
@@ -367,7 +365,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
     const uint32_t ring = raw + pad;
-    const uint32_t slots = ring + STAGES * Cf::STAGE_BYTES;
+    const uint32_t boxes = ring + STAGES * Cf::STAGE_BYTES;
+    const uint32_t slots = boxes + S_EPI_WARPS * Cf::BOXES * 2048;
     const uint32_t queue = slots + S_SLOTS * Cf::SLOT_BYTES;
     uint8_t* bar_area = smem_raw + (queue + Cf::QUEUE_BYTES - raw);
     const uint32_t bar_base = smem_addr(bar_area);
@@ -620,7 +619,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     const int c = min(w.n0 + (COL_VECTOR ? i * 32 + lane : (lane & (Cf::CM - 1)) * 128), p.r.rows - 1);
                     rs[i] = p.r.s + (int64_t)(c >> p.r.shift) * p.r.row + (int64_t)w.k0 * p.r.group;
                 }
-                for (int kb0 = w.k0; kb0 < w.k1; kb0 += S_G) {
+                for (int kb0 = w.k0; kb0 < w.k1; kb0 += Cf::GROUPS) {
                     if (!__all_sync(0xffffffffu, wait(sempty_bar(slot), phase ^ 1u))) {
                         if (lane == 0) fail_pipe();
                         ok = false;
@@ -628,7 +627,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     }
                     uint32_t at = slots + (uint32_t)(slot * Cf::SLOT_BYTES) + (uint32_t)lane * 4;
 #pragma unroll 1
-                    for (int kb = kb0; kb < min(kb0 + S_G, w.k1); ++kb) {
+                    for (int kb = kb0; kb < min(kb0 + Cf::GROUPS, w.k1); ++kb) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             cp_async_4(at + i * 128, ls[i]);
@@ -729,20 +728,20 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     }
                     here = mbar_test(full0 + 8u * (uint32_t)buf, tphase);
                 };
+                // one chunk of columns is read while the one before is added
+                uint32_t v[2][CHUNK];
+                if (chunks > 0) tmem_ld_async(tbase, v[0]);
+                const float mine = ld_shared_f1(my_scales + (uint32_t)(q * 32 + lane) * 4);
+#pragma unroll
+                for (int i = 0; i < (WHOLE ? 2 : 1); ++i) {
+                    factors[i] = mine;
+                    if constexpr (!COL_VECTOR) factors[i] *= ld_shared_f1(my_scales + S_COL_SCALES + (uint32_t)((c0 >> 7) + i) * 4);
+                }
 #pragma unroll
                 for (int c = 0; c < PART / CHUNK; ++c) {
                     if (c < chunks) {
-                        uint32_t v[CHUNK];
-                        tmem_ld_async(tbase + c * CHUNK, v);
-                        if (c == 0) {
-                            const float mine = ld_shared_f1(my_scales + (uint32_t)(q * 32 + lane) * 4);
-#pragma unroll
-                            for (int i = 0; i < (WHOLE ? 2 : 1); ++i) {
-                                factors[i] = mine;
-                                if constexpr (!COL_VECTOR) factors[i] *= ld_shared_f1(my_scales + S_COL_SCALES + (uint32_t)((c0 >> 7) + i) * 4);
-                            }
-                        }
-                        tmem_wait(v);
+                        tmem_wait(v[c & 1]);
+                        if (c + 1 < PART / CHUNK && c + 1 < chunks) tmem_ld_async(tbase + (c + 1) * CHUNK, v[(c + 1) & 1]);
                         if (PAIR && c == PART / CHUNK - 1) release();
 #pragma unroll
                         for (int i = 0; i < CHUNK; i += 4) {
@@ -751,20 +750,20 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                             float4 f = make_float4(factor, factor, factor, factor);
                             if constexpr (COL_VECTOR) f = ld_shared_f4(my_cols + (uint32_t)(at + (WHOLE && at >= 64 ? 64 : 0)) * 4);
                             float* a = acc + c * CHUNK + i;
-                            S_ADD4(a, v + i, f, factor);
+                            S_ADD4(a, v[c & 1] + i, f, factor);
                         }
                     }
                 }
                 if (!PAIR) release();
             };
 #pragma unroll 1
-            for (int kb0 = w.k0; kb0 < w.k1; kb0 += S_G) {
+            for (int kb0 = w.k0; kb0 < w.k1; kb0 += Cf::GROUPS) {
                 ok = ok && wait(sfull_bar(slot), sphase);
                 uint32_t my_scales = slots + (uint32_t)(slot * Cf::SLOT_BYTES);
-                const int n = min(S_G, w.k1 - kb0);
-                if (S_UNROLL > 1 && n == S_G) {
+                const int n = min(Cf::GROUPS, w.k1 - kb0);
+                if (S_UNROLL > 1 && n == Cf::GROUPS) {
 #pragma unroll 1
-                    for (int i = 0; i < S_G; i += S_UNROLL) {
+                    for (int i = 0; i < Cf::GROUPS; i += S_UNROLL) {
 #pragma unroll
                         for (int u = 0; u < S_UNROLL; ++u) block(my_scales + u * Cf::SCALE_BYTES);
                         my_scales += S_UNROLL * Cf::SCALE_BYTES;
@@ -817,6 +816,48 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 }
             }
             // ---- the tile to C
+            if (!TURNED && p.boxes) {
+                // by tensor copies of boxes of 32 rows x 64 bytes, 16-byte units swizzled by
+                // row.  (Stored by the lanes, a row each, an instruction touches 32 lines:
+                // some 4000 cycles a tile.)
+                constexpr int B = Cf::BOXES;
+                const uint32_t my_box = boxes + (uint32_t)((warp - S_EPI_WARP0) * B) * 2048u;
+                int box = 0;
+                auto stage = [&](int x, const uint32_t (&u)[16]) {  // 64 bytes of the lane's row
+                    if (lane == 0) bulk_wait_group_read<(B > 0 ? B - 1 : 0)>();
+                    __syncwarp();
+                    const uint32_t at = my_box + (uint32_t)box * 2048u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st_shared_u4(at + (uint32_t)lane * 64u + (uint32_t)((i ^ ((lane >> 1) & 3)) * 16), u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (x < (int)p.ldc && l < p.l_total) tma_store_2d(&tm.c, at, x, l);
+                        bulk_commit_group();
+                    }
+                    box = box + 1 == B ? 0 : box + 1;
+                };
+                if (p.out_dtype == 2) {
+#pragma unroll
+                    for (int i = 0; i < PART; i += 16) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(acc[i + j]);
+                        stage(w.n0 + c0 + i + (WHOLE && i >= 64 ? 64 : 0), u);
+                    }
+                } else {
+                    const bool bf16 = p.out_dtype == 1;
+#pragma unroll
+                    for (int i = 0; i < PART; i += 32) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = scaled_pack2(bf16, acc[i + 2 * j], acc[i + 2 * j + 1]);
+                        stage(w.n0 + c0 + i + (WHOLE && i >= 64 ? 64 : 0), u);
+                    }
+                }
+                continue;
+            }
             if (l >= p.l_total) continue;
             if constexpr (TURNED) {
                 const int count = min(w.valid - c0, chunks * CHUNK);  // columns with a row of C
@@ -825,44 +866,16 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 for (int i = 0; i < PART; ++i)
                     if (i < count) scaled_store(p.out, p.out_dtype, at + (int64_t)i * p.ldc, acc[i]);
             } else {
+                // rows of C that tensor copies cannot address: element by element
                 const int64_t at = (int64_t)l * p.ldc + w.n0 + c0;
-                if (p.out_dtype == 2) {
-                    float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
-                    for (int i = 0; i < PART; i += 8) {
-                        const int c = i + (WHOLE && i >= 64 ? 64 : 0);
-                        const int count = w.valid - c0 - c;
-                        if (p.wide && count >= 8) {
-                            st_u8(out + c, __float_as_uint(acc[i]), __float_as_uint(acc[i + 1]), __float_as_uint(acc[i + 2]),
-                                  __float_as_uint(acc[i + 3]), __float_as_uint(acc[i + 4]), __float_as_uint(acc[i + 5]),
-                                  __float_as_uint(acc[i + 6]), __float_as_uint(acc[i + 7]));
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (j < count) out[c + j] = acc[i + j];
-                        }
-                    }
-                } else {
-                    const bool bf16 = p.out_dtype == 1;
-                    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-                    for (int i = 0; i < PART; i += 16) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = scaled_pack2(bf16, acc[i + 2 * j], acc[i + 2 * j + 1]);
-                        const int c = i + (WHOLE && i >= 64 ? 64 : 0);
-                        const int count = w.valid - c0 - c;
-                        if (p.wide && count >= 16) {
-                            st_u8(out + c, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (j < count) out[c + j] = (uint16_t)(o[j / 2] >> (16 * (j & 1)));
-                        }
-                    }
+                for (int i = 0; i < PART; ++i) {
+                    const int c = i + (WHOLE && i >= 64 ? 64 : 0);
+                    if (c0 + c < w.valid) scaled_store(p.out, p.out_dtype, at + c, acc[i]);
                 }
             }
         }
+        if (lane == 0) bulk_wait_group_0();  // the copies are complete before the CTA ends
     }
 
     tc_fence_before_sync();
