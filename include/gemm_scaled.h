@@ -142,14 +142,21 @@ gemm_status_t gemm_rms_norm_grad(const void *dy, int64_t lddy, const void *s, in
 
 typedef struct gemm_scaled_plan *gemm_scaled_plan_t;
 
+typedef enum {
+    GEMM_SCALED_STRAIGHT = 0,  /* A along the tensor memory's lanes, B along its columns */
+    GEMM_SCALED_TURNED = 1,    /* B along the lanes: the rows of A cost steps of 16 */
+    GEMM_SCALED_FEW = 2        /* without tensor memory: at most 16 rows of A, A row-major and
+                                * B column-major */
+} gemm_scaled_form_t;
+
 /* Options for gemm_scaled_plan_set_option (key, value). */
 enum {
     /* CTAs of a scheduling unit: 1 (tiles of 128 x up to 128), or 2, a cluster
      * that runs pair MMAs (256 x 256); 0 (default) lets the plan choose. */
     GEMM_SCALED_OPT_CTAS = 1,
-    /* 1: B along the tensor memory's lanes and the rows of A along its columns
-     * (one CTA a unit); 0: the other way; -1 (default) lets the plan choose. */
-    GEMM_SCALED_OPT_TURNED = 2,
+    /* how the product is computed, a gemm_scaled_form_t (all but STRAIGHT with one
+     * CTA a unit); -1 (default) lets the plan choose. */
+    GEMM_SCALED_OPT_FORM = 2,
     /* test hook: the scheduling unit with this index gives up before it writes
      * its first tile, as if a wait had run out, in every run that starts after
      * the call, replays of captured ones among them.  -1 (default) = off. */
@@ -159,13 +166,12 @@ enum {
 /* Keys for gemm_scaled_plan_get_info. */
 enum {
     GEMM_SCALED_INFO_CTAS = 1,        /* CTAs of a scheduling unit (1 or 2) */
-    GEMM_SCALED_INFO_TURNED = 2,      /* 1: the rows of A are the tiles' columns */
+    GEMM_SCALED_INFO_FORM = 2,        /* a gemm_scaled_form_t */
+    /* the rest for all forms but FEW */
     GEMM_SCALED_INFO_UNITS = 3,       /* scheduling units of a launch */
     GEMM_SCALED_INFO_TILES = 4,
     GEMM_SCALED_INFO_TILE_WIDTH = 5,  /* columns of a tile */
-    GEMM_SCALED_INFO_SHARES = 6,      /* parts along k of a tile that is split */
-    GEMM_SCALED_INFO_STAGES = 7,      /* depth of the shared-memory ring */
-    GEMM_SCALED_INFO_SMEM_BYTES = 8
+    GEMM_SCALED_INFO_SHARES = 6       /* parts along k of a tile that is split */
 };
 
 /*

@@ -8,8 +8,8 @@ not built: there is no CPU fallback.
 """
 from ._binding import (  # noqa: F401
     GEMM_BF16, GEMM_COL_MAJOR, GEMM_E4M3, GEMM_E5M2, GEMM_F32, GEMM_NORM_MAX_HIDDEN, GEMM_QUANTIZE_BLOCKS,
-    GEMM_QUANTIZE_COLS, GEMM_QUANTIZE_ROWS, GEMM_SCALED_OPT_CTAS, GEMM_SCALED_OPT_INJECT_GIVE_UP,
-    GEMM_SCALED_OPT_TURNED, GEMM_SCALE_BLOCK, GEMM_SCALE_GROUP, GEMM_SCALE_VECTOR, GEMM_GROUPED_INNER, GEMM_GROUPED_OPT_CTAS,
+    GEMM_QUANTIZE_COLS, GEMM_QUANTIZE_ROWS, GEMM_SCALED_OPT_CTAS, GEMM_SCALED_FEW, GEMM_SCALED_OPT_FORM,
+    GEMM_SCALED_OPT_INJECT_GIVE_UP, GEMM_SCALED_STRAIGHT, GEMM_SCALED_TURNED, GEMM_SCALE_BLOCK, GEMM_SCALE_GROUP, GEMM_SCALE_VECTOR, GEMM_GROUPED_INNER, GEMM_GROUPED_OPT_CTAS,
     GEMM_GROUPED_OPT_INJECT_GIVE_UP, GEMM_GROUPED_ROWS, GEMM_INDEX_I32, GEMM_INDEX_I64,
     GEMM_MOE_MAX_EXPERTS, GEMM_SCHED_AUTO, GEMM_F16, GEMM_ROW_MAJOR, GEMM_SCHED_DATA_PARALLEL,
     GEMM_SCHED_PERSISTENT, GEMM_SCHED_SPLITK, GEMM_SCHED_STREAMK, GemmError, GroupedPlan, Plan, SCHEDULES,

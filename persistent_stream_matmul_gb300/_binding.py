@@ -61,8 +61,9 @@ GEMM_SCALE_VECTOR, GEMM_SCALE_BLOCK = 0, 1
 GEMM_SCALE_GROUP = 128
 GEMM_QUANTIZE_ROWS, GEMM_QUANTIZE_COLS, GEMM_QUANTIZE_BLOCKS = 0, 1, 2
 GEMM_NORM_MAX_HIDDEN = 65536
-GEMM_SCALED_OPT_CTAS, GEMM_SCALED_OPT_TURNED, GEMM_SCALED_OPT_INJECT_GIVE_UP = 1, 2, 3
-SCALED_INFO = {"ctas": 1, "turned": 2, "units": 3, "tiles": 4, "tile_width": 5, "shares": 6, "stages": 7, "smem_bytes": 8}
+GEMM_SCALED_STRAIGHT, GEMM_SCALED_TURNED, GEMM_SCALED_FEW = 0, 1, 2
+GEMM_SCALED_OPT_CTAS, GEMM_SCALED_OPT_FORM, GEMM_SCALED_OPT_INJECT_GIVE_UP = 1, 2, 3
+SCALED_INFO = {"ctas": 1, "form": 2, "units": 3, "tiles": 4, "tile_width": 5, "shares": 6}
 
 ROLE_FULL, ROLE_OWNER, ROLE_PEER, ROLE_CLUSTER_PART = 0, 1, 2, 3
 TRACE_STAMPS = 6   # uint64 per CTA written by gemm_plan_set_trace: 4 timer + 2 clock stamps
@@ -564,14 +565,14 @@ class ScaledPlan:
     """Owning wrapper around a scaled plan handle (marshalling only)."""
 
     def __init__(self, M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b, offline_sms=None,
-                 ctas=None, turned=None):
+                 ctas=None, form=None):
         self.M, self.N, self.K = M, N, K
         self.out_dtype = out_dtype
         args = (M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b)
         self.handle = (gemm_scaled_plan_create(*args) if offline_sms is None
                        else gemm_scaled_plan_create_offline(*args, offline_sms))
-        if turned is not None:
-            self.set_option(GEMM_SCALED_OPT_TURNED, int(turned))
+        if form is not None:
+            self.set_option(GEMM_SCALED_OPT_FORM, int(form))
         if ctas is not None:
             self.set_option(GEMM_SCALED_OPT_CTAS, int(ctas))
 

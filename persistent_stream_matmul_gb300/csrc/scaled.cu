@@ -9,7 +9,8 @@
 
 #include "gemm_scaled.h"
 #include "host.cuh"
-#include "scaled_kernel.cuh"
+#include "rows.cuh"
+#include "scaled_few.cuh"
 
 using namespace psm;
 
@@ -20,9 +21,9 @@ struct gemm_scaled_plan {
     int type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b;
     int device, num_sms;
     bool offline;
-    int opt_ctas, opt_turned;
+    int opt_ctas, opt_form;
     // derived
-    int ctas, turned, col_vector;
+    int form, ctas, turned, col_vector;
     int width;               // columns of a tile
     GroupedShape shape;
     size_t counter_bytes, ws_bytes;
@@ -96,10 +97,12 @@ int resident_pairs(int dev) {
 }
 
 gemm_status_t derive(gemm_scaled_plan* p) {
-    int turned = p->opt_turned, ctas = p->opt_ctas;
-    if (turned < 0) turned = ctas != 2 && p->M <= 128;
-    if (ctas == 0) ctas = !turned && cdiv(p->M, 256) * cdiv(p->N, 256) >= 64 ? 2 : 1;
-    if (turned && ctas == 2) return GEMM_ERR_UNSUPPORTED;
+    const bool few = p->M <= F_MOST_ROWS && p->layout_a == GEMM_ROW_MAJOR && p->layout_b == GEMM_COL_MAJOR;
+    int form = p->opt_form, ctas = p->opt_ctas;
+    if (form < 0) form = ctas == 2 ? GEMM_SCALED_STRAIGHT : few ? GEMM_SCALED_FEW : p->M <= 128 ? GEMM_SCALED_TURNED : GEMM_SCALED_STRAIGHT;
+    if (ctas == 0) ctas = form == GEMM_SCALED_STRAIGHT && cdiv(p->M, 256) * cdiv(p->N, 256) >= 64 ? 2 : 1;
+    if ((form != GEMM_SCALED_STRAIGHT && ctas == 2) || (form == GEMM_SCALED_FEW && !few)) return GEMM_ERR_UNSUPPORTED;
+    const int turned = form != GEMM_SCALED_STRAIGHT;
     const int64_t lanes = turned ? p->N : p->M, cols = turned ? p->M : p->N;
     const int tile = 128 * ctas;
     GroupedShape s{};
@@ -121,13 +124,14 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     const int64_t side = std::max<int64_t>(1, cdiv(cols, tile));
     if (s.tiles_m > 0 && side > MAX_INDEX / s.tiles_m) return GEMM_ERR_UNSUPPORTED;
     s.may_split = (int64_t)s.units * s.kb < MAX_INDEX;
+    p->form = form;
     p->ctas = ctas;
     p->turned = turned;
     p->col_vector = turned || p->scale_b == GEMM_SCALE_VECTOR;
     p->width = (int)(cdiv(std::max<int64_t>(1, cdiv(cols, side)), s.step) * s.step);
     p->shape = s;
     p->counter_bytes = p->ws_bytes = 0;
-    if (p->M > 0 && p->N > 0 && p->K > 0 && grouped_split(s, (int32_t)(side * s.tiles_m), 0).most > 0) {
+    if (form != GEMM_SCALED_FEW && p->M > 0 && p->N > 0 && p->K > 0 && grouped_split(s, (int32_t)(side * s.tiles_m), 0).most > 0) {
         const size_t slot = 128 * (size_t)tile * sizeof(float), grid = (size_t)s.units * ctas;
         p->counter_bytes = (grid * 8 + 255) / 256 * 256;
         p->ws_bytes = p->counter_bytes + grid * slot;
@@ -174,7 +178,7 @@ gemm_status_t make_plan(gemm_scaled_plan_t* out, int64_t M, int64_t N, int64_t K
     p->device = dev;
     p->num_sms = num_sms;
     p->offline = offline;
-    p->opt_turned = -1;
+    p->opt_form = -1;
     const gemm_status_t st = derive(p);
     if (st != GEMM_OK) {
         delete p;
@@ -202,6 +206,23 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool W, bool X, int NT>
+gemm_status_t run_few_v(const FewParams& kp, int num_sms, gemm_stream_t stream) {
+    // Two tiles of 16 rows a warp read A half as often; one makes twice the blocks.
+#ifdef F_MT
+    return launch(few_kernel<W, X, F_MT, NT, F_U>, dim3((unsigned)cdiv(kp.N, 16 * F_MT)), dim3(32 * F_WARPS), 0, stream, kp);
+#endif
+    if (cdiv(kp.N, 32) >= 2 * num_sms) return launch(few_kernel<W, X, 2, NT, 2>, dim3((unsigned)cdiv(kp.N, 32)), dim3(32 * F_WARPS), 0, stream, kp);
+    return launch(few_kernel<W, X, 1, NT, 3>, dim3((unsigned)cdiv(kp.N, 16)), dim3(32 * F_WARPS), 0, stream, kp);
+}
+
+gemm_status_t run_few(const gemm_scaled_plan* p, const FewParams& kp, gemm_stream_t stream) {
+    const bool w = p->type_b == GEMM_E5M2, x = p->type_a == GEMM_E5M2;
+    auto* fn = kp.M <= 8 ? (w ? (x ? run_few_v<true, true, 1> : run_few_v<true, false, 1>) : (x ? run_few_v<false, true, 1> : run_few_v<false, false, 1>))
+                         : (w ? (x ? run_few_v<true, true, 2> : run_few_v<true, false, 2>) : (x ? run_few_v<false, true, 2> : run_few_v<false, false, 2>));
+    return fn(kp, p->num_sms, stream);
 }
 
 // One operand, as the lanes or the columns side sees it: `rows` of K elements.
@@ -236,8 +257,6 @@ bool encode_side(CUtensorMap* m, const Side& o, uint32_t rows) {
                 : encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, o.K, o.rows, S_BK, rows);
 }
 
-bool misaligned(const void* p, size_t size) { return ((uintptr_t)p & (size - 1)) != 0; }
-
 }  // namespace
 
 extern "C" {
@@ -267,20 +286,20 @@ gemm_status_t gemm_scaled_plan_set_option(gemm_scaled_plan_t p, int key, int64_t
                    ? GEMM_OK
                    : GEMM_ERR_CUDA;
     }
-    const int saved[2] = {p->opt_ctas, p->opt_turned};
+    const int saved[2] = {p->opt_ctas, p->opt_form};
     if (key == GEMM_SCALED_OPT_CTAS) {
         if (value < 0 || value > 2) return GEMM_ERR_UNSUPPORTED;
         p->opt_ctas = (int)value;
-    } else if (key == GEMM_SCALED_OPT_TURNED) {
-        if (value < -1 || value > 1) return GEMM_ERR_UNSUPPORTED;
-        p->opt_turned = (int)value;
+    } else if (key == GEMM_SCALED_OPT_FORM) {
+        if (value < -1 || value > GEMM_SCALED_FEW) return GEMM_ERR_UNSUPPORTED;
+        p->opt_form = (int)value;
     } else {
         return GEMM_ERR_INVALID_ARG;
     }
     const gemm_status_t st = derive(p);
     if (st != GEMM_OK) {
         p->opt_ctas = saved[0];
-        p->opt_turned = saved[1];
+        p->opt_form = saved[1];
         derive(p);
     }
     return st;
@@ -290,13 +309,11 @@ gemm_status_t gemm_scaled_plan_get_info(gemm_scaled_plan_t p, int key, int64_t* 
     if (!p || !value) return GEMM_ERR_INVALID_ARG;
     switch (key) {
         case GEMM_SCALED_INFO_CTAS: *value = p->ctas; break;
-        case GEMM_SCALED_INFO_TURNED: *value = p->turned; break;
+        case GEMM_SCALED_INFO_FORM: *value = p->form; break;
         case GEMM_SCALED_INFO_UNITS: *value = p->shape.units; break;
         case GEMM_SCALED_INFO_TILES: *value = grouped_tiles(p->shape, p->shape.rows); break;
         case GEMM_SCALED_INFO_TILE_WIDTH: *value = p->width; break;
         case GEMM_SCALED_INFO_SHARES: *value = p->ws_bytes ? grouped_split(p->shape, grouped_tiles(p->shape, p->shape.rows), 0).shares : 1; break;
-        case GEMM_SCALED_INFO_STAGES: *value = kernel_of(p->ctas, p->turned, p->col_vector).stages; break;
-        case GEMM_SCALED_INFO_SMEM_BYTES: *value = kernel_of(p->ctas, p->turned, p->col_vector).smem; break;
         default: return GEMM_ERR_INVALID_ARG;
     }
     return GEMM_OK;
@@ -324,6 +341,20 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (p->K == 0)  // empty sums: +0
         return cudaMemsetAsync(C, 0, (size_t)p->M * (size_t)p->N * (size_t)size, st) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    if (p->form == GEMM_SCALED_FEW) {
+        FewParams kp{};
+        kp.a = static_cast<const uint8_t*>(A);
+        kp.b = static_cast<const uint8_t*>(B);
+        kp.sa = side_of(A, scales_a, p->M, p->K, true, p->scale_a).s;
+        kp.sb = side_of(B, scales_b, p->N, p->K, true, p->scale_b).s;
+        kp.out = C;
+        kp.K = p->K;
+        kp.N = p->N;
+        kp.M = (int32_t)p->M;
+        kp.kb = p->shape.kb;
+        kp.out_dtype = p->out_dtype;
+        return run_few(p, kp, stream);
+    }
     if (!prepared(p->ctas, p->turned, p->col_vector, p->device)) return GEMM_ERR_CUDA;
 
     const Side a = side_of(A, scales_a, p->M, p->K, p->layout_a == GEMM_ROW_MAJOR, p->scale_a);

@@ -1,0 +1,149 @@
+// Scaled products of a few rows of A (one generated token, a small batch), both
+// operands with the summed dimension contiguous.
+//
+// Bound by the reading of B: 2 M operations a byte of it.  What a small product
+// pays beside that is latency, so this kernel has no ring, no tensor memory and
+// no second pass: a warp reads its rows of B from global memory straight into the
+// fragments of m16n8k32 products, whose rows are B's and whose columns are the rows
+// of A.  A sum does not depend on the order of k, so a thread takes 32 neighbouring
+// bytes of a row (four threads a 128-byte group) and gives four of them at a time
+// to a product, where the fragment's layout has k 4t .. 4t + 3 and 16 + 4t .. ;
+// A's fragments are read the same way.
+//
+// The k-blocks are cut into one part a warp of the block; the parts are added in
+// ascending k through shared memory.
+#pragma once
+#include "scaled_kernel.cuh"
+
+namespace psm {
+
+#ifndef F_W
+#define F_W 8
+#define F_MIN 1
+#endif
+constexpr int F_WARPS = F_W;
+constexpr int F_MOST_ROWS = 16;  // of A
+
+struct FewParams {
+    const uint8_t *a, *b;
+    ScaledScales sa, sb;
+    void* out;
+    int64_t K, N;
+    int32_t M, kb, out_dtype;
+};
+
+template <bool A_E5M2, bool B_E5M2>
+__device__ __forceinline__ void mma_f8_m16n8k32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+#define PSM_MMA_F8(TA, TB)                                                                          \
+    asm("mma.sync.aligned.m16n8k32.row.col.f32." TA "." TB ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, " \
+        "{%8, %9}, {%0, %1, %2, %3};"                                                               \
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                            \
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]))
+    if constexpr (A_E5M2 && B_E5M2) PSM_MMA_F8("e5m2", "e5m2");
+    else if constexpr (A_E5M2) PSM_MMA_F8("e5m2", "e4m3");
+    else if constexpr (B_E5M2) PSM_MMA_F8("e4m3", "e5m2");
+    else PSM_MMA_F8("e4m3", "e4m3");
+#undef PSM_MMA_F8
+}
+
+// 32 bytes; rows start at 16-byte boundaries, and end at one (`bytes` of them are there).
+__device__ __forceinline__ void few_load(const uint8_t* p, int64_t bytes, uint32_t (&w)[8]) {
+    uint4 x{}, y{};
+    if (bytes > 0) x = *reinterpret_cast<const uint4*>(p);
+    if (bytes > 16) y = *reinterpret_cast<const uint4*>(p + 16);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+}
+
+// MT: tiles of 16 rows of B a warp; NT: tiles of 8 rows of A; U: k-blocks in flight.
+template <bool W_E5M2, bool X_E5M2, int MT, int NT, int U>
+__global__ void __launch_bounds__(32 * F_WARPS, F_MIN) few_kernel(const __grid_constant__ FewParams p) {
+    __shared__ float part[F_WARPS][MT * 16][NT * 8 + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int64_t n0 = (int64_t)blockIdx.x * (MT * 16);
+    // rows past the end read the last one's
+    const uint8_t* b[MT][2];
+    const float* sb[MT][2];
+    const uint8_t* a[NT];
+    const float* sa[NT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = min(n0 + i * 16 + h * 8 + g, p.N - 1);
+            b[i][h] = p.b + n * p.K + t * 32;
+            sb[i][h] = p.sb.s + (n >> p.sb.shift) * p.sb.row;
+        }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        a[j] = p.a + (int64_t)min(j * 8 + g, p.M - 1) * p.K + t * 32;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) sa[j][h] = p.sa.s + (int64_t)(min(j * 8 + t * 2 + h, p.M - 1) >> p.sa.shift) * p.sa.row;
+    }
+    const int k0 = (int)((int64_t)p.kb * warp / F_WARPS), k1 = (int)((int64_t)p.kb * (warp + 1) / F_WARPS);
+    float acc[MT][NT][4] = {};
+    grid_dependency_wait();
+    grid_launch_dependents();
+#pragma unroll 1
+    for (int kb0 = k0; kb0 < k1; kb0 += U) {
+        uint32_t wb[U][MT][2][8], wa[U][NT][8];
+        float fb[U][MT][2], fa[U][NT][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = kb0 + u;
+            // nothing is read past this warp's part (or the row)
+            const int64_t at = (int64_t)kb * S_BK, left = kb < k1 ? p.K - at - t * 32 : 0;
+            const int64_t gb = (int64_t)min(kb, k1 - 1);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) few_load(b[i][h] + at, left, wb[u][i][h]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) few_load(a[j] + at, left, wa[u][j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) fb[u][i][h] = sb[i][h][gb * p.sb.group];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) fa[u][j][h] = sa[j][h][gb * p.sa.group];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (kb0 + u >= k1) break;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float d[4] = {};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t x[4] = {wb[u][i][0][2 * s], wb[u][i][1][2 * s], wb[u][i][0][2 * s + 1], wb[u][i][1][2 * s + 1]};
+                        const uint32_t y[2] = {wa[u][j][2 * s], wa[u][j][2 * s + 1]};
+                        mma_f8_m16n8k32<W_E5M2, X_E5M2>(d, x, y);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(d[c], fb[u][i][c >> 1] * fa[u][j][c & 1], acc[i][j][c]);
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) part[warp][i * 16 + (c >> 1) * 8 + g][j * 8 + t * 2 + (c & 1)] = acc[i][j][c];
+    __syncthreads();
+    for (int e = threadIdx.x; e < MT * 16 * p.M; e += 32 * F_WARPS) {
+        const int r = e % (MT * 16), m = e / (MT * 16);
+        if (n0 + r >= p.N) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < F_WARPS; ++w) sum += part[w][r][m];
+        scaled_store(p.out, p.out_dtype, (int64_t)m * p.N + n0 + r, sum);
+    }
+}
+
+}  // namespace psm

@@ -45,9 +45,7 @@
 
 namespace psm {
 
-#ifndef S_EPI_WARPS
-#define S_EPI_WARPS 8
-#endif
+constexpr int S_EPI_WARPS = 8;
 constexpr int S_THREADS = 128 + 32 * S_EPI_WARPS;
 constexpr int S_BK = 128;
 constexpr int S_EPI_WARP0 = 4;
@@ -55,51 +53,10 @@ constexpr int S_EPI_THREADS = 32 * S_EPI_WARPS;
 constexpr int S_QUEUE = 4;
 constexpr int S_SLOTS = 2;       // of scales, GROUPS k-blocks each
 constexpr int S_COL_SCALES = 128 * 4;  // a k-block's: the lanes' scales, then the columns'
-#ifndef S_FMA
-#define S_FMA 1
-#endif
-#if S_FMA == 1
-#define S_ADD4(a, v, f, factor)                                                                                   \
-    {                                                                                                             \
-        uint64_t p0 = pack_f32x2((v)[0], (v)[1]), p1 = pack_f32x2((v)[2], (v)[3]);                                \
-        const uint64_t f0 = pack_f32x2((f).x, (f).y), f1 = pack_f32x2((f).z, (f).w), ff = pack_f32x2(factor, factor); \
-        uint64_t a0 = pack_f32x2((a)[0], (a)[1]), a1 = pack_f32x2((a)[2], (a)[3]);                                \
-        if constexpr (COL_VECTOR) {                                                                               \
-            a0 = fma_f32x2(mul_f32x2(p0, f0), ff, a0);                                                            \
-            a1 = fma_f32x2(mul_f32x2(p1, f1), ff, a1);                                                            \
-        } else {                                                                                                  \
-            a0 = fma_f32x2(p0, f0, a0);                                                                           \
-            a1 = fma_f32x2(p1, f1, a1);                                                                           \
-        }                                                                                                         \
-        const float2 x0 = unpack_f32x2(a0), x1 = unpack_f32x2(a1);                                                \
-        (a)[0] = x0.x; (a)[1] = x0.y; (a)[2] = x1.x; (a)[3] = x1.y;                                               \
-    }
-#else
-#define S_ADD4(a, v, f, factor)                                                                                   \
-    if constexpr (COL_VECTOR) {                                                                                   \
-        (a)[0] = fmaf(__uint_as_float((v)[0]) * (f).x, factor, (a)[0]);                                           \
-        (a)[1] = fmaf(__uint_as_float((v)[1]) * (f).y, factor, (a)[1]);                                           \
-        (a)[2] = fmaf(__uint_as_float((v)[2]) * (f).z, factor, (a)[2]);                                           \
-        (a)[3] = fmaf(__uint_as_float((v)[3]) * (f).w, factor, (a)[3]);                                           \
-    } else {                                                                                                      \
-        (a)[0] = fmaf(__uint_as_float((v)[0]), factor, (a)[0]);                                                   \
-        (a)[1] = fmaf(__uint_as_float((v)[1]), factor, (a)[1]);                                                   \
-        (a)[2] = fmaf(__uint_as_float((v)[2]), factor, (a)[2]);                                                   \
-        (a)[3] = fmaf(__uint_as_float((v)[3]), factor, (a)[3]);                                                   \
-    }
-#endif
-#ifndef S_EPI_REGS
-#define S_EPI_REGS 216
-#endif
-#ifndef S_UNROLL
-#define S_UNROLL 1
-#endif
-#ifndef S_CHUNK_V
-#define S_CHUNK_V 16
-#endif
-#ifndef S_CHUNK
-#define S_CHUNK 32
-#endif
+constexpr int S_CHUNK = 16;  // columns a load from tensor memory
+// Registers a thread of the pair kernel's epilogue; the other four warps give what its
+// eight take above the launch's 168 (2 x 48 = 96).
+constexpr int S_EPI_REGS = 216, S_OTHER_REGS = 3 * 168 - 2 * S_EPI_REGS;
 enum : uint32_t { S_BAR_EPI = 1, S_BAR_VOTE = 2 };
 
 template <bool PAIR, bool TURNED, bool COL_VECTOR>
@@ -318,6 +275,25 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     return v;
 }
 
+// a[0 .. 3] += v * f (COL_VECTOR: v * f * factor), two at a time: twice as fast as one by
+// one where the registers' moves count (8192 x 14336 x 4096 390 us against 435).
+template <bool COL_VECTOR>
+__device__ __forceinline__ void scaled_add4(float* a, const uint32_t* v, float4 f, float factor) {
+    uint64_t v0 = pack_f32x2(v[0], v[1]), v1 = pack_f32x2(v[2], v[3]);
+    uint64_t f0 = pack_f32x2(f.x, f.y), f1 = pack_f32x2(f.z, f.w);
+    if constexpr (COL_VECTOR) {
+        v0 = mul_f32x2(v0, f0);
+        v1 = mul_f32x2(v1, f1);
+        f0 = f1 = pack_f32x2(factor, factor);
+    }
+    const float2 x = unpack_f32x2(fma_f32x2(v0, f0, pack_f32x2(a[0], a[1])));
+    const float2 y = unpack_f32x2(fma_f32x2(v1, f1, pack_f32x2(a[2], a[3])));
+    a[0] = x.x;
+    a[1] = x.y;
+    a[2] = y.x;
+    a[3] = y.y;
+}
+
 template <int N>
 __device__ __forceinline__ void registers_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -470,7 +446,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     };
 
     if (warp < S_EPI_WARP0) {
-        if constexpr (PAIR) registers_fewer<(S_EPI_WARPS == 16 ? 64 : 504 - 2 * S_EPI_REGS)>();
+        if constexpr (PAIR) registers_fewer<S_OTHER_REGS>();
         if (warp == 0) {
             // -------------------------------------------------------- producer
             int stage = 0;
@@ -680,27 +656,24 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if constexpr (PAIR) registers_more<(S_EPI_WARPS == 16 ? 104 : S_EPI_REGS)>();
+        if constexpr (PAIR) registers_more<S_EPI_REGS>();
         const int q = warp & 3;  // tensor-memory lanes 32q .. 32q + 31
         const int part = (warp - S_EPI_WARP0) >> 2;
         const int et = threadIdx.x - S_EPI_WARP0 * 32;
         const uint64_t tag = grouped_tag(p.epoch, p.status);
         const bool give_up = p.status[G_WORD_GIVE_UP] == unit + 1;
-        constexpr int PARTS = S_EPI_WARPS / 4;
-        constexpr bool WHOLE = PAIR && PARTS == 2;  // a part reads a product, else half of one
-        const int first_buf = PAIR ? (WHOLE ? part : part >> 1) * BUFFERS : 0;
+        const int first_buf = PAIR ? part * BUFFERS : 0;
         const uint32_t full0 = tfull_bar(first_buf);
         const uint32_t release0 = PAIR ? mapa_shared(tempty_bar(first_buf), 0) : tempty_bar(0);
-        constexpr int CHUNK = !PAIR ? 16 : COL_VECTOR ? S_CHUNK_V : S_CHUNK;  // columns a load from tensor memory
         int buf = 0, slot = 0;
         uint32_t tphase = 0, sphase = 0;
         while (next_work()) {
-            // this warp's columns: c0 .. c0 + CHUNK * chunks - 1 of the tile, from t0 on of
+            // this warp's columns: c0 .. c0 + S_CHUNK * chunks - 1 of the tile, from t0 on of
             // a product's in tensor memory
-            const int wide = PAIR ? PART : (w.width / PARTS + 15) & ~15;
-            const int c0 = WHOLE ? part * 64 : PAIR ? (part >> 1) * 64 + (part & 1) * 128 : part * wide;
-            const int t0 = WHOLE ? 0 : PAIR ? (part & 1) * 64 : c0;
-            const int chunks = PAIR ? PART / CHUNK : max(0, min(w.width - c0, wide)) >> 4;
+            const int wide = PAIR ? PART : (w.width / 2 + 15) & ~15;
+            const int c0 = PAIR ? part * 64 : part * wide;
+            const int t0 = PAIR ? 0 : c0;
+            const int chunks = PAIR ? PART / S_CHUNK : max(0, min(w.width - c0, wide)) >> 4;
             const int l = (w.tm * Cf::CM + rank) * 128 + q * 32 + lane;
             float acc[PART];
 #pragma unroll
@@ -717,7 +690,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 const uint32_t tbase = tmem_lanes + (uint32_t)(buf * 128);
                 // the lane's scale, or its products with those of the columns
                 const uint32_t my_cols = my_scales + S_COL_SCALES + (uint32_t)c0 * 4;
-                float factors[WHOLE ? 2 : 1];
+                float factors[Cf::CM];
                 auto release = [&]() {  // the product has been read, by all lanes (wait::ld is the warp's)
                     tc_fence_before_sync();
                     if constexpr (PAIR) mbar_arrive_cluster_if(lane == 0, release0 + 8u * (uint32_t)buf);
@@ -729,28 +702,28 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     here = mbar_test(full0 + 8u * (uint32_t)buf, tphase);
                 };
                 // one chunk of columns is read while the one before is added
-                uint32_t v[2][CHUNK];
+                uint32_t v[2][S_CHUNK];
                 if (chunks > 0) tmem_ld_async(tbase, v[0]);
                 const float mine = ld_shared_f1(my_scales + (uint32_t)(q * 32 + lane) * 4);
 #pragma unroll
-                for (int i = 0; i < (WHOLE ? 2 : 1); ++i) {
+                for (int i = 0; i < (Cf::CM); ++i) {
                     factors[i] = mine;
                     if constexpr (!COL_VECTOR) factors[i] *= ld_shared_f1(my_scales + S_COL_SCALES + (uint32_t)((c0 >> 7) + i) * 4);
                 }
 #pragma unroll
-                for (int c = 0; c < PART / CHUNK; ++c) {
+                for (int c = 0; c < PART / S_CHUNK; ++c) {
                     if (c < chunks) {
                         tmem_wait(v[c & 1]);
-                        if (c + 1 < PART / CHUNK && c + 1 < chunks) tmem_ld_async(tbase + (c + 1) * CHUNK, v[(c + 1) & 1]);
-                        if (PAIR && c == PART / CHUNK - 1) release();
+                        if (c + 1 < PART / S_CHUNK && c + 1 < chunks) tmem_ld_async(tbase + (c + 1) * S_CHUNK, v[(c + 1) & 1]);
+                        if (PAIR && c == PART / S_CHUNK - 1) release();
 #pragma unroll
-                        for (int i = 0; i < CHUNK; i += 4) {
-                            const int at = c * CHUNK + i;
-                            const float factor = factors[WHOLE && at >= 64 ? 1 : 0];
+                        for (int i = 0; i < S_CHUNK; i += 4) {
+                            const int at = c * S_CHUNK + i;
+                            const float factor = factors[PAIR && at >= 64 ? 1 : 0];
                             float4 f = make_float4(factor, factor, factor, factor);
-                            if constexpr (COL_VECTOR) f = ld_shared_f4(my_cols + (uint32_t)(at + (WHOLE && at >= 64 ? 64 : 0)) * 4);
-                            float* a = acc + c * CHUNK + i;
-                            S_ADD4(a, v[c & 1] + i, f, factor);
+                            if constexpr (COL_VECTOR) f = ld_shared_f4(my_cols + (uint32_t)(at + (PAIR && at >= 64 ? 64 : 0)) * 4);
+                            float* a = acc + c * S_CHUNK + i;
+                            scaled_add4<COL_VECTOR>(a, v[c & 1] + i, f, factor);
                         }
                     }
                 }
@@ -761,17 +734,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 ok = ok && wait(sfull_bar(slot), sphase);
                 uint32_t my_scales = slots + (uint32_t)(slot * Cf::SLOT_BYTES);
                 const int n = min(Cf::GROUPS, w.k1 - kb0);
-                if (S_UNROLL > 1 && n == Cf::GROUPS) {
 #pragma unroll 1
-                    for (int i = 0; i < Cf::GROUPS; i += S_UNROLL) {
-#pragma unroll
-                        for (int u = 0; u < S_UNROLL; ++u) block(my_scales + u * Cf::SCALE_BYTES);
-                        my_scales += S_UNROLL * Cf::SCALE_BYTES;
-                    }
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < n; ++i, my_scales += Cf::SCALE_BYTES) block(my_scales);
-                }
+                for (int i = 0; i < n; ++i, my_scales += Cf::SCALE_BYTES) block(my_scales);
                 __syncwarp();
                 mbar_arrive_if(lane == 0, sempty_bar(slot));
                 if (++slot == S_SLOTS) {
@@ -786,7 +750,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 float4* mine = reinterpret_cast<float4*>(p.partials + (size_t)blockIdx.x * Cf::SLOT_FLOATS) + et;
 #pragma unroll
                 for (int i = 0; i < PART / 4; ++i)
-                    if (i < chunks * (CHUNK / 4))
+                    if (i < chunks * (S_CHUNK / 4))
                         st_f4(mine + i * S_EPI_THREADS, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
                 // the barrier orders the partial's stores before the count, a release
                 // and acquire at GPU scope
@@ -806,7 +770,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                         p.partials + (size_t)((w.item + x) * Cf::CM + rank) * Cf::SLOT_FLOATS) + et;
 #pragma unroll
                     for (int i = 0; i < PART / 4; ++i)
-                        if (i < chunks * (CHUNK / 4)) {
+                        if (i < chunks * (S_CHUNK / 4)) {
                             const float4 y = ld_cg_f4(from + i * S_EPI_THREADS);
                             acc[4 * i] += y.x;
                             acc[4 * i + 1] += y.y;
@@ -844,7 +808,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                         uint32_t u[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(acc[i + j]);
-                        stage(w.n0 + c0 + i + (WHOLE && i >= 64 ? 64 : 0), u);
+                        stage(w.n0 + c0 + i + (PAIR && i >= 64 ? 64 : 0), u);
                     }
                 } else {
                     const bool bf16 = p.out_dtype == 1;
@@ -853,14 +817,14 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                         uint32_t u[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) u[j] = scaled_pack2(bf16, acc[i + 2 * j], acc[i + 2 * j + 1]);
-                        stage(w.n0 + c0 + i + (WHOLE && i >= 64 ? 64 : 0), u);
+                        stage(w.n0 + c0 + i + (PAIR && i >= 64 ? 64 : 0), u);
                     }
                 }
                 continue;
             }
             if (l >= p.l_total) continue;
             if constexpr (TURNED) {
-                const int count = min(w.valid - c0, chunks * CHUNK);  // columns with a row of C
+                const int count = min(w.valid - c0, chunks * S_CHUNK);  // columns with a row of C
                 const int64_t at = (int64_t)(w.n0 + c0) * p.ldc + l;
 #pragma unroll
                 for (int i = 0; i < PART; ++i)
@@ -870,7 +834,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 const int64_t at = (int64_t)l * p.ldc + w.n0 + c0;
 #pragma unroll
                 for (int i = 0; i < PART; ++i) {
-                    const int c = i + (WHOLE && i >= 64 ? 64 : 0);
+                    const int c = i + (PAIR && i >= 64 ? 64 : 0);
                     if (c0 + c < w.valid) scaled_store(p.out, p.out_dtype, at + c, acc[i]);
                 }
             }

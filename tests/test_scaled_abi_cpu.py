@@ -112,25 +112,36 @@ def test_plan_refusals(status, changes):
     refused(status, B.gemm_scaled_plan_create, *_with(PLAN, **changes))
 
 
-@pytest.mark.parametrize("M,N,K,ctas,turned", [(1, 4096, 4096, 1, 1), (128, 128, 128, 1, 1), (129, 4096, 512, 1, 0), (8192, 8192, 512, 2, 0)])
-def test_offline_plans(M, N, K, ctas, turned):
+@pytest.mark.parametrize("M,N,K,ctas,form", [(1, 4096, 4096, 1, 2), (16, 4096, 4096, 1, 2), (17, 4096, 4096, 1, 1), (128, 128, 128, 1, 1),
+                                             (129, 4096, 512, 1, 0), (8192, 8192, 512, 2, 0)])
+def test_offline_plans(M, N, K, ctas, form):
     p = B.ScaledPlan(M, N, K, 0, 0, 1, 0, 1, 0, 1, offline_sms=152)
-    assert (p.info("ctas"), p.info("turned")) == (ctas, turned)
-    width = -(-M // 16) * 16 if turned else 128 * ctas
-    assert p.info("tile_width") == width and p.info("units") == 152 // ctas
-    tiles = -(-N // 128) if turned else -(-M // (128 * ctas)) * -(-N // (128 * ctas))
-    assert p.info("tiles") == tiles
+    assert (p.info("ctas"), p.info("form")) == (ctas, form)
+    if form != B.GEMM_SCALED_FEW:
+        width = -(-M // 16) * 16 if form else 128 * ctas
+        assert p.info("tile_width") == width and p.info("units") == 152 // ctas
+        tiles = -(-N // 128) if form else -(-M // (128 * ctas)) * -(-N // (128 * ctas))
+        assert p.info("tiles") == tiles
     assert (p.workspace_size > 0) == (p.info("shares") > 1)
     refused(B.GEMM_ERR_NO_DEVICE, p.run, P, P, P, P, P, P)
     assert p.last_status() == B.GEMM_ERR_NO_DEVICE
-    for key, value, status in ((1, 3, UNS), (1, -1, UNS), (2, 2, UNS), (2, -2, UNS), (3, -2, UNS), (3, 0, B.GEMM_ERR_NO_DEVICE), (4, 0, INV)):
+    for key, value, status in ((1, 3, UNS), (1, -1, UNS), (2, 3, UNS), (2, -2, UNS), (3, -2, UNS), (3, 0, B.GEMM_ERR_NO_DEVICE), (4, 0, INV)):
         refused(status, p.set_option, key, value)
-    p.set_option(2, 1)
+    p.set_option(2, B.GEMM_SCALED_TURNED)
     p.set_option(1, 1)
     refused(UNS, p.set_option, 1, 2)  # a turned product has one CTA a unit
-    assert p.info("ctas") == 1
+    assert p.info("ctas") == 1 and p.info("form") == B.GEMM_SCALED_TURNED
+    if M > 16:
+        refused(UNS, p.set_option, 2, B.GEMM_SCALED_FEW)
     refused(INV, p.info, 99)
     p.close()
+
+
+def test_few_rows_need_contiguous_sums():
+    for layouts in ((1, 1), (0, 0)):
+        p = B.ScaledPlan(16, 64, 64, 0, 0, 1, *layouts, 0, 1, offline_sms=152)
+        assert p.info("form") == B.GEMM_SCALED_TURNED
+        refused(UNS, p.set_option, 2, B.GEMM_SCALED_FEW)
 
 
 def test_offline_refusals():

@@ -191,31 +191,31 @@ def test_quantised_layer_end_to_end():
         assert_product(C, *product(A, sa, ka, Bm, sb, kb, la == ROW, lb == ROW), K)
 
 
-# every form of the kernel, whatever the plan would choose: (ctas, turned)
-FORMS = [(1, 0), (2, 0), (1, 1)]
+# every form of the kernel on tensor memory, whatever the plan would choose: (ctas, form)
+FORMS = [(1, B.GEMM_SCALED_STRAIGHT), (2, B.GEMM_SCALED_STRAIGHT), (1, B.GEMM_SCALED_TURNED)]
 
 
-@pytest.mark.parametrize("ctas,turned", FORMS)
+@pytest.mark.parametrize("ctas,form", FORMS)
 @pytest.mark.parametrize("layout_a", [ROW, COL])
 @pytest.mark.parametrize("layout_b", [ROW, COL])
 @pytest.mark.parametrize("scale_a,scale_b", [(VEC, BLOCK), (VEC, VEC), (BLOCK, VEC), (BLOCK, BLOCK)])
 @pytest.mark.parametrize("M,N,K", [(16, 144, 272), (304, 528, 784), (528, 272, 4112)])
-def test_forms(M, N, K, layout_a, layout_b, scale_a, scale_b, ctas, turned):
-    kw = dict(layout_a=layout_a, layout_b=layout_b, scale_a=scale_a, scale_b=scale_b, ctas=ctas, turned=turned)
+def test_forms(M, N, K, layout_a, layout_b, scale_a, scale_b, ctas, form):
+    kw = dict(layout_a=layout_a, layout_b=layout_b, scale_a=scale_a, scale_b=scale_b, ctas=ctas, form=form)
     for out in ("f32", "bf16"):
         Case(M, N, K, out=out, seed=M, **kw).check()
     c = Case(M, N, K, out="f32", integers=True, seed=M, **kw)
-    assert c.plan.info("ctas") == ctas and c.plan.info("turned") == turned
+    assert c.plan.info("ctas") == ctas and c.plan.info("form") == form
     # whole sixteenths below 9 * 16 * 4112 < 2^20: 24 bits, exact in any order
     assert torch.equal(c.run().double(), c.reference()[0])
 
 
-@pytest.mark.parametrize("ctas,turned,M,N,K", [(2, 0, 2048, 2560, 4096), (2, 0, 512, 512, 16384), (1, 0, 1280, 2048, 2304),
+@pytest.mark.parametrize("ctas,form,M,N,K", [(2, 0, 2048, 2560, 4096), (2, 0, 512, 512, 16384), (1, 0, 1280, 2048, 2304),
                                                (1, 0, 128, 128, 20000), (1, 1, 48, 512, 8192), (1, 1, 300, 8192, 4096), (1, 1, 1, 128, 65536)])
 @pytest.mark.parametrize("scale_b", [VEC, BLOCK])
-def test_split_tiles(ctas, turned, M, N, K, scale_b):
+def test_split_tiles(ctas, form, M, N, K, scale_b):
     """Tiles left over a whole round of the units, or fewer than one, cut along k and joined."""
-    c = Case(M, N, K, out="f32", integers=False, seed=K, ctas=ctas, turned=turned, scale_b=scale_b)
+    c = Case(M, N, K, out="f32", integers=False, seed=K, ctas=ctas, form=form, scale_b=scale_b)
     assert c.plan.info("shares") > 1
     first = c.run().clone()
     exact, absolute = c.reference()
@@ -224,9 +224,9 @@ def test_split_tiles(ctas, turned, M, N, K, scale_b):
         assert torch.equal(c.run(), first)
 
 
-@pytest.mark.parametrize("ctas,turned", FORMS)
-def test_timeout_is_reported_and_replays_recover(ctas, turned):
-    c = Case(96, 1024, 8192, seed=5, ctas=ctas, turned=turned)
+@pytest.mark.parametrize("ctas,form", FORMS)
+def test_timeout_is_reported_and_replays_recover(ctas, form):
+    c = Case(96, 1024, 8192, seed=5, ctas=ctas, form=form)
     want = c.run().clone()
     out, graph, stream = torch.empty_like(want), torch.cuda.CUDAGraph(), torch.cuda.Stream()
     with torch.cuda.graph(graph, stream=stream):
@@ -243,3 +243,15 @@ def test_timeout_is_reported_and_replays_recover(ctas, turned):
                 graph.replay()
                 assert c.plan.last_status(stream) == B.GEMM_OK
                 assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 15, 16])
+@pytest.mark.parametrize("N,K", [(1, 16), (17, 128), (33, 144), (4096, 2064), (9999, 1040), (500, 14336)])
+@pytest.mark.parametrize("scale_a,scale_b", [(VEC, BLOCK), (VEC, VEC), (BLOCK, VEC)])
+def test_few_rows(M, N, K, scale_a, scale_b):
+    c = Case(M, N, K, seed=M + N, scale_a=scale_a, scale_b=scale_b)
+    assert c.plan.info("form") == B.GEMM_SCALED_FEW and c.plan.workspace_size == 0
+    c.check()
+    Case(M, N, K, "e5m2", "e4m3", "f32", seed=N, scale_a=scale_a, scale_b=scale_b).check(offset=1)
+    c = Case(M, N, K, out="f32", integers=True, seed=M, scale_a=scale_a, scale_b=scale_b)
+    assert torch.equal(c.run().double(), c.reference()[0])  # sixteenths below 9 * 16 * 14336 < 2^21: 25 bits at most
