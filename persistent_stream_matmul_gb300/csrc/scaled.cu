@@ -208,21 +208,11 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base
                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool W, bool X, int NT>
-gemm_status_t run_few_v(const FewParams& kp, int num_sms, gemm_stream_t stream) {
-    // Two tiles of 16 rows a warp read A half as often; one makes twice the blocks.
-#ifdef F_MT
-    return launch(few_kernel<W, X, F_MT, NT, F_U>, dim3((unsigned)cdiv(kp.N, 16 * F_MT)), dim3(32 * F_WARPS), 0, stream, kp);
-#endif
-    if (cdiv(kp.N, 32) >= 2 * num_sms) return launch(few_kernel<W, X, 2, NT, 2>, dim3((unsigned)cdiv(kp.N, 32)), dim3(32 * F_WARPS), 0, stream, kp);
-    return launch(few_kernel<W, X, 1, NT, 3>, dim3((unsigned)cdiv(kp.N, 16)), dim3(32 * F_WARPS), 0, stream, kp);
-}
-
 gemm_status_t run_few(const gemm_scaled_plan* p, const FewParams& kp, gemm_stream_t stream) {
     const bool w = p->type_b == GEMM_E5M2, x = p->type_a == GEMM_E5M2;
-    auto* fn = kp.M <= 8 ? (w ? (x ? run_few_v<true, true, 1> : run_few_v<true, false, 1>) : (x ? run_few_v<false, true, 1> : run_few_v<false, false, 1>))
-                         : (w ? (x ? run_few_v<true, true, 2> : run_few_v<true, false, 2>) : (x ? run_few_v<false, true, 2> : run_few_v<false, false, 2>));
-    return fn(kp, p->num_sms, stream);
+    auto* fn = kp.M <= 8 ? (w ? (x ? few_kernel<true, true, 1> : few_kernel<true, false, 1>) : (x ? few_kernel<false, true, 1> : few_kernel<false, false, 1>))
+                         : (w ? (x ? few_kernel<true, true, 2> : few_kernel<true, false, 2>) : (x ? few_kernel<false, true, 2> : few_kernel<false, false, 2>));
+    return launch(fn, dim3((unsigned)cdiv(kp.N, 16)), dim3(32 * F_WARPS), 0, stream, kp);
 }
 
 // One operand, as the lanes or the columns side sees it: `rows` of K elements.

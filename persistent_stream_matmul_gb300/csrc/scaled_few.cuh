@@ -17,11 +17,12 @@
 
 namespace psm {
 
-#ifndef F_W
-#define F_W 8
-#define F_MIN 1
-#endif
-constexpr int F_WARPS = F_W;
+constexpr int F_WARPS = 8;
+// k-blocks of a warp in flight, and blocks an SM.  Bytes in flight against registers: us
+// for one row, 14336 x 4096 / 4096 x 14336 / 4096 x 4096, with 2 and 2 blocks 15.0 / 14.6
+// / 5.9; 2 and 3 15.3 / 20.8 / 7.7; 1 and 3 13.1 / 17.2 / 6.3; 3 and 2 15.5 / 14.0 / 6.2
+// (16 rows 18.5, 32.4, 24.9 and 30.1); with 32 rows of B a warp 17.2 / 19.7 / 8.2.
+constexpr int F_BLOCKS = 2, F_RESIDENT = 2;
 constexpr int F_MOST_ROWS = 16;  // of A
 
 struct FewParams {
@@ -55,26 +56,25 @@ __device__ __forceinline__ void few_load(const uint8_t* p, int64_t bytes, uint32
     w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
 }
 
-// MT: tiles of 16 rows of B a warp; NT: tiles of 8 rows of A; U: k-blocks in flight.
-template <bool W_E5M2, bool X_E5M2, int MT, int NT, int U>
-__global__ void __launch_bounds__(32 * F_WARPS, F_MIN) few_kernel(const __grid_constant__ FewParams p) {
-    __shared__ float part[F_WARPS][MT * 16][NT * 8 + 1];
+// NT: tiles of 8 rows of A.
+template <bool W_E5M2, bool X_E5M2, int NT>
+__global__ void __launch_bounds__(32 * F_WARPS, F_RESIDENT) few_kernel(const __grid_constant__ FewParams p) {
+    constexpr int U = F_BLOCKS;
+    __shared__ float part[F_WARPS][16][NT * 8 + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int64_t n0 = (int64_t)blockIdx.x * (MT * 16);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     // rows past the end read the last one's
-    const uint8_t* b[MT][2];
-    const float* sb[MT][2];
+    const uint8_t* b[2];
+    const float* sb[2];
     const uint8_t* a[NT];
     const float* sa[NT][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n = min(n0 + i * 16 + h * 8 + g, p.N - 1);
-            b[i][h] = p.b + n * p.K + t * 32;
-            sb[i][h] = p.sb.s + (n >> p.sb.shift) * p.sb.row;
-        }
+    for (int h = 0; h < 2; ++h) {
+        const int64_t n = min(n0 + h * 8 + g, p.N - 1);
+        b[h] = p.b + n * p.K + t * 32;
+        sb[h] = p.sb.s + (n >> p.sb.shift) * p.sb.row;
+    }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         a[j] = p.a + (int64_t)min(j * 8 + g, p.M - 1) * p.K + t * 32;
@@ -82,13 +82,13 @@ __global__ void __launch_bounds__(32 * F_WARPS, F_MIN) few_kernel(const __grid_c
         for (int h = 0; h < 2; ++h) sa[j][h] = p.sa.s + (int64_t)(min(j * 8 + t * 2 + h, p.M - 1) >> p.sa.shift) * p.sa.row;
     }
     const int k0 = (int)((int64_t)p.kb * warp / F_WARPS), k1 = (int)((int64_t)p.kb * (warp + 1) / F_WARPS);
-    float acc[MT][NT][4] = {};
+    float acc[NT][4] = {};
     grid_dependency_wait();
     grid_launch_dependents();
 #pragma unroll 1
     for (int kb0 = k0; kb0 < k1; kb0 += U) {
-        uint32_t wb[U][MT][2][8], wa[U][NT][8];
-        float fb[U][MT][2], fa[U][NT][2];
+        uint32_t wb[U][2][8], wa[U][NT][8];
+        float fb[U][2], fa[U][NT][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = kb0 + u;
@@ -96,15 +96,11 @@ __global__ void __launch_bounds__(32 * F_WARPS, F_MIN) few_kernel(const __grid_c
             const int64_t at = (int64_t)kb * S_BK, left = kb < k1 ? p.K - at - t * 32 : 0;
             const int64_t gb = (int64_t)min(kb, k1 - 1);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) few_load(b[i][h] + at, left, wb[u][i][h]);
+            for (int h = 0; h < 2; ++h) few_load(b[h] + at, left, wb[u][h]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) few_load(a[j] + at, left, wa[u][j]);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) fb[u][i][h] = sb[i][h][gb * p.sb.group];
+            for (int h = 0; h < 2; ++h) fb[u][h] = sb[h][gb * p.sb.group];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -114,30 +110,26 @@ __global__ void __launch_bounds__(32 * F_WARPS, F_MIN) few_kernel(const __grid_c
         for (int u = 0; u < U; ++u) {
             if (kb0 + u >= k1) break;
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int j = 0; j < NT; ++j) {
+                float d[4] = {};
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float d[4] = {};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint32_t x[4] = {wb[u][i][0][2 * s], wb[u][i][1][2 * s], wb[u][i][0][2 * s + 1], wb[u][i][1][2 * s + 1]};
-                        const uint32_t y[2] = {wa[u][j][2 * s], wa[u][j][2 * s + 1]};
-                        mma_f8_m16n8k32<W_E5M2, X_E5M2>(d, x, y);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(d[c], fb[u][i][c >> 1] * fa[u][j][c & 1], acc[i][j][c]);
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t x[4] = {wb[u][0][2 * s], wb[u][1][2 * s], wb[u][0][2 * s + 1], wb[u][1][2 * s + 1]};
+                    const uint32_t y[2] = {wa[u][j][2 * s], wa[u][j][2 * s + 1]};
+                    mma_f8_m16n8k32<W_E5M2, X_E5M2>(d, x, y);
                 }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[j][c] = fmaf(d[c], fb[u][c >> 1] * fa[u][j][c & 1], acc[j][c]);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) part[warp][i * 16 + (c >> 1) * 8 + g][j * 8 + t * 2 + (c & 1)] = acc[i][j][c];
+        for (int c = 0; c < 4; ++c) part[warp][(c >> 1) * 8 + g][j * 8 + t * 2 + (c & 1)] = acc[j][c];
     __syncthreads();
-    for (int e = threadIdx.x; e < MT * 16 * p.M; e += 32 * F_WARPS) {
-        const int r = e % (MT * 16), m = e / (MT * 16);
+    for (int e = threadIdx.x; e < 16 * p.M; e += 32 * F_WARPS) {
+        const int r = e % (16), m = e / (16);
         if (n0 + r >= p.N) continue;
         float sum = 0.f;
 #pragma unroll
