@@ -24,8 +24,7 @@ struct gemm_scaled_plan {
     int opt_ctas, opt_form;
     // derived
     int form, ctas, turned, col_vector;
-    int width;               // columns of a tile
-    GroupedShape shape;
+    ScaledShape shape;
     size_t counter_bytes, ws_bytes;
     int* d_status;           // G_WORDS words
     int timeouts;            // G_WORD_TIMEOUTS
@@ -99,39 +98,58 @@ int resident_pairs(int dev) {
 gemm_status_t derive(gemm_scaled_plan* p) {
     const bool few = p->M <= F_MOST_ROWS && p->layout_a == GEMM_ROW_MAJOR && p->layout_b == GEMM_COL_MAJOR;
     int form = p->opt_form, ctas = p->opt_ctas;
-    if (form < 0) form = ctas == 2 ? GEMM_SCALED_STRAIGHT : few ? GEMM_SCALED_FEW : p->M <= 128 ? GEMM_SCALED_TURNED : GEMM_SCALED_STRAIGHT;
-    if (ctas == 0) ctas = form == GEMM_SCALED_STRAIGHT && cdiv(p->M, 256) * cdiv(p->N, 256) >= 64 ? 2 : 1;
+    // Turned, a tile's columns fit the rows of A, but each has a scale of its own to be
+    // read and multiplied: us, turned against straight, 4096 x 14336 with 32 rows 18.6 /
+    // 20.8, 4096 x 4096 with 17 rows 11.5 / 14.9, with 48 13.4 / 12.8, 14336 x 4096 with 64
+    // 22.4 / 16.1.
+    if (form < 0) form = ctas == 2 ? GEMM_SCALED_STRAIGHT : few ? GEMM_SCALED_FEW : p->M <= 32 ? GEMM_SCALED_TURNED : GEMM_SCALED_STRAIGHT;
+    // Pairs read their operands half as often, single CTAs make four times the tiles: us,
+    // single against pairs, 512 x 4096 x 4096 (32 pair tiles) 14.0 / 19.7, 256 x 14336 x
+    // 4096 (56) 25.8 / 20.7, 1024 x 4096 x 4096 (64) 23.9 / 19.1.
+    if (ctas == 0) ctas = form == GEMM_SCALED_STRAIGHT && cdiv(p->M, 256) * cdiv(p->N, 256) >= 48 ? 2 : 1;
     if ((form != GEMM_SCALED_STRAIGHT && ctas == 2) || (form == GEMM_SCALED_FEW && !few)) return GEMM_ERR_UNSUPPORTED;
     const int turned = form != GEMM_SCALED_STRAIGHT;
     const int64_t lanes = turned ? p->N : p->M, cols = turned ? p->M : p->N;
     const int tile = 128 * ctas;
-    GroupedShape s{};
-    s.groups = 1;
-    s.rows = (int32_t)cols;
-    s.tiles_m = (int32_t)cdiv(lanes, tile);
-    s.kb = (int32_t)cdiv(p->K, S_BK);
-    s.tile_n = tile;
-    s.tile_shift = ctas == 2 ? 8 : 7;
-    // straight tiles have one width, so that a half's columns share a block's scale
-    s.step = !turned ? tile : p->layout_a == GEMM_ROW_MAJOR ? 16 : 32;
-    s.band = 8;
-    s.least_share = ctas == 2 ? 16 : turned ? 8 : 12;
-    s.units = p->num_sms / ctas;
+    ScaledShape s{};
+    int64_t units = p->num_sms / ctas;
     if (ctas == 2 && !p->offline) {
         const int n = resident_pairs(p->device);
-        if (n > 0) s.units = std::min(s.units, n);
+        if (n > 0) units = std::min<int64_t>(units, n);
     }
-    const int64_t side = std::max<int64_t>(1, cdiv(cols, tile));
-    if (s.tiles_m > 0 && side > MAX_INDEX / s.tiles_m) return GEMM_ERR_UNSUPPORTED;
-    s.may_split = (int64_t)s.units * s.kb < MAX_INDEX;
+    const int64_t tiles_l = cdiv(lanes, tile), side = cdiv(cols, tile), tiles = tiles_l * side, kb = cdiv(p->K, S_BK);
+    if (tiles > MAX_INDEX) return GEMM_ERR_UNSUPPORTED;
+    s.tiles = (int32_t)tiles;
+    s.tiles_l = (int32_t)tiles_l;
+    s.cols = (int32_t)cols;
+    s.side = (int32_t)side;
+    // straight tiles have one width, so that a half's columns share a block's scale
+    const int64_t step = !turned ? tile : p->layout_a == GEMM_ROW_MAJOR ? 16 : 32;
+    s.width = (int32_t)(cdiv(side == 0 ? 1 : cdiv(cols, side), step) * step);
+    // even bands of about eight tiles along the columns side: a round of 76 pairs in a
+    // band of b tiles reads b + 76 / b operand tiles, least near 9
+    const int64_t bands = 2 * side > 24 ? (side + 3) / 8 : 1;
+    s.band = (int32_t)cdiv(side, bands);
+    s.kb = (int32_t)kb;
+    s.units = (int32_t)units;
+    // the tiles left over a whole round, in shares of `least` k-blocks at least: shorter
+    // ones are not worth joining
+    const int64_t least = ctas == 2 ? 16 : turned ? 8 : 12, rest = tiles < units ? tiles : tiles % units;
+    s.shares = 1;
+    if (rest > 0 && kb > least) {
+        const int64_t most = std::max(cdiv(rest * kb, units - rest), least), shares = cdiv(kb, most);
+        if (shares > 1) {
+            s.split = (int32_t)rest;
+            s.shares = (int32_t)shares;
+        }
+    }
     p->form = form;
     p->ctas = ctas;
     p->turned = turned;
     p->col_vector = turned || p->scale_b == GEMM_SCALE_VECTOR;
-    p->width = (int)(cdiv(std::max<int64_t>(1, cdiv(cols, side)), s.step) * s.step);
     p->shape = s;
     p->counter_bytes = p->ws_bytes = 0;
-    if (form != GEMM_SCALED_FEW && p->M > 0 && p->N > 0 && p->K > 0 && grouped_split(s, (int32_t)(side * s.tiles_m), 0).most > 0) {
+    if (form != GEMM_SCALED_FEW && s.shares > 1) {
         const size_t slot = 128 * (size_t)tile * sizeof(float), grid = (size_t)s.units * ctas;
         p->counter_bytes = (grid * 8 + 255) / 256 * 256;
         p->ws_bytes = p->counter_bytes + grid * slot;
@@ -301,9 +319,9 @@ gemm_status_t gemm_scaled_plan_get_info(gemm_scaled_plan_t p, int key, int64_t* 
         case GEMM_SCALED_INFO_CTAS: *value = p->ctas; break;
         case GEMM_SCALED_INFO_FORM: *value = p->form; break;
         case GEMM_SCALED_INFO_UNITS: *value = p->shape.units; break;
-        case GEMM_SCALED_INFO_TILES: *value = grouped_tiles(p->shape, p->shape.rows); break;
-        case GEMM_SCALED_INFO_TILE_WIDTH: *value = p->width; break;
-        case GEMM_SCALED_INFO_SHARES: *value = p->ws_bytes ? grouped_split(p->shape, grouped_tiles(p->shape, p->shape.rows), 0).shares : 1; break;
+        case GEMM_SCALED_INFO_TILES: *value = p->shape.tiles; break;
+        case GEMM_SCALED_INFO_TILE_WIDTH: *value = p->shape.width; break;
+        case GEMM_SCALED_INFO_SHARES: *value = p->form == GEMM_SCALED_FEW ? 1 : p->shape.shares; break;
         default: return GEMM_ERR_INVALID_ARG;
     }
     return GEMM_OK;
@@ -364,7 +382,7 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     // The maps are encoded for every run: they cost well under a microsecond
     // of host time, and nothing is kept by an operand's address.
     ScaledMaps tm{};
-    bool ok = encode_side(&tm.l, l, 128) && encode_side(&tm.r, r, (uint32_t)(p->width / p->ctas));
+    bool ok = encode_side(&tm.l, l, 128) && encode_side(&tm.r, r, (uint32_t)(p->shape.width / p->ctas));
     if (kp.boxes)
         ok = ok && encode(&tm.c, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, size, C, p->N, p->M,
                           (uint32_t)(64 / size), 32, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -372,8 +390,6 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t p, const void* A, const float* 
     if (p->ws_bytes > 0) {
         kp.counters = reinterpret_cast<unsigned long long*>(workspace);
         kp.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + p->counter_bytes);
-    } else {
-        kp.s.may_split = 0;
     }
     kp.epoch = next_epoch();
     kp.status = p->d_status;

@@ -39,7 +39,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "grouped_sched.cuh"
 #include "join.cuh"
 #include "ptx.cuh"
 
@@ -53,7 +52,7 @@ constexpr int S_EPI_THREADS = 32 * S_EPI_WARPS;
 constexpr int S_QUEUE = 4;
 constexpr int S_SLOTS = 2;       // of scales, GROUPS k-blocks each
 constexpr int S_COL_SCALES = 128 * 4;  // a k-block's: the lanes' scales, then the columns'
-constexpr int S_CHUNK = 16;  // columns a load from tensor memory
+constexpr int S_CHUNK = 16;  // columns that a turned tile's half is cut into
 // Registers a thread of the pair kernel's epilogue; the other four warps give what its
 // eight take above the launch's 168 (2 x 48 = 96).
 constexpr int S_EPI_REGS = 216, S_OTHER_REGS = 3 * 168 - 2 * S_EPI_REGS;
@@ -74,7 +73,7 @@ struct ScaledCfg {
     static constexpr int BUFFERS = 4 / PRODUCTS;  // of each, 128 columns of tensor memory
     static constexpr int SCALE_BYTES = S_COL_SCALES + (COL_VECTOR ? TILE_N * 4 : 16);  // of a k-block
     static constexpr int SLOT_BYTES = GROUPS * SCALE_BYTES;
-    static constexpr int QUEUE_BYTES = S_QUEUE * 48;
+    static constexpr int QUEUE_BYTES = S_QUEUE * 32;
     static constexpr int BAR_BYTES = 384;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + S_EPI_WARPS * BOXES * 2048 + S_SLOTS * SLOT_BYTES + QUEUE_BYTES + BAR_BYTES + 1024;
     static constexpr int SLOT_FLOATS = 128 * TILE_N;
@@ -82,6 +81,54 @@ struct ScaledCfg {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(BARS * 8 + 32 <= BAR_BYTES, "barrier area");
 };
+
+// Tiles and who runs them.  Tiles that do not fill a round of the units (all of them
+// when there are fewer than units) run first, the k-blocks of each cut into near-equal
+// shares, one a unit at most; then every unit takes whole tiles in turn.  The plan has
+// worked out what does not depend on the unit: the first copy starts some 1000 cycles
+// after the launch instead of 4000 with the general scheduler of the grouped products.
+struct ScaledShape {
+    int32_t tiles, tiles_l;       // all tiles; along the lanes side
+    int32_t cols, side, width;    // extent of the columns side, tiles along it, and their columns
+    int32_t band;                 // tiles along the columns side that are visited before the next lanes tile
+    int32_t kb, units;
+    int32_t split, shares;        // the first tiles are cut into so many shares
+};
+
+struct ScaledWork {
+    int32_t item;                 // the unit of the first share; -1: the end
+    int32_t shares, tm, n0;       // tile along the lanes; first column
+    int32_t valid, k0, k1;        // columns of C; k-blocks
+};
+
+// The unit's work number `step`; false past its last.
+__device__ __forceinline__ bool scaled_work(const ScaledShape& s, int32_t unit, int32_t step, ScaledWork& w) {
+    const bool has = unit < s.split * s.shares;
+    uint32_t tile;
+    w.shares = 1;
+    w.item = unit;
+    w.k0 = 0;
+    w.k1 = s.kb;
+    if (has && step == 0) {
+        const int32_t t = unit / s.shares, share = unit - t * s.shares;
+        tile = (uint32_t)t;
+        w.shares = s.shares;
+        w.item = unit - share;
+        w.k0 = (int32_t)((int64_t)s.kb * share / s.shares);
+        w.k1 = (int32_t)((int64_t)s.kb * (share + 1) / s.shares);
+    } else {
+        tile = (uint32_t)s.split + (uint32_t)unit + (uint32_t)(step - has) * (uint32_t)s.units;
+    }
+    if (tile >= (uint32_t)s.tiles) return false;
+    const uint32_t in_band = (uint32_t)s.band * (uint32_t)s.tiles_l;
+    const uint32_t b = s.band == s.side ? 0u : tile / in_band;
+    const uint32_t local = tile - b * in_band;
+    const uint32_t first = b * (uint32_t)s.band, wide = min((uint32_t)s.side - first, (uint32_t)s.band);
+    w.tm = (int32_t)(wide == 1 ? local : local / wide);
+    w.n0 = (int32_t)(first + local - (uint32_t)w.tm * wide) * s.width;
+    w.valid = min(s.cols - w.n0, s.width);
+    return true;
+}
 
 // Scales of one operand: that of row r and k-block g at
 // s[(r >> shift) * row + g * group].
@@ -92,7 +139,7 @@ struct ScaledScales {
 };
 
 struct ScaledParams {
-    GroupedShape s;               // one group: the columns side
+    ScaledShape s;
     int32_t l_total;              // extent of the lanes side
     ScaledScales l, r;
     void* out;
@@ -359,7 +406,6 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * Cf::BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 8 * Cf::BARS + 4);
     volatile int* last_flag = reinterpret_cast<volatile int*>(bar_area + 8 * Cf::BARS + 8);
-    int32_t* table = reinterpret_cast<int32_t*>(bar_area + 8 * Cf::BARS + 16);  // offsets, first tiles
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -388,9 +434,6 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             mbar_init(qempty_bar(s), readers);
         }
         *abort_flag = 0;
-        table[0] = table[2] = 0;
-        table[1] = p.s.rows;
-        table[3] = grouped_tiles(p.s, p.s.rows);
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -421,7 +464,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     };
 
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, p.pipe_limit_ns, abort_flag); };
-    GroupedWork w{};
+    ScaledWork w{};
     int qslot = 0;
     uint32_t qphase = 0;
     // The next piece of work, for a whole warp; false at the end or after a
@@ -432,16 +475,15 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             if (lane == 0) fail_pipe();
             return false;
         }
-        const uint32_t at = queue + (uint32_t)qslot * 48u;
-        const uint4 a = ld_shared_u4(at), b = ld_shared_u4(at + 16), c = ld_shared_u4(at + 32);
+        const uint32_t at = queue + (uint32_t)qslot * 32u;
+        const uint4 a = ld_shared_u4(at), b = ld_shared_u4(at + 16);
         __syncwarp();
         if (lane == 0) mbar_arrive(qempty_bar(qslot));
         if (++qslot == S_QUEUE) {
             qslot = 0;
             qphase ^= 1u;
         }
-        w = GroupedWork{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y,
-                        (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
+        w = ScaledWork{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z};
         return w.item >= 0;
     };
 
@@ -456,7 +498,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             const uint32_t full0_c = PAIR ? mapa_shared(full_bar(0), 0) : 0u;
             while (ok && next_work()) {
                 const int l0 = (w.tm * Cf::CM + rank) * 128;
-                const int cols = w.width / Cf::CM;  // this CTA's columns
+                const int cols = p.s.width / Cf::CM;  // this CTA's columns
                 const int r0 = w.n0 + rank * cols;
                 const uint32_t r_bytes = p.r_mn ? (uint32_t)Cf::R_BYTES : (uint32_t)cols * S_BK;
                 for (int kb = w.k0; kb < w.k1; ++kb) {
@@ -508,7 +550,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                 // 64 columns: of 128 bytes a row, or rows of 128 bytes
                 const uint64_t r_part = p.r_mn ? 64 >> 4 : (64 * 128) >> 4;
                 while (ok && next_work()) {
-                    const uint32_t idesc = p.idesc | ((uint32_t)(w.width / Cf::PRODUCTS >> 3) << 17);
+                    const uint32_t idesc = p.idesc | ((uint32_t)(p.s.width / Cf::PRODUCTS >> 3) << 17);
                     for (int kb = w.k0; kb < w.k1; ++kb) {
                         // the barriers' states are asked for together, as each answer takes
                         // some hundred cycles, and waited for where one is not ready
@@ -611,7 +653,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                         }
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
-                            if (COL_VECTOR ? i * 32 < w.width : lane < Cf::CM) cp_async_4(at + S_COL_SCALES + i * 128, rs[i]);
+                            if (COL_VECTOR ? i * 32 < p.s.width : lane < Cf::CM) cp_async_4(at + S_COL_SCALES + i * 128, rs[i]);
                             rs[i] += p.r.group;
                         }
                         at += Cf::SCALE_BYTES;
@@ -626,26 +668,21 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             cp_async_wait_all();  // the copies are complete before the CTA ends
         } else if (warp == 3) {
             // -------------------------------------------------------- scheduler
-            const uint64_t tag = grouped_tag(p.epoch, p.status);
-            const GroupedTables tab{table, table + 2};
-            const int32_t items = table[3];
-            const GroupedSplit split = grouped_split(p.s, items, 0);
             bool more = true;
             for (int32_t step = 0; more; ++step) {
-                more = grouped_work(p.s, tab, split, unit, step, items, w);
+                more = scaled_work(p.s, unit, step, w);
                 if (!more) w.item = -1;
                 if (!__all_sync(0xffffffffu, wait(qempty_bar(qslot), qphase ^ 1u))) {
                     if (lane == 0) fail_pipe();
                     break;
                 }
                 if (lane == 0) {
-                    const uint32_t at = queue + (uint32_t)qslot * 48u;
-                    st_shared_u4(at, w.item, w.shares, w.group, w.tm);
-                    st_shared_u4(at + 16, w.n0, w.width, w.valid, w.r0);
-                    st_shared_u4(at + 32, w.r1, w.k0, w.k1, w.kb);
+                    const uint32_t at = queue + (uint32_t)qslot * 32u;
+                    st_shared_u4(at, w.item, w.shares, w.tm, w.n0);
+                    st_shared_u4(at + 16, w.valid, w.k0, w.k1, 0);
                     mbar_arrive(qfull_bar(qslot));
                     if (more && w.shares > 1 && w.item == unit)  // this unit has the first share
-                        grouped_open_counter(p.counters + (size_t)unit * Cf::CM + rank, tag);
+                        grouped_open_counter(p.counters + (size_t)unit * Cf::CM + rank, grouped_tag(p.epoch, p.status));
                 }
                 __syncwarp();
                 if (++qslot == S_QUEUE) {
@@ -670,10 +707,10 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         while (next_work()) {
             // this warp's columns: c0 .. c0 + S_CHUNK * chunks - 1 of the tile, from t0 on of
             // a product's in tensor memory
-            const int wide = PAIR ? PART : (w.width / 2 + 15) & ~15;
+            const int wide = PAIR ? PART : (p.s.width / 2 + 15) & ~15;
             const int c0 = PAIR ? part * 64 : part * wide;
             const int t0 = PAIR ? 0 : c0;
-            const int chunks = PAIR ? PART / S_CHUNK : max(0, min(w.width - c0, wide)) >> 4;
+            const int chunks = !TURNED ? PART / S_CHUNK : max(0, min(p.s.width - c0, wide)) >> 4;
             const int l = (w.tm * Cf::CM + rank) * 128 + q * 32 + lane;
             float acc[PART];
 #pragma unroll
@@ -701,33 +738,40 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     }
                     here = mbar_test(full0 + 8u * (uint32_t)buf, tphase);
                 };
-                // one chunk of columns is read while the one before is added
-                uint32_t v[2][S_CHUNK];
-                if (chunks > 0) tmem_ld_async(tbase, v[0]);
+                // Columns read from tensor memory at once: a load takes some 100 cycles, whatever
+                // its size, so many; but few where each column's scale is read from shared
+                // memory beside them, and then one batch is read while the one before is added.
+                // us, 16 against 64 at once: 8192 x 14336 x 4096 with blocks 368 / 356, with
+                // vectors 496 / 561.
+                constexpr int BATCH = COL_VECTOR ? 16 : 64, BATCHES = PART / BATCH, READS = COL_VECTOR ? 2 : 1;
+                const int batches = TURNED ? chunks : BATCHES;
+                uint32_t v[READS][BATCH];
+                if (batches > 0) tmem_ld_async(tbase, v[0]);
                 const float mine = ld_shared_f1(my_scales + (uint32_t)(q * 32 + lane) * 4);
 #pragma unroll
-                for (int i = 0; i < (Cf::CM); ++i) {
+                for (int i = 0; i < Cf::CM; ++i) {
                     factors[i] = mine;
                     if constexpr (!COL_VECTOR) factors[i] *= ld_shared_f1(my_scales + S_COL_SCALES + (uint32_t)((c0 >> 7) + i) * 4);
                 }
 #pragma unroll
-                for (int c = 0; c < PART / S_CHUNK; ++c) {
-                    if (c < chunks) {
-                        tmem_wait(v[c & 1]);
-                        if (c + 1 < PART / S_CHUNK && c + 1 < chunks) tmem_ld_async(tbase + (c + 1) * S_CHUNK, v[(c + 1) & 1]);
-                        if (PAIR && c == PART / S_CHUNK - 1) release();
+                for (int b = 0; b < BATCHES; ++b) {
+                    if (b < batches) {
+                        uint32_t (&r)[BATCH] = v[b % READS];
+                        if (READS == 1 && b > 0) tmem_ld_async(tbase + b * BATCH, r);
+                        tmem_wait(r);
+                        if (READS == 2 && b + 1 < BATCHES && b + 1 < batches) tmem_ld_async(tbase + (b + 1) * BATCH, v[(b + 1) % READS]);
+                        if (!TURNED && b == BATCHES - 1) release();
 #pragma unroll
-                        for (int i = 0; i < S_CHUNK; i += 4) {
-                            const int at = c * S_CHUNK + i;
+                        for (int i = 0; i < BATCH; i += 4) {
+                            const int at = b * BATCH + i;
                             const float factor = factors[PAIR && at >= 64 ? 1 : 0];
                             float4 f = make_float4(factor, factor, factor, factor);
                             if constexpr (COL_VECTOR) f = ld_shared_f4(my_cols + (uint32_t)(at + (PAIR && at >= 64 ? 64 : 0)) * 4);
-                            float* a = acc + c * S_CHUNK + i;
-                            scaled_add4<COL_VECTOR>(a, v[c & 1] + i, f, factor);
+                            scaled_add4<COL_VECTOR>(acc + at, r + i, f, factor);
                         }
                     }
                 }
-                if (!PAIR) release();
+                if (TURNED) release();
             };
 #pragma unroll 1
             for (int kb0 = w.k0; kb0 < w.k1; kb0 += Cf::GROUPS) {
@@ -824,11 +868,21 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             }
             if (l >= p.l_total) continue;
             if constexpr (TURNED) {
-                const int count = min(w.valid - c0, chunks * S_CHUNK);  // columns with a row of C
+                // a column is a row of C: 32 lanes store neighbours
+                const int count = min(w.valid - c0, chunks * S_CHUNK);
                 const int64_t at = (int64_t)(w.n0 + c0) * p.ldc + l;
+                if (p.out_dtype == 2) {
+                    float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
-                for (int i = 0; i < PART; ++i)
-                    if (i < count) scaled_store(p.out, p.out_dtype, at + (int64_t)i * p.ldc, acc[i]);
+                    for (int i = 0; i < PART; ++i)
+                        if (i < count) out[(int64_t)i * p.ldc] = acc[i];
+                } else {
+                    const bool bf16 = p.out_dtype == 1;
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+                    for (int i = 0; i < PART; ++i)
+                        if (i < count) out[(int64_t)i * p.ldc] = (uint16_t)scaled_pack2(bf16, acc[i], 0.f);
+                }
             } else {
                 // rows of C that tensor copies cannot address: element by element
                 const int64_t at = (int64_t)l * p.ldc + w.n0 + c0;

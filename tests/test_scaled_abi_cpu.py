@@ -112,7 +112,7 @@ def test_plan_refusals(status, changes):
     refused(status, B.gemm_scaled_plan_create, *_with(PLAN, **changes))
 
 
-@pytest.mark.parametrize("M,N,K,ctas,form", [(1, 4096, 4096, 1, 2), (16, 4096, 4096, 1, 2), (17, 4096, 4096, 1, 1), (128, 128, 128, 1, 1),
+@pytest.mark.parametrize("M,N,K,ctas,form", [(1, 4096, 4096, 1, 2), (16, 4096, 4096, 1, 2), (17, 4096, 4096, 1, 1), (32, 128, 128, 1, 1), (33, 4096, 1024, 1, 0),
                                              (129, 4096, 512, 1, 0), (8192, 8192, 512, 2, 0)])
 def test_offline_plans(M, N, K, ctas, form):
     p = B.ScaledPlan(M, N, K, 0, 0, 1, 0, 1, 0, 1, offline_sms=152)
