@@ -105,7 +105,7 @@ gemm_status_t gemm_scaled_quantize_both(const void *x, int64_t ldx, int64_t rows
  * (hidden > GEMM_NORM_MAX_HIDDEN, rows > 2^31 - 1024, an operand not aligned to its
  * element), LAUNCH.  rows == 0 or hidden == 0: nothing is written.
  */
-#define GEMM_NORM_MAX_HIDDEN 65536
+#define GEMM_NORM_MAX_HIDDEN 32768
 gemm_status_t gemm_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldres,
                             const void *weight, float eps, int64_t rows, int64_t hidden,
                             gemm_dtype_t dtype, void *sum, int64_t ldsum, void *y, int64_t ldy,

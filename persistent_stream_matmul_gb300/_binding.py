@@ -60,7 +60,7 @@ GEMM_F32 = 2                       # an output type of scaled products only
 GEMM_SCALE_VECTOR, GEMM_SCALE_BLOCK = 0, 1
 GEMM_SCALE_GROUP = 128
 GEMM_QUANTIZE_ROWS, GEMM_QUANTIZE_COLS, GEMM_QUANTIZE_BLOCKS = 0, 1, 2
-GEMM_NORM_MAX_HIDDEN = 65536
+GEMM_NORM_MAX_HIDDEN = 32768
 GEMM_SCALED_STRAIGHT, GEMM_SCALED_TURNED, GEMM_SCALED_FEW = 0, 1, 2
 GEMM_SCALED_OPT_CTAS, GEMM_SCALED_OPT_FORM, GEMM_SCALED_OPT_INJECT_GIVE_UP = 1, 2, 3
 SCALED_INFO = {"ctas": 1, "form": 2, "units": 3, "tiles": 4, "tile_width": 5, "shares": 6}

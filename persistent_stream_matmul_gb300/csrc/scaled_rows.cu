@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
 // Tiles of 128 x 128: vectors along the columns, a block, or vectors along both
 // dimensions.  A thread has eight columns of eight rows, 16 apart.
 template <typename T, bool E5M2, bool ALIGNED, int KIND, bool BOTH>
-__global__ void __launch_bounds__(256) quantize_tile_kernel(QuantizeArgs a) {
+__global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(QuantizeArgs a) {
     __shared__ float part[8][GROUP];
     const int lane = threadIdx.x & 15, r = threadIdx.x >> 4, warp = threadIdx.x >> 5;
     const int64_t tile_row = blockIdx.x / a.row_groups;
@@ -318,60 +318,101 @@ __device__ __forceinline__ float over_row(float v, float* part) {
     return v;
 }
 
+// Elements h .. h + 7 of a row of n, zeros past its end.
+template <bool ALIGNED, bool ONCE = true>
+__device__ __forceinline__ Chunk load_masked(const uint16_t* row, int h, int n) {
+    if (h >= n) return Chunk{};
+    if constexpr (ALIGNED && !ONCE) return load_word<false>(row + h);
+    Chunk c = load_chunk<ALIGNED>(row, h, n);
+    if constexpr (!ALIGNED)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (h + i >= n) c.w[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+    return c;
+}
+
 // A row of `blockDim.x` threads, V chunks each, strided by blockDim.x, so that
-// 16 lanes have a group.  The row stays in registers between the sum and the
-// output.
-template <typename T, bool E5M2, bool ALIGNED, int V>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
-    __shared__ float part[32];
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const bool in = row < a.rows;
+// 16 lanes have a group.  Bound by memory.  The row stays in registers between the
+// sum and the output, and so does the weight over all the rows that a block takes
+// (every gridDim.x x blockDim.y th); AHEAD: the next row is on its way while this
+// one is summed and written, which keeps reads in flight over the barrier.
+template <typename T, bool E5M2, bool ALIGNED, int V, bool AHEAD, int THREADS, int RESIDENT>
+__global__ void __launch_bounds__(THREADS, RESIDENT) norm_kernel(NormArgs a) {
+    __shared__ float part[2][32];
     const int n = a.hidden;
     grid_dependency_wait();
     grid_launch_dependents();
-    Chunk s[V];
-    float square = 0.f;
+    auto added = [&](const Chunk& x, const Chunk& r) {
+        float f[8], g[8];
+        unpack<T>(x, f);
+        unpack<T>(r, g);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int h = (v * blockDim.x + threadIdx.x) * 8;
-        s[v] = Chunk{};
-        if (!in || h >= n) continue;
-        float x[8];
-        load_row<T, ALIGNED>(a.x + row * a.ldx, h, n, x);
-        if (a.residual) {
-            float y[8];
-            load_row<T, ALIGNED>(a.residual + row * a.ldres, h, n, y);
+        for (int i = 0; i < 8; ++i) f[i] += g[i];
+        return pack<T>(f);
+    };
+    // without AHEAD registers are short: the sum is made at once, the weight read when used
+    Chunk w[AHEAD ? V : 1], x[V], r[AHEAD ? V : 1];
+    auto load = [&](int64_t row) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] += y[i];
+        for (int v = 0; v < V; ++v) {
+            const int h = (v * blockDim.x + threadIdx.x) * 8;
+            x[v] = Chunk{};
+            if (AHEAD) r[v] = Chunk{};
+            if (row >= a.rows) continue;
+            x[v] = load_masked<ALIGNED>(a.x + row * a.ldx, h, n);
+            if (!a.residual) continue;
+            const Chunk c = load_masked<ALIGNED>(a.residual + row * a.ldres, h, n);
+            if (AHEAD) r[v] = c;
+            else x[v] = added(x[v], c);
         }
-        s[v] = pack<T>(x);
-        unpack<T>(s[v], x);
+    };
+    int64_t first = (int64_t)blockIdx.x * blockDim.y;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    load(first + threadIdx.y);
+    if (AHEAD)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) square = fmaf(x[i], x[i], square);
-    }
-    square = over_row(square, part);
-    const float rstd = __frsqrt_rn(__fdiv_rn(square, (float)n) + a.eps);
-    if (in && threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+        for (int v = 0; v < V; ++v) w[v] = load_masked<ALIGNED, false>(a.weight, (v * blockDim.x + threadIdx.x) * 8, n);
+    int turn = 0;
+#pragma unroll 1
+    for (; first < a.rows; first += step, turn ^= 1) {
+        const int64_t row = first + threadIdx.y;
+        const bool in = row < a.rows;
+        Chunk s[V];
+        float square = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int h = (v * blockDim.x + threadIdx.x) * 8;
-        const bool here = in && h < n;
-        float x[8], w[8];
-        unpack<T>(s[v], x);
-        if (here) {
-            if (a.sum) store_16bit<ALIGNED>(a.sum + row * a.ldsum, h, n, s[v]);
-            load_row<T, ALIGNED>(a.weight, h, n, w);
+        for (int v = 0; v < V; ++v) {
+            s[v] = AHEAD && a.residual ? added(x[v], r[v]) : x[v];
+            float f[8];
+            unpack<T>(s[v], f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * w[i];
-            if (a.y) store_16bit<ALIGNED>(a.y + row * a.ldy, h, n, pack<T>(x));
+            for (int i = 0; i < 8; ++i) square = fmaf(f[i], f[i], square);
         }
-        if (a.q) {
-            const float m = over_half(here ? magnitude(x) : 0.f);
+        if (AHEAD) load(row + step);
+        square = over_row(square, part[turn]);
+        const float rstd = __frsqrt_rn(__fdiv_rn(square, (float)n) + a.eps);
+        if (in && threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int h = (v * blockDim.x + threadIdx.x) * 8;
+            const bool here = in && h < n;
+            float f[8], g[8];
+            unpack<T>(s[v], f);
+            unpack<T>(AHEAD ? w[v] : load_masked<ALIGNED, false>(a.weight, h, n), g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
             if (here) {
-                store_quantized<ALIGNED>(a.q + row * a.ldq, h, n, quantized<E5M2, false>(x, inverse_of<E5M2>(m)));
-                if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(h / GROUP) * a.rows + row] = scale_of<E5M2>(m);
+                if (a.sum) store_16bit<ALIGNED>(a.sum + row * a.ldsum, h, n, s[v]);
+                if (a.y) store_16bit<ALIGNED>(a.y + row * a.ldy, h, n, pack<T>(f));
+            }
+            if (a.q) {
+                const float m = over_half(magnitude(f));
+                if (here) {
+                    store_quantized<ALIGNED>(a.q + row * a.ldq, h, n, quantized<E5M2, false>(f, inverse_of<E5M2>(m)));
+                    if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(h / GROUP) * a.rows + row] = scale_of<E5M2>(m);
+                }
             }
         }
+        if (!AHEAD) load(row + step);
     }
 }
 
@@ -384,52 +425,71 @@ struct NormGradArgs {
     float* part;  // gridDim.x x hidden, or null
 };
 
-// As norm_kernel, one row a block and the next gridDim.x further on, so that a
-// thread has the same columns of every row and sums their dweight in registers.
-template <typename T, bool ALIGNED, int V>
-__global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
+// As norm_kernel, a row a block: a thread has the same columns of every row and
+// sums their dweight in registers.
+template <typename T, bool ALIGNED, int V, bool AHEAD, int THREADS, int RESIDENT>
+__global__ void __launch_bounds__(THREADS, RESIDENT) norm_grad_kernel(NormGradArgs a) {
     __shared__ float part[2][32];
     const int n = a.hidden;
     grid_dependency_wait();
     grid_launch_dependents();
-    float dw[V][8] = {};
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        Chunk dy[V], s[V];
-        const float rstd = a.rstd[row];
-        float dot = 0.f;
+    Chunk w[AHEAD ? V : 1], dy[V], s[V], d[AHEAD ? V : 1];
+    auto weight = [&](int v) { return load_masked<ALIGNED, false>(a.weight, (v * blockDim.x + threadIdx.x) * 8, n); };
+    float rstd = 0.f;
+    auto load = [&](int64_t row) {
+        if (row >= a.rows) return;
+        rstd = a.rstd[row];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int h = (v * blockDim.x + threadIdx.x) * 8;
-            dy[v] = s[v] = Chunk{};
-            if (h >= n) continue;
-            float g[8], x[8], w[8];
-            load_row<T, ALIGNED>(a.dy + row * a.lddy, h, n, g);
-            load_row<T, ALIGNED>(a.s + row * a.lds, h, n, x);
-            load_row<T, ALIGNED>(a.weight, h, n, w);
-            dy[v] = pack<T>(g);
-            s[v] = pack<T>(x);
+            dy[v] = load_masked<ALIGNED>(a.dy + row * a.lddy, h, n);
+            s[v] = load_masked<ALIGNED>(a.s + row * a.lds, h, n);
+            if (AHEAD) d[v] = a.dsum ? load_masked<ALIGNED>(a.dsum + row * a.lddsum, h, n) : Chunk{};
+        }
+    };
+    load(blockIdx.x);
+    if (AHEAD)
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[v] = weight(v);
+    float dw[V][8] = {};
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const float scale = rstd;
+        Chunk p[V], q[V], e[AHEAD ? V : 1];
+        float dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float g[8], f[8], c[8];
+            unpack<T>(dy[v], g);
+            unpack<T>(s[v], f);
+            unpack<T>(AHEAD ? w[v] : weight(v), c);
+            p[v] = dy[v];
+            q[v] = s[v];
+            if (AHEAD) e[v] = d[v];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float p = g[i] * (x[i] * rstd);
-                dw[v][i] += p;
-                dot = fmaf(p, w[i], dot);
+                const float x = g[i] * (f[i] * scale);
+                dw[v][i] += x;
+                dot = fmaf(x, c[i], dot);
             }
         }
+        if (AHEAD) load(row + gridDim.x);
         const float mean = __fdiv_rn(over_row(dot, part[turn]), (float)n);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int h = (v * blockDim.x + threadIdx.x) * 8;
             if (h >= n) continue;
-            float g[8], x[8], w[8], d[8] = {};
-            unpack<T>(dy[v], g);
-            unpack<T>(s[v], x);
-            load_row<T, ALIGNED>(a.weight, h, n, w);
-            if (a.dsum) load_row<T, ALIGNED>(a.dsum + row * a.lddsum, h, n, d);
+            float g[8], f[8], c[8], b[8];
+            unpack<T>(p[v], g);
+            unpack<T>(q[v], f);
+            unpack<T>(AHEAD ? w[v] : weight(v), c);
+            unpack<T>(AHEAD ? e[v] : a.dsum ? load_masked<ALIGNED>(a.dsum + row * a.lddsum, h, n) : Chunk{}, b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = rstd * (w[i] * g[i] - (x[i] * rstd) * mean) + d[i];
+            for (int i = 0; i < 8; ++i) g[i] = scale * (c[i] * g[i] - (f[i] * scale) * mean) + b[i];
             store_16bit<ALIGNED>(a.dx + row * a.lddx, h, n, pack<T>(g));
         }
+        if (!AHEAD) load(row + gridDim.x);
     }
     if (a.part)
 #pragma unroll
@@ -468,44 +528,66 @@ dim3 norm_block(int64_t hidden, int v) {
     return dim3(width, width < 256 ? 256 / width : 1, 1);
 }
 
-int norm_chunks(int64_t hidden) {
-    const int64_t chunks = cdiv(hidden, 8);
-    return chunks <= 256 ? 1 : chunks <= 1024 ? 2 : chunks <= 4096 ? 4 : 8;
+constexpr int SMS = 152;
+#ifndef N_RES
+#define N_RES 3
+#define G_RES 2
+#endif
+// Blocks of `threads` that are resident at once where `resident` of `most` are.
+int64_t resident_blocks(int64_t threads, int most, int resident) {
+    return SMS * std::max<int64_t>(1, most * resident / threads);
 }
 
-// Blocks of the gradient, each with a part of dweight.
-constexpr int64_t GRAD_BLOCKS = 456;
+template <typename T, bool E5M2, bool ALIGNED>
+gemm_status_t norm_v(const NormArgs& a, gemm_stream_t stream) {
+    const int64_t chunks = cdiv(a.hidden, 8);
+    auto run = [&](void (*fn)(NormArgs), int v, int most, int resident) {
+        const dim3 block = norm_block(a.hidden, v);
+        const int64_t grid = std::min(cdiv(a.rows, block.y), resident_blocks(block.x * block.y, most, resident));
+        return launch(fn, dim3((unsigned)grid), block, 0, stream, a);
+    };
+    if (chunks <= 256) return run(norm_kernel<T, E5M2, ALIGNED, 1, true, 256, N_RES>, 1, 256, N_RES);
+    if (chunks <= 512) return run(norm_kernel<T, E5M2, ALIGNED, 2, true, 256, N_RES>, 2, 256, N_RES);
+    if (chunks <= 1024) return run(norm_kernel<T, E5M2, ALIGNED, 2, true, 512, 2>, 2, 512, 2);
+    if (chunks <= 2048) return run(norm_kernel<T, E5M2, ALIGNED, 2, true, 1024, 1>, 2, 1024, 1);
+    return run(norm_kernel<T, E5M2, ALIGNED, 4, false, 1024, 1>, 4, 1024, 1);
+}
 
 template <typename T, bool E5M2>
 gemm_status_t norm(const NormArgs& a, bool aligned, gemm_stream_t stream) {
-    const int v = norm_chunks(a.hidden);
-    const dim3 block = norm_block(a.hidden, v);
-    const int64_t grid = cdiv(a.rows, block.y);
-    void (*fn)(NormArgs);
-    if (aligned)
-        fn = v == 1 ? norm_kernel<T, E5M2, true, 1> : v == 2 ? norm_kernel<T, E5M2, true, 2>
-             : v == 4 ? norm_kernel<T, E5M2, true, 4> : norm_kernel<T, E5M2, true, 8>;
-    else
-        fn = v == 1 ? norm_kernel<T, E5M2, false, 1> : v == 2 ? norm_kernel<T, E5M2, false, 2>
-             : v == 4 ? norm_kernel<T, E5M2, false, 4> : norm_kernel<T, E5M2, false, 8>;
-    return launch(fn, dim3((unsigned)grid), block, 0, stream, a);
+    return (aligned ? norm_v<T, E5M2, true> : norm_v<T, E5M2, false>)(a, stream);
+}
+
+// How the gradient of rows of `hidden` is launched.
+struct GradShape {
+    int v, most, resident;
+    int64_t threads, blocks;
+};
+
+GradShape grad_shape(int64_t rows, int64_t hidden) {
+    const int64_t chunks = cdiv(hidden, 8);
+    GradShape s = chunks <= 256 ? GradShape{1, 256, G_RES} : chunks <= 512 ? GradShape{2, 256, G_RES} : chunks <= 1024 ? GradShape{2, 512, 1}
+                : chunks <= 2048 ? GradShape{4, 512, 1} : GradShape{4, 1024, 1};
+    s.threads = norm_block(hidden, s.v).x;
+    s.blocks = std::min(rows, resident_blocks(s.threads, s.most, s.resident));
+    return s;
+}
+
+template <typename T, bool ALIGNED>
+gemm_status_t norm_grad_v(const NormGradArgs& a, float* dweight, gemm_stream_t stream) {
+    const GradShape s = grad_shape(a.rows, a.hidden);
+    auto* fn = s.v == 1       ? norm_grad_kernel<T, ALIGNED, 1, true, 256, G_RES>
+               : s.v == 2     ? (s.most == 256 ? norm_grad_kernel<T, ALIGNED, 2, true, 256, G_RES> : norm_grad_kernel<T, ALIGNED, 2, true, 512, 1>)
+               : s.most == 512 ? norm_grad_kernel<T, ALIGNED, 4, false, 512, 1>
+                               : norm_grad_kernel<T, ALIGNED, 4, false, 1024, 1>;
+    const gemm_status_t st = launch(fn, dim3((unsigned)s.blocks), dim3((unsigned)s.threads), 0, stream, a);
+    if (st != GEMM_OK || !dweight) return st;
+    return launch(norm_weight_kernel, dim3((unsigned)cdiv(a.hidden, 32)), dim3(1024), 0, stream, a.part, (int)s.blocks, a.hidden, dweight);
 }
 
 template <typename T>
 gemm_status_t norm_grad(const NormGradArgs& a, bool aligned, float* dweight, gemm_stream_t stream) {
-    const int v = norm_chunks(a.hidden);
-    const dim3 block(norm_block(a.hidden, v).x);
-    const int64_t grid = std::min<int64_t>(a.rows, GRAD_BLOCKS);
-    void (*fn)(NormGradArgs);
-    if (aligned)
-        fn = v == 1 ? norm_grad_kernel<T, true, 1> : v == 2 ? norm_grad_kernel<T, true, 2>
-             : v == 4 ? norm_grad_kernel<T, true, 4> : norm_grad_kernel<T, true, 8>;
-    else
-        fn = v == 1 ? norm_grad_kernel<T, false, 1> : v == 2 ? norm_grad_kernel<T, false, 2>
-             : v == 4 ? norm_grad_kernel<T, false, 4> : norm_grad_kernel<T, false, 8>;
-    const gemm_status_t st = launch(fn, dim3((unsigned)grid), block, 0, stream, a);
-    if (st != GEMM_OK || !dweight) return st;
-    return launch(norm_weight_kernel, dim3((unsigned)cdiv(a.hidden, 32)), dim3(1024), 0, stream, a.part, (int)grid, a.hidden, dweight);
+    return (aligned ? norm_grad_v<T, true> : norm_grad_v<T, false>)(a, dweight, stream);
 }
 
 gemm_status_t check_norm(int64_t rows, int64_t hidden) {
@@ -609,7 +691,7 @@ gemm_status_t gemm_rms_norm_grad_workspace_size(int64_t rows, int64_t hidden, si
     if (!bytes) return GEMM_ERR_INVALID_ARG;
     const gemm_status_t st = check_norm(rows, hidden);
     if (st != GEMM_OK) return st;
-    *bytes = (size_t)std::min<int64_t>(rows, GRAD_BLOCKS) * (size_t)hidden * sizeof(float);
+    *bytes = (size_t)grad_shape(rows, hidden).blocks * (size_t)hidden * sizeof(float);
     return GEMM_OK;
 }
 

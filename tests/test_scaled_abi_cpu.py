@@ -66,7 +66,7 @@ NORM = dict(x=P, ldx=16, residual=P, ldres=16, weight=P, eps=1e-5, rows=4, hidde
     (INV, dict(scales=None)), (INV, dict(residual=None)), (INV, dict(rows=-1)), (INV, dict(hidden=-1)), (INV, dict(eps=-1e-9)),
     (INV, dict(eps=NAN)), (INV, dict(ldx=15)), (INV, dict(ldres=15)), (INV, dict(ldsum=15)), (INV, dict(ldy=15)),
     (INV, dict(ldq=15)), (INV, dict(dtype=2)), (INV, dict(type=2)), (UNS, dict(rows=2 ** 31)),
-    (UNS, dict(hidden=65537, ldx=65537, ldres=65537, ldsum=65537, ldy=65537, ldq=65537)), (UNS, dict(x=P + 1)),
+    (UNS, dict(hidden=32769, ldx=32769, ldres=32769, ldsum=32769, ldy=32769, ldq=32769)), (UNS, dict(x=P + 1)),
     (UNS, dict(residual=P + 1)), (UNS, dict(weight=P + 1)), (UNS, dict(sum=P + 1)), (UNS, dict(y=P + 1)), (UNS, dict(scales=P + 2)),
     (UNS, dict(rstd=P + 2))])
 def test_norm_refusals(status, changes):
@@ -81,7 +81,7 @@ GRAD = dict(dy=P, lddy=16, s=P, lds=16, weight=P, rstd=P, dsum=P, lddsum=16, row
     (INV, dict(dy=None)), (INV, dict(s=None)), (INV, dict(weight=None)), (INV, dict(rstd=None)), (INV, dict(dx=None)),
     (INV, dict(rows=-1)), (INV, dict(hidden=-1)), (INV, dict(lddy=15)), (INV, dict(lds=15)), (INV, dict(lddsum=15)),
     (INV, dict(lddx=15)), (INV, dict(dtype=2)), (UNS, dict(rows=2 ** 31)),
-    (UNS, dict(hidden=65537, lddy=65537, lds=65537, lddsum=65537, lddx=65537)), (UNS, dict(dy=P + 1)), (UNS, dict(s=P + 1)),
+    (UNS, dict(hidden=32769, lddy=32769, lds=32769, lddsum=32769, lddx=32769)), (UNS, dict(dy=P + 1)), (UNS, dict(s=P + 1)),
     (UNS, dict(weight=P + 1)), (UNS, dict(rstd=P + 2)), (UNS, dict(dsum=P + 1)), (UNS, dict(dx=P + 1)), (UNS, dict(dweight=P + 2)),
     (WS, dict(workspace=None)), (WS, dict(workspace=P + 8))])
 def test_norm_grad_refusals(status, changes):
@@ -95,7 +95,7 @@ def test_norm_without_rows_or_elements():
     B.gemm_rms_norm_grad(*_with(GRAD, rows=0, dweight=None, workspace=None))
     for bad in ((-1, 16), (4, -1)):
         refused(INV, B.gemm_rms_norm_grad_workspace_size, *bad)
-    refused(UNS, B.gemm_rms_norm_grad_workspace_size, 4, 65537)
+    refused(UNS, B.gemm_rms_norm_grad_workspace_size, 4, 32769)
     refused(UNS, B.gemm_rms_norm_grad_workspace_size, 2 ** 31, 16)
     assert B.load().gemm_rms_norm_grad_workspace_size(4, 16, None) == INV
     assert B.gemm_rms_norm_grad_workspace_size(0, 16) == 0
