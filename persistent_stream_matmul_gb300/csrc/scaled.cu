@@ -304,7 +304,13 @@ gemm_status_t gemm_scaled_plan_set_option(gemm_scaled_plan_t p, int key, int64_t
     } else {
         return GEMM_ERR_INVALID_ARG;
     }
-    const gemm_status_t st = derive(p);
+    gemm_status_t st = GEMM_ERR_CUDA;
+    if (p->offline) {
+        st = derive(p);
+    } else {
+        DeviceGuard guard(p->device);
+        if (guard.ok) st = derive(p);
+    }
     if (st != GEMM_OK) {
         p->opt_ctas = saved[0];
         p->opt_form = saved[1];

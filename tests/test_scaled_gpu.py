@@ -255,3 +255,43 @@ def test_few_rows(M, N, K, scale_a, scale_b):
     Case(M, N, K, "e5m2", "e4m3", "f32", seed=N, scale_a=scale_a, scale_b=scale_b).check(offset=1)
     c = Case(M, N, K, out="f32", integers=True, seed=M, scale_a=scale_a, scale_b=scale_b)
     assert torch.equal(c.run().double(), c.reference()[0])  # sixteenths below 9 * 16 * 14336 < 2^21: 25 bits at most
+
+
+@pytest.mark.parametrize("K", [1, 3, 127, 129, 1000])
+@pytest.mark.parametrize("M,N", [(16, 16), (48, 400), (400, 272), (4112, 4096)])
+def test_sums_over_any_number_of_tokens(M, N, K):
+    """Both operands MN-major: the summed dimension needs no alignment."""
+    Case(M, N, K, seed=K, **WGRAD).check()
+    c = Case(M, N, K, out="f32", layout_a=COL, layout_b=ROW, scale_b=VEC, integers=True, seed=K)
+    assert torch.equal(c.run().double(), c.reference()[0])
+
+
+@pytest.mark.parametrize("M", [3, 24, 200])
+def test_offsets_past_32_bits(M):
+    """B of 2.3 GB: its last rows against 64 bits, and its first, in each form."""
+    N, K = 140016, 16384
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a = (torch.randn(M, K, generator=g, device="cuda") * 20).to(torch.float8_e4m3fn)
+    some = (torch.randn(1008, K, generator=g, device="cuda") * 20).to(torch.float8_e4m3fn)
+    b = torch.empty(N, K, dtype=torch.uint8, device="cuda")
+    b[:1008] = some.view(torch.uint8)
+    for at in range(1008, N, 1008):
+        b[at:at + 1008] = b[:min(1008, N - at)]
+    sa = torch.exp(torch.randn(K // 128, M, generator=g, device="cuda"))
+    sb = torch.exp(torch.randn(K // 128, N, generator=g, device="cuda"))
+    p = B.ScaledPlan(M, N, K, 0, 0, B.GEMM_F32, ROW, COL, VEC, VEC)
+    assert p.info("form") == {3: B.GEMM_SCALED_FEW, 24: B.GEMM_SCALED_TURNED, 200: B.GEMM_SCALED_STRAIGHT}[M]
+    ws = torch.empty(max(16, p.workspace_size), dtype=torch.uint8, device="cuda")
+    C = torch.empty(M, N, device="cuda")
+    p.run(a, sa, b, sb, C, ws)
+    assert p.last_status() == B.GEMM_OK
+    for rows in (slice(0, 300), slice(N - 300, N)):
+        part = b[rows].contiguous().view(torch.float8_e4m3fn)
+        assert_product(C[:, rows], *product(a, sa, "rows", part, sb[:, rows].contiguous(), "rows", True, False), K)
+
+
+def test_device_of_the_plan_is_kept():
+    before = torch.cuda.current_device()
+    c = Case(300, 272, 272, seed=1)
+    c.check()
+    assert torch.cuda.current_device() == before

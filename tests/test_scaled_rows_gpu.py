@@ -293,3 +293,42 @@ def test_norm_grad_against_automatic_differentiation():
     n = s.double() * rstd.double()[:, None]
     e = ((R + 2) * 2.0 ** -24 + relative(H)) * 1.01 * (dy.double() * n).abs().sum(0)
     assert bool(((dw.double() - W.grad[0]).abs() <= e).all())
+
+
+def test_offsets_past_32_bits():
+    """2.3 G elements: the last rows of every form."""
+    R, H = 70016, 32768
+    x = torch.empty(R, H, dtype=torch.bfloat16, device="cuda")
+    some = activations((1024, H), torch.bfloat16, 1)
+    for at in range(0, R, 1024):
+        x[at:at + 1024] = some[:min(1024, R - at)]
+    x[-7:] = activations((7, H), torch.bfloat16, 2)
+    last = slice(R - 128 - R % 128, R)
+    q, s, qc, sc = (torch.empty(R, H, dtype=torch.uint8, device="cuda"), torch.empty(up(H), R, device="cuda"),
+                    torch.empty(R, H, dtype=torch.uint8, device="cuda"), torch.empty(up(R), H, device="cuda"))
+    B.gemm_scaled_quantize_both(x, H, R, H, B.GEMM_BF16, 0, q, H, s, qc, H, sc)
+    part = x[last].double()
+    want, scales = quantized(part, "e4m3", "rows")
+    assert torch.equal(q[last].view(torch.float8_e4m3fn).double(), want) and torch.equal(s[:, last], scales.float())
+    want, scales = quantized(part, "e4m3", "cols")
+    assert torch.equal(qc[last].view(torch.float8_e4m3fn).double(), want) and torch.equal(sc[-scales.shape[0]:], scales.float())
+    q.zero_()
+    B.gemm_scaled_quantize(B.GEMM_QUANTIZE_ROWS, x, H, R, H, B.GEMM_BF16, 0, q, H, s)
+    want, _ = quantized(part, "e4m3", "rows")
+    assert torch.equal(q[last].view(torch.float8_e4m3fn).double(), want)
+    del qc, sc
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    rstd, y = torch.empty(R, device="cuda"), torch.empty_like(x)
+    B.gemm_rms_norm(x, H, None, 0, w, EPS, R, H, B.GEMM_BF16, None, 0, y, H, q, H, 0, s, rstd)
+    want_rstd = (part.square().mean(1) + EPS).rsqrt()
+    assert bool(((rstd[last].double() - want_rstd).abs() <= relative(H) * want_rstd).all())
+    want = part * want_rstd[:, None]
+    assert bool(((y[last].double() - want).abs() <= (2.0 ** -8 + 2 * relative(H)) * want.abs()).all())
+    B.gemm_rms_norm_grad(y, H, x, H, w, rstd, None, 0, R, H, B.GEMM_BF16, y, H, None, None)  # dy is the normed row itself: no gradient
+    # y = n + d with |d| <= 2^-8 |n|, so dx = rstd (d + n (1 - mean n^2) - n mean(d n)), where mean n^2 is 1 - eps
+    # rstd^2 within twice rstd's error, and the sums round as in run_grad; dx rounds once more
+    r = rstd[last].double()[:, None]
+    n = part * r
+    square = n.square().mean(1, keepdim=True)
+    bound = r * n.abs() * (2.0 ** -8 * (1 + square) + EPS * r ** 2 + 2 * relative(H) + (H + 8) * 2.0 ** -24 * square)
+    assert bool((y[last].double().abs() <= bound * 1.01 + 2.0 ** -100).all())
