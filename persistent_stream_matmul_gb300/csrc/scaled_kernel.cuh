@@ -758,6 +758,14 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                     if (b < batches) {
                         uint32_t (&r)[BATCH] = v[b % READS];
                         if (READS == 1 && b > 0) tmem_ld_async(tbase + b * BATCH, r);
+                        // (the scales' latency passes while the columns are on their way)
+                        float4 f[COL_VECTOR ? BATCH / 4 : 1];
+                        if constexpr (COL_VECTOR)
+#pragma unroll
+                            for (int i = 0; i < BATCH; i += 4) {
+                                const int at = b * BATCH + i;
+                                f[i / 4] = ld_shared_f4(my_cols + (uint32_t)(at + (PAIR && at >= 64 ? 64 : 0)) * 4);
+                            }
                         tmem_wait(r);
                         if (READS == 2 && b + 1 < BATCHES && b + 1 < batches) tmem_ld_async(tbase + (b + 1) * BATCH, v[(b + 1) % READS]);
                         if (!TURNED && b == BATCHES - 1) release();
@@ -765,9 +773,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                         for (int i = 0; i < BATCH; i += 4) {
                             const int at = b * BATCH + i;
                             const float factor = factors[PAIR && at >= 64 ? 1 : 0];
-                            float4 f = make_float4(factor, factor, factor, factor);
-                            if constexpr (COL_VECTOR) f = ld_shared_f4(my_cols + (uint32_t)(at + (PAIR && at >= 64 ? 64 : 0)) * 4);
-                            scaled_add4<COL_VECTOR>(acc + at, r + i, f, factor);
+                            scaled_add4<COL_VECTOR>(acc + at, r + i, COL_VECTOR ? f[i / 4] : make_float4(factor, factor, factor, factor), factor);
                         }
                     }
                 }

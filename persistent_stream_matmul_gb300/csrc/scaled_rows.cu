@@ -32,35 +32,41 @@ __device__ __forceinline__ float scale_of(float m) { return __fdiv_rn(fmaxf(m, L
 template <bool E5M2>
 __device__ __forceinline__ float inverse_of(float m) { return __fdiv_rn(Fp8<E5M2>::LARGEST, fmaxf(m, LEAST)); }
 
-// Eight 8-bit values nearest to x * L / m.  x * fl(L / m) is within 2^-23 of
-// that, which could lift a quotient off a border between two 8-bit values or onto
-// the other side, and between 16-bit x and m quotients on a border are common
-// (0.3 % of normal bf16 values).  But those that are not on a border t (5 bits) are
-// 2^-16 away from it at least: x L / m - t is a whole multiple of 1 / m over t
-// of 5 bits and m of 11.  So EXACT rounds the product to 20 bits first, which
-// puts it back on the border it came from and moves no other across.
+// The eight 8-bit values nearest to x * L / m, from v = x * exact_inverse_of(m).
+//
+// x * fl(L / m) is within 2^-23 of x * L / m, which could lift a quotient off a border
+// between two 8-bit values or onto the other side, and between 16-bit x and m
+// quotients on a border are common (0.3 % of normal bf16 values).  But those that are not on
+// a border t (5 bits) are 2^-16 away from it at least: x L / m - t is a whole multiple
+// of 1 / m over t of 5 bits and m of 11.  So the product, made 2^-21 larger, is cut
+// to 20 bits: that puts what belongs on a border back onto it, and moves nothing
+// across one.  (NaN and infinity stay what they are.)
+template <bool E5M2>
+__device__ __forceinline__ float exact_inverse_of(float m) { return __fmul_rn(inverse_of<E5M2>(m), 1.f + 0x1p-21f); }
+
 template <bool E5M2, bool EXACT>
-__device__ __forceinline__ uint2 quantized(const float (&x)[8], float inverse) {
+__device__ __forceinline__ uint2 quantized(const float (&v)[8]) {
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t pair[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float v[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                v[i] = __fmul_rn(x[4 * h + 2 * j + i], inverse);
-                if constexpr (EXACT) {  // the leading part of a splitting by 2^4 + 1
-                    const float c = __fmul_rn(v[i], 17.f);
-                    v[i] = __fsub_rn(c, __fsub_rn(c, v[i]));
-                }
-            }
-            pair[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, Fp8<E5M2>::KIND);
+            float2 x = make_float2(v[4 * h + 2 * j], v[4 * h + 2 * j + 1]);
+            if constexpr (EXACT) x = make_float2(__uint_as_float(__float_as_uint(x.x) & ~15u), __uint_as_float(__float_as_uint(x.y) & ~15u));
+            pair[j] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, Fp8<E5M2>::KIND);
         }
         w[h] = pair[0] | (pair[1] << 16);
     }
     return make_uint2(w[0], w[1]);
+}
+
+template <bool E5M2, bool EXACT>
+__device__ __forceinline__ uint2 quantized(const float (&x)[8], float inverse) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inverse);
+    return quantized<E5M2, EXACT>(v);
 }
 
 // Elements h .. h + 7 of a row of n to memory; ALIGNED: all of them, at once.
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
         const int g = g0 + u * ACROSS, h = g * GROUP + lane * 8;
         const float m = over_half(magnitude(x[u]));
         if (row >= a.rows || h >= a.cols) continue;
-        store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x[u], inverse_of<E5M2>(m)));
+        store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x[u], exact_inverse_of<E5M2>(m)));
         if (lane == 0) a.scales[(int64_t)g * a.rows + row] = scale_of<E5M2>(m);
     }
 }
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(Quanti
             const int64_t row = row0 + 16 * i;
             const float m = over_half(magnitude(x));
             if (row < a.rows && h < a.cols) {
-                store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x, inverse_of<E5M2>(m)));
+                store_quantized<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x, exact_inverse_of<E5M2>(m)));
                 if (lane == 0) a.scales[(int64_t)tile_col * a.rows + row] = scale_of<E5M2>(m);
             }
         }
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(Quanti
 #pragma unroll
         for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (threadIdx.x == 0) a.scales[tile_row * a.row_groups + tile_col] = scale_of<E5M2>(m);
-        const float inverse = inverse_of<E5M2>(m);
+        const float inverse = exact_inverse_of<E5M2>(m);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t row = row0 + 16 * i;
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(Quanti
             for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i][threadIdx.x]);
             const int at = tile_col * GROUP + threadIdx.x;
             if (at < a.cols) scales[tile_row * a.cols + at] = scale_of<E5M2>(m);
-            part[0][threadIdx.x] = inverse_of<E5M2>(m);
+            part[0][threadIdx.x] = exact_inverse_of<E5M2>(m);
         }
         __syncthreads();
 #pragma unroll
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(Quanti
             unpack<T>(c[i], x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], col[j]);
-            if (row < a.rows && h < a.cols) store_quantized<ALIGNED>(q + row * ldq, h, a.cols, quantized<E5M2, true>(x, 1.f));
+            if (row < a.rows && h < a.cols) store_quantized<ALIGNED>(q + row * ldq, h, a.cols, quantized<E5M2, true>(x));
         }
     }
 }
