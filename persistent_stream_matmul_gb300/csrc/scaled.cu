@@ -133,8 +133,9 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     s.kb = (int32_t)kb;
     s.units = (int32_t)units;
     // the tiles left over a whole round, in shares of `least` k-blocks at least: shorter
-    // ones are not worth joining
-    const int64_t least = ctas == 2 ? 16 : turned ? 8 : 12, rest = tiles < units ? tiles : tiles % units;
+    // ones are not worth joining (us, single CTAs, with 12 and 16: 200 x 2048 x 2048 10.2 /
+    // 8.4, 300 x 4096 x 2048 9.4 / 9.4; turned, 8 and 12: 24 x 4096 x 4096 11.5 / 11.6)
+    const int64_t least = turned ? 8 : 16, rest = tiles < units ? tiles : tiles % units;
     s.shares = 1;
     if (rest > 0 && kb > least) {
         const int64_t most = std::max(cdiv(rest * kb, units - rest), least), shares = cdiv(kb, most);

@@ -66,8 +66,10 @@ struct ScaledCfg {
     static constexpr int L_BYTES = 128 * S_BK;
     static constexpr int R_BYTES = 128 * S_BK;    // this CTA's columns
     static constexpr int STAGE_BYTES = L_BYTES + R_BYTES;
-    static constexpr int STAGES = TURNED ? 6 : 5;
-    static constexpr int GROUPS = COL_VECTOR && PAIR ? 4 : 8;  // k-blocks of a slot of scales
+    // us with 3, 4, 5: pairs, 8192 x 14336 x 4096 365 / 349 / 353, its gradient 455 / 451 /
+    // 473; single CTAs, 96 x 4096 x 14336 22.5 / 21.2 / 20.8
+    static constexpr int STAGES = PAIR ? 4 : TURNED ? 6 : 5;
+    static constexpr int GROUPS = 8;               // k-blocks of a slot of scales
     static constexpr int BOXES = TURNED ? 0 : 3;  // staged boxes of a warp, 32 rows x 64 bytes
     static constexpr int PRODUCTS = CM;           // products a k-block
     static constexpr int BUFFERS = 4 / PRODUCTS;  // of each, 128 columns of tensor memory
