@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpsm_gemm.so")
@@ -122,6 +123,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_packed = None  # psm_packed_call: its arguments as one array, a slot of 64 bits each
 
 
 class GemmError(RuntimeError):
@@ -132,7 +134,7 @@ class GemmError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load the CUDA library; raise if it is missing (there is no fallback)."""
-    global _lib
+    global _lib, _packed
     if _lib is None:
         if not os.path.exists(path):
             raise ImportError(
@@ -143,6 +145,8 @@ def load(path: str = LIB_PATH):
             f = getattr(lib, name)
             f.restype = res
             f.argtypes = args
+        _packed = lib.psm_packed_call
+        _packed.restype, _packed.argtypes = _i32, [_i32, ctypes.c_char_p]
         _lib = lib
     return _lib
 
@@ -481,23 +485,40 @@ class GroupedPlan:
         self.close()
 
 
+# The row operators' and the scaled products' calls are short and have many
+# arguments, which ctypes would convert one by one.
+_PACK_QUANTIZE, _PACK_BOTH = struct.Struct("11q").pack, struct.Struct("13q").pack
+_PACK_NORM, _PACK_NORM_GRAD, _PACK_RUN = struct.Struct("5qd13q").pack, struct.Struct("16q").pack, struct.Struct("8q").pack
+
+
+def _call(op, packed, where):
+    st = (_packed or _loaded())(op, packed)
+    if st != GEMM_OK:
+        raise GemmError(st, where)
+
+
+def _loaded():
+    load()
+    return _packed
+
+
 def gemm_scaled_quantize(kind, x, ldx, rows, cols, dtype, type, q, ldq, scales, stream=None):
-    _check(load().gemm_scaled_quantize(kind, _addr(x), ldx, rows, cols, dtype, type, _addr(q), ldq, _addr(scales),
-                                       _stream(stream)), "gemm_scaled_quantize")
+    _call(0, _PACK_QUANTIZE(kind, _addr(x) or 0, ldx, rows, cols, dtype, type, _addr(q) or 0, ldq, _addr(scales) or 0,
+                            _stream(stream) or 0), "gemm_scaled_quantize")
 
 
 def gemm_scaled_quantize_both(x, ldx, rows, cols, dtype, type, q_rows, ldq_rows, scales_rows, q_cols, ldq_cols,
                               scales_cols, stream=None):
-    _check(load().gemm_scaled_quantize_both(_addr(x), ldx, rows, cols, dtype, type, _addr(q_rows), ldq_rows,
-                                            _addr(scales_rows), _addr(q_cols), ldq_cols, _addr(scales_cols),
-                                            _stream(stream)), "gemm_scaled_quantize_both")
+    _call(1, _PACK_BOTH(_addr(x) or 0, ldx, rows, cols, dtype, type, _addr(q_rows) or 0, ldq_rows, _addr(scales_rows) or 0,
+                        _addr(q_cols) or 0, ldq_cols, _addr(scales_cols) or 0, _stream(stream) or 0),
+          "gemm_scaled_quantize_both")
 
 
 def gemm_rms_norm(x, ldx, residual, ldres, weight, eps, rows, hidden, dtype, sum, ldsum, y, ldy, q, ldq, type, scales,
                   rstd, stream=None):
-    _check(load().gemm_rms_norm(_addr(x), ldx, _addr(residual), ldres, _addr(weight), eps, rows, hidden, dtype,
-                                _addr(sum), ldsum, _addr(y), ldy, _addr(q), ldq, type, _addr(scales), _addr(rstd),
-                                _stream(stream)), "gemm_rms_norm")
+    _call(2, _PACK_NORM(_addr(x) or 0, ldx, _addr(residual) or 0, ldres, _addr(weight) or 0, eps, rows, hidden, dtype,
+                        _addr(sum) or 0, ldsum, _addr(y) or 0, ldy, _addr(q) or 0, ldq, type, _addr(scales) or 0,
+                        _addr(rstd) or 0, _stream(stream) or 0), "gemm_rms_norm")
 
 
 def gemm_rms_norm_grad_workspace_size(rows, hidden) -> int:
@@ -509,9 +530,9 @@ def gemm_rms_norm_grad_workspace_size(rows, hidden) -> int:
 
 def gemm_rms_norm_grad(dy, lddy, s, lds, weight, rstd, dsum, lddsum, rows, hidden, dtype, dx, lddx, dweight,
                        workspace=None, stream=None):
-    _check(load().gemm_rms_norm_grad(_addr(dy), lddy, _addr(s), lds, _addr(weight), _addr(rstd), _addr(dsum), lddsum,
-                                     rows, hidden, dtype, _addr(dx), lddx, _addr(dweight), _addr(workspace),
-                                     _stream(stream)), "gemm_rms_norm_grad")
+    _call(3, _PACK_NORM_GRAD(_addr(dy) or 0, lddy, _addr(s) or 0, lds, _addr(weight) or 0, _addr(rstd) or 0,
+                             _addr(dsum) or 0, lddsum, rows, hidden, dtype, _addr(dx) or 0, lddx, _addr(dweight) or 0,
+                             _addr(workspace) or 0, _stream(stream) or 0), "gemm_rms_norm_grad")
 
 
 def gemm_scaled_plan_create(M, N, K, type_a, type_b, out_dtype, layout_a, layout_b, scale_a, scale_b) -> int:
@@ -548,8 +569,8 @@ def gemm_scaled_workspace_size(plan) -> int:
 
 
 def gemm_scaled_run(plan, A, scales_a, B, scales_b, C, workspace=None, stream=None):
-    _check(load().gemm_scaled_run(plan, _addr(A), _addr(scales_a), _addr(B), _addr(scales_b), _addr(C),
-                                  _addr(workspace), _stream(stream)), "gemm_scaled_run")
+    _call(4, _PACK_RUN(plan or 0, _addr(A) or 0, _addr(scales_a) or 0, _addr(B) or 0, _addr(scales_b) or 0,
+                       _addr(C) or 0, _addr(workspace) or 0, _stream(stream) or 0), "gemm_scaled_run")
 
 
 def gemm_scaled_last_status(plan, stream=None) -> int:

@@ -16,6 +16,7 @@ UNITS = {
     "moe.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "gemm.h", "gemm_moe.h"),
     "grouped.cu": ("grouped_kernel.cuh", "grouped_sched.cuh", "join.cuh", "host.cuh", "ptx.cuh", "gemm.h", "gemm_moe.h"),
     "scaled_rows.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "gemm.h", "gemm_scaled.h"),
+    "packed.cu": ("gemm.h", "gemm_scaled.h"),
     "scaled.cu": ("scaled_few.cuh", "scaled_kernel.cuh", "rows.cuh", "join.cuh", "host.cuh", "ptx.cuh", "gemm.h", "gemm_scaled.h"),
 }
 SOURCES = [os.path.join(CSRC, f) for f in UNITS]
