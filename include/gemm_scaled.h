@@ -145,8 +145,8 @@ typedef struct gemm_scaled_plan *gemm_scaled_plan_t;
 typedef enum {
     GEMM_SCALED_STRAIGHT = 0,  /* A along the tensor memory's lanes, B along its columns */
     GEMM_SCALED_TURNED = 1,    /* B along the lanes: the rows of A cost steps of 16 */
-    GEMM_SCALED_FEW = 2        /* without tensor memory: at most 16 rows of A, A row-major and
-                                * B column-major */
+    GEMM_SCALED_FEW = 2        /* without tensor memory, for few rows of A: A row-major and B
+                                * column-major */
 } gemm_scaled_form_t;
 
 /* Options for gemm_scaled_plan_set_option (key, value). */

@@ -96,13 +96,22 @@ int resident_pairs(int dev) {
 }
 
 gemm_status_t derive(gemm_scaled_plan* p) {
-    const bool few = p->M <= F_MOST_ROWS && p->layout_a == GEMM_ROW_MAJOR && p->layout_b == GEMM_COL_MAJOR;
+    const bool few = p->layout_a == GEMM_ROW_MAJOR && p->layout_b == GEMM_COL_MAJOR && cdiv(p->M, F_MOST_ROWS) <= 65535;
+    // Without tensor memory: up to 16 rows always, more while the product is small. On tensor
+    // memory it takes 5 us with few k-blocks and 8 to 12 with more, however small; without,
+    // each 32 rows of A read B again and each 16 rows of B read those. us, without against
+    // with: 24 x 1536 x 2048 3.6 / 9.3, 24 x 4096 x 4096 8.4 / 11.3, 32 x 4096 x 4096 10.5 /
+    // 11.3, 64 x 2048 x 2048 6.0 / 8.5, 128 x 1024 x 1024 4.0 / 5.9, 128 x 256 x 8192 11.7 /
+    // 12.4; but 256 x 1024 x 1024 6.9 / 6.0, 64 x 4096 x 512 5.7 / 4.9, 48 x 4096 x 2048 10.8 /
+    // 9.1, 24 x 14336 x 4096 23.4 / 16.1.
+    const double out = (double)p->M * (double)p->N, products = out * (double)p->K;
+    const bool small = p->M <= 16 || (out <= 1.4e5 && products <= (p->M <= 32 ? 5.4e8 : 2.9e8));
     int form = p->opt_form, ctas = p->opt_ctas;
     // Turned, a tile's columns fit the rows of A, but each has a scale of its own to be
     // read and multiplied: us, turned against straight, 4096 x 14336 with 32 rows 18.6 /
     // 20.8, 4096 x 4096 with 17 rows 11.5 / 14.9, with 48 13.4 / 12.8, 14336 x 4096 with 64
     // 22.4 / 16.1.
-    if (form < 0) form = ctas == 2 ? GEMM_SCALED_STRAIGHT : few ? GEMM_SCALED_FEW : p->M <= 32 ? GEMM_SCALED_TURNED : GEMM_SCALED_STRAIGHT;
+    if (form < 0) form = ctas == 2 ? GEMM_SCALED_STRAIGHT : few && small ? GEMM_SCALED_FEW : p->M <= 32 ? GEMM_SCALED_TURNED : GEMM_SCALED_STRAIGHT;
     // Pairs read their operands half as often, single CTAs make four times the tiles: us,
     // single against pairs, 512 x 4096 x 4096 (32 pair tiles) 14.0 / 19.7, 256 x 14336 x
     // 4096 (56) 25.8 / 20.7, 1024 x 4096 x 4096 (64) 23.9 / 19.1.
@@ -227,11 +236,16 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base
                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool W, bool X>
+auto few_of(int rows) -> void (*)(FewParams) {
+    return rows <= 8 ? few_kernel<W, X, 1> : rows <= 16 ? few_kernel<W, X, 2> : rows <= 24 ? few_kernel<W, X, 3> : few_kernel<W, X, 4>;
+}
+
 gemm_status_t run_few(const gemm_scaled_plan* p, const FewParams& kp, gemm_stream_t stream) {
     const bool w = p->type_b == GEMM_E5M2, x = p->type_a == GEMM_E5M2;
-    auto* fn = kp.M <= 8 ? (w ? (x ? few_kernel<true, true, 1> : few_kernel<true, false, 1>) : (x ? few_kernel<false, true, 1> : few_kernel<false, false, 1>))
-                         : (w ? (x ? few_kernel<true, true, 2> : few_kernel<true, false, 2>) : (x ? few_kernel<false, true, 2> : few_kernel<false, false, 2>));
-    return launch(fn, dim3((unsigned)cdiv(kp.N, 16)), dim3(32 * F_WARPS), 0, stream, kp);
+    const dim3 grid((unsigned)cdiv(kp.N, 16), (unsigned)cdiv(kp.M, F_MOST_ROWS));
+    auto* fn = w ? (x ? few_of<true, true>(kp.M) : few_of<true, false>(kp.M)) : (x ? few_of<false, true>(kp.M) : few_of<false, false>(kp.M));
+    return launch(fn, grid, dim3(32 * F_WARPS), 0, stream, kp);
 }
 
 // One operand, as the lanes or the columns side sees it: `rows` of K elements.

@@ -1,5 +1,5 @@
-// Scaled products of a few rows of A (one generated token, a small batch), both
-// operands with the summed dimension contiguous.
+// Scaled products of a few rows of A (one generated token, a small batch) and other
+// small ones, both operands with the summed dimension contiguous.
 //
 // Bound by the reading of B: 2 M operations a byte of it.  What a small product
 // pays beside that is latency, so this kernel has no ring, no tensor memory and
@@ -18,12 +18,13 @@
 namespace psm {
 
 constexpr int F_WARPS = 8;
-// k-blocks of a warp in flight, and blocks an SM.  Bytes in flight against registers: us
-// for one row, 14336 x 4096 / 4096 x 14336 / 4096 x 4096, with 2 and 2 blocks 15.0 / 14.6
-// / 5.9; 2 and 3 15.3 / 20.8 / 7.7; 1 and 3 13.1 / 17.2 / 6.3; 3 and 2 15.5 / 14.0 / 6.2
-// (16 rows 18.5, 32.4, 24.9 and 30.1); with 32 rows of B a warp 17.2 / 19.7 / 8.2.
+// k-blocks of a warp in flight (one for more than 16 rows), and blocks an SM.  Bytes in
+// flight against registers: us for one row, 14336 x 4096 / 4096 x 14336 / 4096 x 4096, with 2
+// and 2 blocks 15.0 / 14.6 / 5.9; 2 and 3 15.3 / 20.8 / 7.7; 1 and 3 13.1 / 17.2 / 6.3; 3 and 2
+// 15.5 / 14.0 / 6.2 (16 rows 18.5, 32.4, 24.9 and 30.1); with 32 rows of B a warp 17.2 / 19.7 /
+// 8.2.  24 rows of 4096 x 4096, 1 and 2 8.4, 2 and 1 10.7.
 constexpr int F_BLOCKS = 2, F_RESIDENT = 2;
-constexpr int F_MOST_ROWS = 16;  // of A
+constexpr int F_MOST_ROWS = 32;  // of A, a block
 
 // k-blocks of a warp that are brought into L2 ahead.  us in a chain of products of one row,
 // with 0, 2, 8: 14336 x 4096 15.0 / 14.3 / 14.5, 4096 x 14336 14.7 / 14.2 / 15.1, 4096 x 4096
@@ -66,11 +67,12 @@ __device__ __forceinline__ void few_load(const uint8_t* p, int64_t bytes, uint32
 // NT: tiles of 8 rows of A.
 template <bool W_E5M2, bool X_E5M2, int NT>
 __global__ void __launch_bounds__(32 * F_WARPS, F_RESIDENT) few_kernel(const __grid_constant__ FewParams p) {
-    constexpr int U = F_BLOCKS;
+    constexpr int U = NT <= 2 ? F_BLOCKS : 1;
     __shared__ float part[F_WARPS][16][NT * 8 + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int m0 = blockIdx.y * (NT * 8), rows = min(p.M - m0, NT * 8);  // of A
     // rows past the end read the last one's
     const uint8_t* b[2];
     const float* sb[2];
@@ -84,9 +86,9 @@ __global__ void __launch_bounds__(32 * F_WARPS, F_RESIDENT) few_kernel(const __g
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        a[j] = p.a + (int64_t)min(j * 8 + g, p.M - 1) * p.K + t * 32;
+        a[j] = p.a + (int64_t)(m0 + min(j * 8 + g, rows - 1)) * p.K + t * 32;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) sa[j][h] = p.sa.s + (int64_t)(min(j * 8 + t * 2 + h, p.M - 1) >> p.sa.shift) * p.sa.row;
+        for (int h = 0; h < 2; ++h) sa[j][h] = p.sa.s + (int64_t)((m0 + min(j * 8 + t * 2 + h, rows - 1)) >> p.sa.shift) * p.sa.row;
     }
     const int k0 = (int)((int64_t)p.kb * warp / F_WARPS), k1 = (int)((int64_t)p.kb * (warp + 1) / F_WARPS);
     float acc[NT][4] = {};
@@ -140,13 +142,13 @@ __global__ void __launch_bounds__(32 * F_WARPS, F_RESIDENT) few_kernel(const __g
 #pragma unroll
         for (int c = 0; c < 4; ++c) part[warp][(c >> 1) * 8 + g][j * 8 + t * 2 + (c & 1)] = acc[j][c];
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * p.M; e += 32 * F_WARPS) {
+    for (int e = threadIdx.x; e < 16 * rows; e += 32 * F_WARPS) {
         const int r = e % (16), m = e / (16);
         if (n0 + r >= p.N) continue;
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < F_WARPS; ++w) sum += part[w][r][m];
-        scaled_store(p.out, p.out_dtype, (int64_t)m * p.N + n0 + r, sum);
+        scaled_store(p.out, p.out_dtype, (int64_t)(m0 + m) * p.N + n0 + r, sum);
     }
 }
 

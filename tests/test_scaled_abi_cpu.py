@@ -112,8 +112,8 @@ def test_plan_refusals(status, changes):
     refused(status, B.gemm_scaled_plan_create, *_with(PLAN, **changes))
 
 
-@pytest.mark.parametrize("M,N,K,ctas,form", [(1, 4096, 4096, 1, 2), (16, 4096, 4096, 1, 2), (17, 4096, 4096, 1, 1), (32, 128, 128, 1, 1), (33, 4096, 1024, 1, 0),
-                                             (129, 4096, 512, 1, 0), (8192, 8192, 512, 2, 0)])
+@pytest.mark.parametrize("M,N,K,ctas,form", [(1, 4096, 4096, 1, 2), (16, 65536, 4096, 1, 2), (17, 14336, 4096, 1, 1), (32, 128, 128, 1, 2), (33, 4096, 8192, 1, 0), (300, 256, 512, 1, 2),
+                                             (129, 4096, 2048, 1, 0), (8192, 8192, 512, 2, 0)])
 def test_offline_plans(M, N, K, ctas, form):
     p = B.ScaledPlan(M, N, K, 0, 0, 1, 0, 1, 0, 1, offline_sms=152)
     assert (p.info("ctas"), p.info("form")) == (ctas, form)
@@ -131,8 +131,6 @@ def test_offline_plans(M, N, K, ctas, form):
     p.set_option(1, 1)
     refused(UNS, p.set_option, 1, 2)  # a turned product has one CTA a unit
     assert p.info("ctas") == 1 and p.info("form") == B.GEMM_SCALED_TURNED
-    if M > 16:
-        refused(UNS, p.set_option, 2, B.GEMM_SCALED_FEW)
     refused(INV, p.info, 99)
     p.close()
 

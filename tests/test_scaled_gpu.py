@@ -81,6 +81,13 @@ def test_product(M, N, K, form):
     Case(*sized(M, N, K, form), seed=M + N + K, **form).check()
 
 
+@pytest.mark.parametrize("options", [dict(form=B.GEMM_SCALED_TURNED), dict(form=B.GEMM_SCALED_STRAIGHT, ctas=1), dict(ctas=2),
+                                     dict(form=B.GEMM_SCALED_FEW)], ids=["turned", "straight", "pairs", "few"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_product_in_every_form(M, N, K, options):
+    Case(M, N, K, seed=M + N + K, **options).check()
+
+
 @pytest.mark.parametrize("scale_a", [VEC, BLOCK])
 @pytest.mark.parametrize("scale_b", [VEC, BLOCK])
 @pytest.mark.parametrize("layout_a", [ROW, COL])
@@ -108,23 +115,26 @@ def test_types(a, b, out, M):
 @pytest.mark.parametrize("M,N", [(7, 33), (5, 1), (200, 333), (300, 1001), (257, 130)])
 @pytest.mark.parametrize("out", DTYPES)
 def test_rows_of_any_length_and_alignment(M, N, out):
-    for offset in (0, 1, 4):
-        Case(M, N, 272, out=out, seed=N).check(offset=offset)
+    for options in (dict(form=B.GEMM_SCALED_FEW), dict(form=B.GEMM_SCALED_TURNED), dict(form=B.GEMM_SCALED_STRAIGHT, ctas=1), dict(ctas=2)):
+        for offset in (0, 1, 4):
+            Case(M, N, 272, out=out, seed=N, **options).check(offset=offset)
 
 
 @pytest.mark.parametrize("K", [0, 16, 112, 128, 144, 256, 272])
 @pytest.mark.parametrize("M", [1, 200])
-def test_short_sums(M, K):
-    c = Case(M, 256, K, seed=K)
+@pytest.mark.parametrize("options", [{}, dict(form=B.GEMM_SCALED_TURNED), dict(form=B.GEMM_SCALED_STRAIGHT), dict(ctas=2)])
+def test_short_sums(M, K, options):
+    c = Case(M, 256, K, seed=K, **options)
     if K == 0:
         assert not c.run().any() and not torch.signbit(c.run()).any()
     else:
         c.check()
 
 
-def test_nan_and_infinity_stay_in_their_row_and_column():
+@pytest.mark.parametrize("options", [{}, dict(form=B.GEMM_SCALED_TURNED), dict(form=B.GEMM_SCALED_STRAIGHT), dict(ctas=2)])
+def test_nan_and_infinity_stay_in_their_row_and_column(options):
     for M in (20, 400):
-        c = Case(M, 400, 400, seed=M)
+        c = Case(M, 400, 400, seed=M, **options)
         a = c.a.float()
         a[3, 7] = float("nan")
         c.a.copy_(a.to(c.a.dtype))
@@ -245,15 +255,16 @@ def test_timeout_is_reported_and_replays_recover(ctas, form):
                 assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 15, 16])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 15, 16, 17, 24, 25, 32, 33, 70, 129])
 @pytest.mark.parametrize("N,K", [(1, 16), (17, 128), (33, 144), (4096, 2064), (9999, 1040), (500, 14336)])
 @pytest.mark.parametrize("scale_a,scale_b", [(VEC, BLOCK), (VEC, VEC), (BLOCK, VEC)])
 def test_few_rows(M, N, K, scale_a, scale_b):
-    c = Case(M, N, K, seed=M + N, scale_a=scale_a, scale_b=scale_b)
+    few = dict(scale_a=scale_a, scale_b=scale_b, form=B.GEMM_SCALED_FEW)
+    c = Case(M, N, K, seed=M + N, **few)
     assert c.plan.info("form") == B.GEMM_SCALED_FEW and c.plan.workspace_size == 0
     c.check()
-    Case(M, N, K, "e5m2", "e4m3", "f32", seed=N, scale_a=scale_a, scale_b=scale_b).check(offset=1)
-    c = Case(M, N, K, out="f32", integers=True, seed=M, scale_a=scale_a, scale_b=scale_b)
+    Case(M, N, K, "e5m2", "e4m3", "f32", seed=N, **few).check(offset=1)
+    c = Case(M, N, K, out="f32", integers=True, seed=M, **few)
     assert torch.equal(c.run().double(), c.reference()[0])  # sixteenths below 9 * 16 * 14336 < 2^21: 25 bits at most
 
 
