@@ -58,10 +58,14 @@ bool prepared(int ctas, int turned, int col_vector, int dev) {
     std::lock_guard<std::mutex> lock(mu);
     bool& r = ready[dev][ctas - 1][turned][col_vector];
     if (!r) {
-        if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
+        cudaFuncAttributes attr{};
+        if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
+            cudaFuncGetAttributes(&attr, k.fn) != cudaSuccess) {
             cudaGetLastError();
             return false;
         }
+        // the epilogue of a pair waits for registers that the launch must have had
+        if (ctas == 2 && attr.numRegs < S_REGS) return false;
         r = true;
     }
     return true;
