@@ -97,8 +97,14 @@ gemm_status_t gemm_scaled_quantize_both(const void *x, int64_t ldx, int64_t rows
  * x, residual, sum, y: rows x hidden of `dtype`; weight: hidden of `dtype`.
  * Outputs, each written unless it is NULL (one of y and q at least is needed):
  * sum = s (may be x or residual, with its leading dimension); y rounded to
- * `dtype`; q and scales, y in 8 bits as GEMM_QUANTIZE_ROWS makes it from fp32; rstd,
+ * `dtype`; q and scales, y in 8 bits in vectors along the rows; rstd,
  * rows of fp32, for the gradient.  q and scales come together.
+ * The 8-bit form is GEMM_QUANTIZE_ROWS's of the unrounded y: rstd cancels from y * L / m, so q
+ * is the 8-bit value nearest to z * L / (the largest |z| of the group) with z = s *
+ * weight, ties to even, and the scale is that largest times rstd, rounded, over L, rounded.
+ * A group whose m is raised to 2^-100 has the value nearest to z * rstd * L / 2^-100, to
+ * within fp32's roundings.  z is formed in fp32: it is exact from 2^-120 on, and a group in which
+ * it overflows has an infinite scale.
  * Errors: INVALID_ARG (NULL x or weight, both y and q NULL, one of q and scales
  * without the other, sum without residual, negative size, negative or NaN eps, a
  * leading dimension of a given operand below hidden, bad enum), UNSUPPORTED

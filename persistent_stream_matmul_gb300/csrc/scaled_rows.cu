@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_scaled.h"
 #include "ptx.cuh"
@@ -61,12 +62,73 @@ __device__ __forceinline__ uint2 quantized(const float (&v)[8]) {
     return make_uint2(w[0], w[1]);
 }
 
-template <bool E5M2, bool EXACT>
+template <bool E5M2>
 __device__ __forceinline__ uint2 quantized(const float (&x)[8], float inverse) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inverse);
-    return quantized<E5M2, EXACT>(v);
+    return quantized<E5M2, true>(v);
+}
+
+// L / d within 2^-40 as the sum of two fp32 values, the second by one step of Newton's
+// method, for d of at least 2^-120 (infinite or NaN: NaN).
+struct Inverse {
+    float high, low;
+};
+template <bool E5M2>
+__device__ __forceinline__ Inverse inverse_in_two(float d) {
+    constexpr float L = Fp8<E5M2>::LARGEST;
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float high = __fmul_rn(L, r);
+    return {high, __fmul_rn(__fmaf_rn(-high, d, L), r)};
+}
+
+// scale_of by two products.  1 / L in two parts is within 2^-46, and m / L, a whole number of
+// sevenths of a power of two, is 1 / 14 of fp32's last digit away from the middle between two
+// fp32 values at least, so their sum is rounded as the quotient.  (Both parts are positive, so
+// that an infinity stays one.)
+template <bool E5M2>
+__device__ __forceinline__ float scale_by_products(float m) {
+    constexpr float L = Fp8<E5M2>::LARGEST, HIGH = 0x1.249248p-3f * (7.f / L), LOW = (float)(1. / L - (double)HIGH);
+    static_assert(LOW > 0.f, "1 / 7 cut, not rounded");
+    return __fmaf_rn(m, HIGH, __fmul_rn(m, LOW));
+}
+
+// The eight 8-bit values nearest to the quotients z * L / m, where m is the largest |z| of the
+// group, for z = s * weight of two 16-bit values, exact in fp32.
+//
+// The product with L / m in two parts is the quotient with one rounding of 2^-24.  So one on a
+// border between two 8-bit values stays on it, and one that is not does not get onto
+// its other side.  bf16: nor onto it, as it is 2^-21 away at least (z L is a whole multiple of
+// its last digit over z of 16 bits, t m of its over t of 5 bits and m of 16).  fp16 (z and m of 22
+// bits): where it does, the sign of |z| L - t m, in two parts each, says from which side (not
+// for m = NaN, of a group whose scale is not made from its largest).
+template <typename T, bool E5M2>
+__device__ __forceinline__ uint2 nearest(const float (&z)[8], Inverse in, float m) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(z[i], in.high, __fmul_rn(z[i], in.low));
+    if constexpr (!std::is_same_v<T, __nv_bfloat16>) {
+        constexpr uint32_t BELOW = E5M2 ? 0x1fffffu : 0xfffffu, HALF = BELOW / 2 + 1;  // fp32's digits after those of the type
+        constexpr float L = Fp8<E5M2>::LARGEST, NORMAL = E5M2 ? 0x1p-14f : 0x1p-6f;    // the least value with a leading one
+        bool close = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) close |= (__float_as_uint(v[i]) & BELOW) == HALF || fabsf(v[i]) < NORMAL;
+        if (close)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // below NORMAL the steps are those of the 2^n above it
+                const float a = fabsf(v[i]), shift = a < NORMAL ? NORMAL : 0.f;
+                const float t = __uint_as_float((__float_as_uint(a + shift) & ~BELOW) | HALF) - shift;
+                if (a == t) {
+                    const float y = fabsf(z[i]), p = __fmul_rn(y, L), q = __fmul_rn(t, m);
+                    const float d = (p - q) + (__fmaf_rn(y, L, -p) - __fmaf_rn(t, m, -q));
+                    v[i] = copysignf(__uint_as_float(__float_as_uint(t) + (d > 0.f) - (d < 0.f)), v[i]);
+                }
+            }
+    }
+    return quantized<E5M2, false>(v);
 }
 
 // Elements h .. h + 7 of a row of n to memory; ALIGNED: all of them, at once.
@@ -182,7 +244,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
     for (int u = 0; u < U; ++u) {
         const int g = g0 + u * ACROSS, h = g * GROUP + lane * 8;
         const float m = over_half(magnitude(x[u]));
-        store_group<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x[u], exact_inverse_of<E5M2>(m)), row < a.rows);
+        store_group<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2>(x[u], exact_inverse_of<E5M2>(m)), row < a.rows);
         if (row < a.rows && h < a.cols && lane == 0) a.scales[(int64_t)g * a.rows + row] = scale_of<E5M2>(m);
     }
 }
@@ -224,7 +286,7 @@ __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(Quanti
         if constexpr (BOTH) {
             const int64_t row = row0 + 16 * i;
             const float m = over_half(magnitude(x));
-            store_group<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x, exact_inverse_of<E5M2>(m)), row < a.rows);
+            store_group<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2>(x, exact_inverse_of<E5M2>(m)), row < a.rows);
             if (row < a.rows && lane == 0) a.scales[(int64_t)tile_col * a.rows + row] = scale_of<E5M2>(m);
         }
     }
@@ -246,7 +308,7 @@ __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(Quanti
             const int64_t row = row0 + 16 * i;
             float x[8];
             unpack<T>(c[i], x);
-            store_group<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2, true>(x, inverse), row < a.rows);
+            store_group<ALIGNED>(a.q + row * a.ldq, h, a.cols, quantized<E5M2>(x, inverse), row < a.rows);
         }
     } else {
         uint8_t* q = BOTH ? a.q_cols : a.q;
@@ -373,9 +435,13 @@ __device__ __forceinline__ Chunk load_masked(const uint16_t* row, int h, int n) 
 // sum and the output, and so does the weight over all the rows that a block takes
 // (every gridDim.x x blockDim.y th); AHEAD: the next row is on its way while this
 // one is summed and written, which keeps reads in flight over the barrier.  8192 rows of
-// 4096 with residual and 8-bit output: 44.4 us, 5.3 TB/s (59 with a row a block and no
-// row ahead).
-template <typename T, bool E5M2, bool ALIGNED, int V, bool AHEAD, int THREADS, int RESIDENT>
+// 4096 with residual and 8-bit output: 45.3 us, 5.2 TB/s (59 with a row a block and no
+// row ahead).  Q: with 8-bit output; without it, kernels of their own have registers to spare
+// (us, in one kernel and so: 16-bit output of 8192 x 4096 30.4 / 28.1).
+//
+// 8-bit values from y by one product with the rounded inverse, some of them on the other side of
+// a border: 44.4 us; from s * weight in two parts, but the scales and inverses by divisions: 47.7.
+template <typename T, bool Q, bool E5M2, bool ALIGNED, int V, bool AHEAD, int THREADS, int RESIDENT>
 __global__ void __launch_bounds__(THREADS, RESIDENT) norm_kernel(NormArgs a) {
     __shared__ float part[2][32];
     const int n = a.hidden;
@@ -430,6 +496,8 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) norm_kernel(NormArgs a) {
         square = over_row(square, part[turn]);
         const float rstd = __frsqrt_rn(__fdiv_rn(square, (float)n) + a.eps);
         if (in && threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+        // the least s * weight that a scale is made from: that of LEAST, while fp32 holds it exactly
+        [[maybe_unused]] const float least = fminf(fmaxf(__fdiv_rn(LEAST, rstd), 0x1p-120f), 0x1p100f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int h = (v * blockDim.x + threadIdx.x) * 8;
@@ -437,17 +505,35 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) norm_kernel(NormArgs a) {
             float f[8], g[8];
             unpack<T>(s[v], f);
             unpack<T>(AHEAD ? w[v] : load_masked<ALIGNED, false>(a.weight, h, n), g);
+            if constexpr (!Q) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
-            if (here) {
-                if (a.sum) store_16bit<ALIGNED>(a.sum + row * a.ldsum, h, n, s[v]);
-                if (a.y) store_16bit<ALIGNED>(a.y + row * a.ldy, h, n, pack<T>(f));
-            }
-            if (a.q) {
-                const float m = over_half(magnitude(f));
+                for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
                 if (here) {
-                    store_quantized<ALIGNED>(a.q + row * a.ldq, h, n, quantized<E5M2, false>(f, inverse_of<E5M2>(m)));
-                    if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(h / GROUP) * a.rows + row] = scale_of<E5M2>(m);
+                    if (a.sum) store_16bit<ALIGNED>(a.sum + row * a.ldsum, h, n, s[v]);
+                    if (a.y) store_16bit<ALIGNED>(a.y + row * a.ldy, h, n, pack<T>(f));
+                }
+            } else {
+                if (here) {
+                    if (a.sum) store_16bit<ALIGNED>(a.sum + row * a.ldsum, h, n, s[v]);
+                    if (a.y) {
+                        float y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = f[i] * rstd * g[i];
+                        store_16bit<ALIGNED>(a.y + row * a.ldy, h, n, pack<T>(y));
+                    }
+                }
+                // The row's factor cancels from y / m, so the values are made from z = s * weight, which
+                // fp32 holds exactly.  (Made from y, its two roundings would decide for quotients
+                // on a border, which are common between products of 16-bit values.)
+                float z[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = f[i] * g[i];
+                const float largest = over_half(magnitude(z)), top = fmaxf(largest, least), m = top * rstd;
+                Inverse inverse = inverse_in_two<E5M2>(top);
+                inverse.low += m * 0.f;  // NaN where m is infinite or NaN
+                if (here) {
+                    store_quantized<ALIGNED>(a.q + row * a.ldq, h, n, nearest<T, E5M2>(z, inverse, largest >= least ? top : NAN));
+                    if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(h / GROUP) * a.rows + row] = scale_by_products<E5M2>(fmaxf(m, LEAST));
                 }
             }
         }
@@ -572,13 +658,15 @@ constexpr int SMS = 152;
 // Blocks of 256 an SM: more bytes in flight against registers that spill.  us with 2, 3, 4:
 // norm of 8192 rows of 4096 45.0 / 44.4 / 48.1, 16384 of 1024 31.6 / 24.6 / 25.6; gradient
 // with 1, 2, 3: 16384 rows of 4096 116 / 91 / 116, of 1024 48 / 33 / 32.
+// Norms of short rows without 8-bit output have the registers for four: 16384 of 1024 19.7 / 18.4
+// with 3, 4; 5003 of 1001 22.5 / 17.8.
 constexpr int NORM_RESIDENT = 3, GRAD_RESIDENT = 2;
 // Blocks of `threads` that are resident at once where `resident` of `most` are.
 int64_t resident_blocks(int64_t threads, int most, int resident) {
     return SMS * std::max<int64_t>(1, most * resident / threads);
 }
 
-template <typename T, bool E5M2, bool ALIGNED>
+template <typename T, bool Q, bool E5M2, bool ALIGNED>
 gemm_status_t norm_v(const NormArgs& a, gemm_stream_t stream) {
     const int64_t chunks = cdiv(a.hidden, 8);
     auto run = [&](void (*fn)(NormArgs), int v, int most, int resident) {
@@ -586,16 +674,21 @@ gemm_status_t norm_v(const NormArgs& a, gemm_stream_t stream) {
         const int64_t grid = std::min(cdiv(a.rows, block.y), resident_blocks(block.x * block.y, most, resident));
         return launch(fn, dim3((unsigned)grid), block, 0, stream, a);
     };
-    if (chunks <= 256) return run(norm_kernel<T, E5M2, ALIGNED, 1, true, 256, NORM_RESIDENT>, 1, 256, NORM_RESIDENT);
-    if (chunks <= 512) return run(norm_kernel<T, E5M2, ALIGNED, 2, true, 256, NORM_RESIDENT>, 2, 256, NORM_RESIDENT);
-    if (chunks <= 1024) return run(norm_kernel<T, E5M2, ALIGNED, 2, true, 512, 2>, 2, 512, 2);
-    if (chunks <= 2048) return run(norm_kernel<T, E5M2, ALIGNED, 2, true, 1024, 1>, 2, 1024, 1);
-    return run(norm_kernel<T, E5M2, ALIGNED, 4, false, 1024, 1>, 4, 1024, 1);
+    if (chunks <= 256) return run(norm_kernel<T, Q, E5M2, ALIGNED, 1, true, 256, Q ? NORM_RESIDENT : 4>, 1, 256, Q ? NORM_RESIDENT : 4);
+    if (chunks <= 512) return run(norm_kernel<T, Q, E5M2, ALIGNED, 2, true, 256, NORM_RESIDENT>, 2, 256, NORM_RESIDENT);
+    if (chunks <= 1024) return run(norm_kernel<T, Q, E5M2, ALIGNED, 2, true, 512, 2>, 2, 512, 2);
+    if (chunks <= 2048) return run(norm_kernel<T, Q, E5M2, ALIGNED, 2, true, 1024, 1>, 2, 1024, 1);
+    return run(norm_kernel<T, Q, E5M2, ALIGNED, 4, false, 1024, 1>, 4, 1024, 1);
 }
 
-template <typename T, bool E5M2>
+template <typename T, bool Q, bool E5M2>
 gemm_status_t norm(const NormArgs& a, bool aligned, gemm_stream_t stream) {
-    return (aligned ? norm_v<T, E5M2, true> : norm_v<T, E5M2, false>)(a, stream);
+    return (aligned ? norm_v<T, Q, E5M2, true> : norm_v<T, Q, E5M2, false>)(a, stream);
+}
+
+template <typename T>
+gemm_status_t norm_any(const NormArgs& a, bool aligned, int type, gemm_stream_t stream) {
+    return (!a.q ? norm<T, false, false> : type == GEMM_E5M2 ? norm<T, true, true> : norm<T, true, false>)(a, aligned, stream);
 }
 
 // How the gradient of rows of `hidden` is launched.
@@ -722,9 +815,7 @@ gemm_status_t gemm_rms_norm(const void* x, int64_t ldx, const void* residual, in
     a.scales = scales;
     a.rstd = rstd;
     const bool al = whole_chunks(hidden, {x, residual, weight, sum, y}, {ldx, a.ldres, a.ldsum, a.ldy}, {q}, {a.ldq});
-    auto* fn = dtype == GEMM_BF16 ? (type == GEMM_E5M2 ? norm<__nv_bfloat16, true> : norm<__nv_bfloat16, false>)
-                                  : (type == GEMM_E5M2 ? norm<__half, true> : norm<__half, false>);
-    return fn(a, al, stream);
+    return (dtype == GEMM_BF16 ? norm_any<__nv_bfloat16> : norm_any<__half>)(a, al, type, stream);
 }
 
 gemm_status_t gemm_rms_norm_grad_workspace_size(int64_t rows, int64_t hidden, size_t* bytes) {
