@@ -80,7 +80,11 @@ struct ScaledCfg {
     // 473; single CTAs, 96 x 4096 x 14336 22.5 / 21.2 / 20.8
     static constexpr int STAGES = PAIR ? 4 : TURNED ? 6 : 5;
     static constexpr int GROUPS = 8;               // k-blocks of a slot of scales
-    static constexpr int BOXES = TURNED ? 0 : 3;  // staged boxes of a warp, 32 rows x 64 bytes
+    // staged boxes of a warp, 32 rows x 64 bytes: a ring, of which all but one may still be read
+    // when the next is written.  A tile has a whole number of rounds, so it starts with the
+    // first.  (us with 2, and with 3 and the ring's place carried on: 8192 x 14336 x 4096 362 / 370,
+    // 8192 x 8192 x 128 34.8 / 37.2.)
+    static constexpr int BOXES = TURNED ? 0 : 2;
     static constexpr int PRODUCTS = CM;           // products a k-block
     static constexpr int BUFFERS = 4 / PRODUCTS;  // of each, 128 columns of tensor memory
     static constexpr int SCALE_BYTES = S_COL_SCALES + (COL_VECTOR ? TILE_N * 4 : 16);  // of a k-block
@@ -91,6 +95,7 @@ struct ScaledCfg {
     static constexpr int SLOT_FLOATS = 128 * TILE_N;
     static constexpr int BARS = 2 * STAGES + 8 + 1 + 2 * S_QUEUE + 2 * S_SLOTS;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(TURNED || (PART / 32 % BOXES == 0 && PART / 16 % BOXES == 0), "boxes of a tile, 16 and 32 bits");
     static_assert(BARS * 8 + 32 <= BAR_BYTES, "barrier area");
 };
 
