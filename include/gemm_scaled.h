@@ -118,7 +118,7 @@ gemm_status_t gemm_rms_norm(const void *x, int64_t ldx, const void *residual, in
                             void *q, int64_t ldq, gemm_fp8_t type, float *scales, float *rstd,
                             gemm_stream_t stream);
 
-/* Bytes of device workspace gemm_rms_norm_grad needs.  Its contents need no
+/* Bytes of device workspace gemm_rms_norm_grad needs (0 for rows or hidden 0).  Its contents need no
  * initialisation.  Errors: as gemm_rms_norm for the sizes, INVALID_ARG for a
  * NULL bytes. */
 gemm_status_t gemm_rms_norm_grad_workspace_size(int64_t rows, int64_t hidden, size_t *bytes);

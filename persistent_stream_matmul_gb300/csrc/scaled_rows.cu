@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, in
 // Threads of a row with v chunks each, and rows of a block.
 dim3 norm_block(int64_t hidden, int v) {
     const int64_t chunks = cdiv(hidden, 8);
-    const unsigned width = (unsigned)(cdiv(cdiv(chunks, v), 32) * 32);
+    const unsigned width = (unsigned)(std::max<int64_t>(cdiv(cdiv(chunks, v), 32), 1) * 32);
     return dim3(width, width < 256 ? 256 / width : 1, 1);
 }
 
@@ -822,7 +822,7 @@ gemm_status_t gemm_rms_norm_grad_workspace_size(int64_t rows, int64_t hidden, si
     if (!bytes) return GEMM_ERR_INVALID_ARG;
     const gemm_status_t st = check_norm(rows, hidden);
     if (st != GEMM_OK) return st;
-    *bytes = (size_t)grad_shape(rows, hidden).blocks * (size_t)hidden * sizeof(float);
+    *bytes = rows == 0 || hidden == 0 ? 0 : (size_t)grad_shape(rows, hidden).blocks * (size_t)hidden * sizeof(float);
     return GEMM_OK;
 }
 
