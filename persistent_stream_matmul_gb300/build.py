@@ -13,11 +13,11 @@ LIB = os.path.join(HERE, "libpsm_gemm.so")
 # each translation unit and the headers it includes
 UNITS = {
     "gemm.cu": ("gemm_kernel.cuh", "ptx.cuh", "sched.cuh", "gemm.h"),
-    "moe.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "gemm.h", "gemm_moe.h"),
-    "grouped.cu": ("grouped_kernel.cuh", "grouped_sched.cuh", "join.cuh", "host.cuh", "ptx.cuh", "gemm.h", "gemm_moe.h"),
-    "scaled_rows.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "gemm.h", "gemm_scaled.h"),
+    "moe.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "upload.cuh", "gemm.h", "gemm_moe.h"),
+    "grouped.cu": ("grouped_kernel.cuh", "grouped_sched.cuh", "join.cuh", "host.cuh", "upload.cuh", "ptx.cuh", "gemm.h", "gemm_moe.h"),
+    "scaled_rows.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "upload.cuh", "gemm.h", "gemm_scaled.h"),
     "packed.cu": ("gemm.h", "gemm_scaled.h"),
-    "scaled.cu": ("scaled_few.cuh", "scaled_kernel.cuh", "rows.cuh", "join.cuh", "host.cuh", "ptx.cuh", "gemm.h", "gemm_scaled.h"),
+    "scaled.cu": ("scaled_few.cuh", "scaled_kernel.cuh", "rows.cuh", "join.cuh", "host.cuh", "upload.cuh", "ptx.cuh", "gemm.h", "gemm_scaled.h"),
 }
 SOURCES = [os.path.join(CSRC, f) for f in UNITS]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

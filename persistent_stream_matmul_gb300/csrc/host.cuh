@@ -8,6 +8,8 @@
 #include <chrono>
 #include <mutex>
 
+#include "upload.cuh"
+
 namespace psm {
 
 constexpr int64_t MAX_INDEX = (1ll << 31) - 1024;

@@ -216,8 +216,8 @@ gemm_status_t make_plan(gemm_scaled_plan_t* out, int64_t M, int64_t N, int64_t K
         delete p;
         return st;
     }
-    if (!offline && (cudaMalloc(&p->d_status, G_WORDS * sizeof(int)) != cudaSuccess ||
-                     cudaMemset(p->d_status, 0, G_WORDS * sizeof(int)) != cudaSuccess)) {
+    const int zeros[G_WORDS] = {};
+    if (!offline && (cudaMalloc(&p->d_status, sizeof(zeros)) != cudaSuccess || !upload(p->d_status, zeros, sizeof(zeros)))) {
         cudaGetLastError();
         if (p->d_status) cudaFree(p->d_status);
         delete p;
@@ -309,9 +309,7 @@ gemm_status_t gemm_scaled_plan_set_option(gemm_scaled_plan_t p, int key, int64_t
         if (p->offline) return GEMM_ERR_NO_DEVICE;
         DeviceGuard guard(p->device);
         const int word = (int)value + 1;
-        return guard.ok && cudaMemcpy(p->d_status + G_WORD_GIVE_UP, &word, sizeof(int), cudaMemcpyHostToDevice) == cudaSuccess
-                   ? GEMM_OK
-                   : GEMM_ERR_CUDA;
+        return guard.ok && upload(p->d_status + G_WORD_GIVE_UP, &word, sizeof(int)) ? GEMM_OK : GEMM_ERR_CUDA;
     }
     const int saved[2] = {p->opt_ctas, p->opt_form};
     if (key == GEMM_SCALED_OPT_CTAS) {
@@ -464,9 +462,7 @@ gemm_status_t gemm_scaled_last_status(gemm_scaled_plan_t p, gemm_stream_t stream
     // see changing under way
     static_assert(G_WORD_STATUS == 0 && G_WORD_TIMEOUTS == 1, "both words are written at once");
     const int words[2] = {0, p->timeouts + 1};
-    if (cudaDeviceSynchronize() != cudaSuccess ||
-        cudaMemcpy(p->d_status, words, sizeof(words), cudaMemcpyHostToDevice) != cudaSuccess)
-        return GEMM_ERR_CUDA;
+    if (cudaDeviceSynchronize() != cudaSuccess || !upload(p->d_status, words, sizeof(words))) return GEMM_ERR_CUDA;
     ++p->timeouts;
     return GEMM_ERR_TIMEOUT;
 }

@@ -95,7 +95,7 @@ struct ScaledCfg {
     static constexpr int SLOT_FLOATS = 128 * TILE_N;
     static constexpr int BARS = 2 * STAGES + 8 + 1 + 2 * S_QUEUE + 2 * S_SLOTS;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-    static_assert(TURNED || (PART / 32 % BOXES == 0 && PART / 16 % BOXES == 0), "boxes of a tile, 16 and 32 bits");
+    static_assert(PART / 32 % (BOXES ? BOXES : 1) == 0, "boxes of a tile of 16 bits; 32 bits have twice as many");
     static_assert(BARS * 8 + 32 <= BAR_BYTES, "barrier area");
 };
 
