@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpsm_gemm.so")
 # each translation unit and the headers it includes
 UNITS = {
-    "gemm.cu": ("gemm_kernel.cuh", "ptx.cuh", "sched.cuh", "gemm.h"),
+    "gemm.cu": ("gemm_kernel.cuh", "upload.cuh", "ptx.cuh", "sched.cuh", "gemm.h"),
     "moe.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "upload.cuh", "gemm.h", "gemm_moe.h"),
     "grouped.cu": ("grouped_kernel.cuh", "grouped_sched.cuh", "join.cuh", "host.cuh", "upload.cuh", "ptx.cuh", "gemm.h", "gemm_moe.h"),
     "scaled_rows.cu": ("ptx.cuh", "rows.cuh", "host.cuh", "upload.cuh", "gemm.h", "gemm_scaled.h"),

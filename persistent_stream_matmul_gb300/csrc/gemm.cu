@@ -14,6 +14,7 @@
 
 #include "gemm.h"
 #include "gemm_kernel.cuh"
+#include "upload.cuh"
 
 using namespace psm;
 
@@ -479,9 +480,12 @@ gemm_status_t derive(gemm_plan* p) {
                 }
                 p->raster_tiles = tiles;
             }
-            if (tiles > 0 && cudaMemcpy(p->raster_dev, p->raster_host->data(),
-                                        (size_t)tiles * sizeof(int32_t),
-                                        cudaMemcpyHostToDevice) != cudaSuccess)
+            // (after the runs that the default stream orders, which may read the table; and
+            // there on return, for runs on streams that it does not)
+            if (tiles > 0 && (cudaMemcpy(p->raster_dev, p->raster_host->data(),
+                                         (size_t)tiles * sizeof(int32_t),
+                                         cudaMemcpyHostToDevice) != cudaSuccess ||
+                              cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess))
                 return GEMM_ERR_CUDA;
         }
     }
@@ -624,8 +628,9 @@ gemm_status_t make_plan(gemm_plan_t* out, int64_t M, int64_t N, int64_t K, int d
         p->device = dev;
         p->num_sms = sms;
         p->max_pair_ctas = max_pair_ctas(dev);
+        const int zero = 0;
         if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess ||
-            cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
+            !upload(p->d_status, &zero, sizeof(int))) {
             if (p->d_status) cudaFree(p->d_status);
             delete p;
             return GEMM_ERR_CUDA;
@@ -1357,7 +1362,8 @@ gemm_status_t gemm_last_status(gemm_plan_t p, gemm_stream_t stream) {
     if (cudaMemcpy(&h, p->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
         return GEMM_ERR_CUDA;
     if (h != STATUS_OK) {
-        if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) return GEMM_ERR_CUDA;
+        const int zero = 0;
+        if (!upload(p->d_status, &zero, sizeof(int))) return GEMM_ERR_CUDA;
         return GEMM_ERR_TIMEOUT;
     }
     return GEMM_OK;

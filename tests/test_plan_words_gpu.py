@@ -63,3 +63,24 @@ def test_words_of_a_grouped_plan():
     torch.cuda.synchronize()
     assert q.last_status(stream) == B.GEMM_OK
     assert torch.equal(out, want)
+
+
+def test_timeout_of_a_new_plan_is_kept():
+    """The status of a 16-bit product's plan: a run that timed out while the default stream was still
+    behind the plan's creation."""
+    from gpu_util import Workspace
+    M, N, K = 128, 128, 4096
+    A, Bm, C = normal((M, K), torch.float16, 1), normal((K, N), torch.float16, 2), torch.zeros(M, N, dtype=torch.float16, device="cuda")
+    options = dict(tile_n=128, grid=4, wait_limit_us=2000)
+    p, stream = B.Plan(M, N, K, B.GEMM_F16, 0, 0, "streamk", **options), torch.cuda.Stream()
+    ws = Workspace().get(p.workspace_size)
+    p.run(A, Bm, C, ws)
+    assert p.last_status() == B.GEMM_OK
+    done = keep_busy()
+    q = B.Plan(M, N, K, B.GEMM_F16, 0, 0, "streamk", inject_skip_post=1, **options)
+    q.run(A, Bm, C, ws, stream)
+    stream.synchronize()
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert q.last_status(stream) == B.GEMM_ERR_TIMEOUT
+    assert q.last_status(stream) == B.GEMM_OK
