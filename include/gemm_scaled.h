@@ -190,6 +190,11 @@ enum {
  * layout_b; each with the kind of scales given.  C is M x N row-major of out_dtype
  * (GEMM_F16, GEMM_BF16 or GEMM_F32), rounded once.  Sums are in fp32: within a
  * group by the tensor cores, over the groups in ascending order.
+ * A form may multiply the two scales that meet, or a group's sum and one of them, first:
+ * where one of these products is neither 0 nor a normal number of fp32, the result may be
+ * less accurate, infinite or NaN.  Between operands as gemm_scaled_quantize makes them that takes
+ * groups whose largest elements have a product below 2^-94 (their part of C is then
+ * within 2^-111 all the same), or one above 2^128 or an element above 2^96.
  * The contiguous dimension of A and of B must be a multiple of 16.  A plan is
  * not thread-safe.
  * Errors: INVALID_ARG (NULL out, negative size, bad enum), UNSUPPORTED (a size >
