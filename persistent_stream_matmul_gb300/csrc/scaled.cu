@@ -72,14 +72,14 @@ bool prepared(int ctas, int turned, int col_vector, int dev) {
 }
 
 // Pairs of CTAs that can be resident at once: a cluster lives inside one GPC,
-// so this can be below #SMs / 2.  0 when unknown.
-int resident_pairs(int dev) {
+// so this can be below #SMs / 2.  0: pairs cannot run.
+int resident_pairs(int col_vector, int dev) {
     static std::mutex mu;
-    static int cache[64];
-    if (!prepared(2, 0, 0, dev)) return 0;
+    static int cache[64][2];
+    if (!prepared(2, 0, col_vector, dev)) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    if (cache[dev]) return cache[dev];
-    const Kernel k = kernel_of(2, 0, 0);
+    if (cache[dev][col_vector]) return cache[dev][col_vector];
+    const Kernel k = kernel_of(2, 0, col_vector);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(S_THREADS, 1, 1);
@@ -96,7 +96,7 @@ int resident_pairs(int dev) {
         cudaGetLastError();
         return 0;
     }
-    return cache[dev] = n;
+    return cache[dev][col_vector] = n;
 }
 
 gemm_status_t derive(gemm_scaled_plan* p) {
@@ -121,15 +121,17 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     // 4096 (56) 25.8 / 20.7, 1024 x 4096 x 4096 (64) 23.9 / 19.1.
     if (ctas == 0) ctas = form == GEMM_SCALED_STRAIGHT && cdiv(p->M, 256) * cdiv(p->N, 256) >= 48 ? 2 : 1;
     if ((form != GEMM_SCALED_STRAIGHT && ctas == 2) || (form == GEMM_SCALED_FEW && !few)) return GEMM_ERR_UNSUPPORTED;
-    const int turned = form != GEMM_SCALED_STRAIGHT;
+    const int turned = form != GEMM_SCALED_STRAIGHT, col_vector = turned || p->scale_b == GEMM_SCALE_VECTOR;
+    const int pairs = ctas == 2 && !p->offline ? resident_pairs(col_vector, p->device) : 0;
+    if (ctas == 2 && !p->offline && pairs == 0) {
+        if (p->opt_ctas == 2) return GEMM_ERR_UNSUPPORTED;
+        ctas = 1;
+    }
     const int64_t lanes = turned ? p->N : p->M, cols = turned ? p->M : p->N;
     const int tile = 128 * ctas;
     ScaledShape s{};
     int64_t units = p->num_sms / ctas;
-    if (ctas == 2 && !p->offline) {
-        const int n = resident_pairs(p->device);
-        if (n > 0) units = std::min<int64_t>(units, n);
-    }
+    if (pairs > 0) units = std::min<int64_t>(units, pairs);
     const int64_t tiles_l = cdiv(lanes, tile), side = cdiv(cols, tile), tiles = tiles_l * side, kb = cdiv(p->K, S_BK);
     if (tiles > MAX_INDEX) return GEMM_ERR_UNSUPPORTED;
     s.tiles = (int32_t)tiles;
@@ -160,7 +162,7 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     p->form = form;
     p->ctas = ctas;
     p->turned = turned;
-    p->col_vector = turned || p->scale_b == GEMM_SCALE_VECTOR;
+    p->col_vector = col_vector;
     p->shape = s;
     p->counter_bytes = p->ws_bytes = 0;
     if (form != GEMM_SCALED_FEW && s.shares > 1) {
