@@ -136,3 +136,27 @@ def test_nan_infinity_and_zeros():
     got, scales, _ = run(x, torch.ones(H, device="cuda").bfloat16(), "e4m3", eps=0.0)
     assert torch.equal(torch.isnan(got).all(1), torch.isnan(got).any(1))
     assert torch.isnan(got).any(1).tolist() == [False, True, True, False, False, False]
+
+
+@pytest.mark.parametrize("type", ["e4m3", "e5m2"])
+def test_quotients_next_to_a_border(type):
+    """fp16: s is chosen for each element so that s * weight * L / m is as near to a border as it gets without being
+    on it; dozens are within half of fp32's last digit of one."""
+    rows, H = 512, 1024
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = torch.randint(1024, 2048, (H,), generator=g, device="cuda").double()
+    top = torch.randint(1024, 2048, (rows, H // 128), generator=g, device="cuda").double()
+    m = (top * w[::128]).repeat_interleave(128, 1)                    # of each element's group
+    digits = 4 if type == "e4m3" else 3
+    best, near = torch.full((rows, H), 1024.0, dtype=torch.float64, device="cuda"), torch.ones(rows, H, dtype=torch.float64, device="cuda")
+    for t in range(2 ** digits + 1, 2 ** (digits + 1), 2):           # 1.xxx1 times a power of two
+        s = t * m / (7 * w)
+        s = s * torch.exp2(10 - torch.floor(torch.log2(s)))           # 11 bits before the point
+        r = torch.round(s)
+        d = (r - s).abs() / s
+        ok = (d > 2.0 ** -40) & (d < near) & (r < 2048)
+        best, near = torch.where(ok, r, best), torch.where(ok, d, near)
+    assert int((near < 2.0 ** -25).sum()) > 10
+    x = best / 4
+    x[:, ::128] = top
+    check(x.half(), (w / 1024).half(), type)
