@@ -245,7 +245,8 @@ gemm_status_t gemm_scaled_run(gemm_scaled_plan_t plan, const void *A, const floa
  * wrong between the timeout and this call. */
 gemm_status_t gemm_scaled_last_status(gemm_scaled_plan_t plan, gemm_stream_t stream);
 
-/* Free the plan.  NULL is accepted.  Always returns GEMM_OK. */
+/* Free the plan and its words on the device: no run of it is under way, and captured ones are not
+ * replayed any more.  NULL is accepted.  Always returns GEMM_OK. */
 gemm_status_t gemm_scaled_plan_destroy(gemm_scaled_plan_t plan);
 
 #ifdef __cplusplus

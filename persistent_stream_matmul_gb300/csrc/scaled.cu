@@ -101,7 +101,10 @@ int resident_pairs(int col_vector, int dev) {
 
 gemm_status_t derive(gemm_scaled_plan* p) {
     const bool few = p->layout_a == GEMM_ROW_MAJOR && p->layout_b == GEMM_COL_MAJOR && cdiv(p->M, F_MOST_ROWS) <= 65535;
-    // Without tensor memory: up to 16 rows always, more while the product is small. On tensor
+    // Without tensor memory: up to 16 rows always, more while the product is small. (us of 2, 8,
+    // 12 and 16 rows, without against with: 14336 x 4096 14.2 / 15.7, 14.7 / 15.9, 17.8 / 16.0, 18.2 /
+    // 15.9; 4096 x 14336 14.3 / 17.9, 14.4 / 18.0, 18.1 / 18.1, 18.3 / 18.2. So from 9 rows on it
+    // loses up to 12 % on large matrices, and wins on smaller ones.) On tensor
     // memory it takes 5 us with few k-blocks and 8 to 12 with more, however small; without,
     // each 32 rows of A read B again and each 16 rows of B read those. us, without against
     // with: 24 x 1536 x 2048 3.6 / 9.3, 24 x 4096 x 4096 8.4 / 11.3, 32 x 4096 x 4096 10.5 /
@@ -118,7 +121,9 @@ gemm_status_t derive(gemm_scaled_plan* p) {
     if (form < 0) form = ctas == 2 ? GEMM_SCALED_STRAIGHT : few && small ? GEMM_SCALED_FEW : p->M <= 32 ? GEMM_SCALED_TURNED : GEMM_SCALED_STRAIGHT;
     // Pairs read their operands half as often, single CTAs make four times the tiles: us,
     // single against pairs, 512 x 4096 x 4096 (32 pair tiles) 14.0 / 19.7, 256 x 14336 x
-    // 4096 (56) 25.8 / 20.7, 1024 x 4096 x 4096 (64) 23.9 / 19.1.
+    // 4096 (56) 25.8 / 20.7, 1024 x 4096 x 4096 (64) 23.9 / 19.1. Where a round of the 76 pairs is
+    // partly empty they are near: K of 1024, 1536, 4096 with 80 tiles 12.7 / 13.8, 16.7 / 17.2, 34.7 / 34.0,
+    // with 112 12.9 / 14.1, 16.7 / 17.5, 36.0 / 35.5, with 144 15.9 / 15.0, 20.9 / 18.2, 46.1 / 35.0.
     if (ctas == 0) ctas = form == GEMM_SCALED_STRAIGHT && cdiv(p->M, 256) * cdiv(p->N, 256) >= 48 ? 2 : 1;
     if ((form != GEMM_SCALED_STRAIGHT && ctas == 2) || (form == GEMM_SCALED_FEW && !few)) return GEMM_ERR_UNSUPPORTED;
     const int turned = form != GEMM_SCALED_STRAIGHT, col_vector = turned || p->scale_b == GEMM_SCALE_VECTOR;

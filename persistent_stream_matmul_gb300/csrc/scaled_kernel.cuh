@@ -36,8 +36,8 @@
 //
 // What bounds it.  Large products: the epilogue's chain at every k-block (barrier, two
 // loads of some 100 cycles, additions), 840 cycles where the tensor cores need 512 and the
-// operands' way through shared memory 640: 8192 x 14336 x 4096 takes 342 to 395 us (2.4 to 2.8
-// PFLOP/s), with a scale a column 440 to 480 for as many products (14336 x 4096 x 8192). Small
+// operands' way through shared memory 640: 8192 x 14336 x 4096 takes 342 to 402 us (2.4 to 2.8
+// PFLOP/s), with a scale a column 440 to 483 for as many products (14336 x 4096 x 8192). Small
 // ones: 2 us to the first copy, and 3 to join split tiles: 96 x 4096 x 14336 takes 20 us,
 // 2.9 TB/s.
 //

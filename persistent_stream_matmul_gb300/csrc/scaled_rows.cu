@@ -220,7 +220,7 @@ struct QuantizeArgs {
     float* scales_cols;
 };
 
-// Vectors along the rows (8192 x 4096 in 21.7 us, 4.7 TB/s): 16 lanes a group, a block takes R rows and its 16 / R
+// Vectors along the rows (8192 x 4096 in 21.9 us, 4.7 TB/s; issue slots 69 % busy): 16 lanes a group, a block takes R rows and its 16 / R
 // half-warps a row, U groups each.
 template <typename T, bool E5M2, bool ALIGNED, int R, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantizeArgs a) {
 // dimensions.  A thread has eight columns of eight rows, 16 apart, which stay in
 // registers between the magnitudes and the output, so the matrix is read once.  Blocks an
 // SM: bytes in flight against registers that spill.  us with 2, 3, 4: blocks of 14336 x 4096
-// 40.8 / 35.1 / 33.4, columns of 8192 x 4096 25.2 / 23.9 / 23.3, both 39.8 / 44.7 / 48.8, which
-// is bound by its two conversions of every element (since, with a cheaper rounding, 31.4 at
-// 5.6 TB/s, 21.8 and 36.2).
+// 40.8 / 35.1 / 33.4, columns of 8192 x 4096 25.2 / 23.9 / 23.3, both 39.8 / 44.7 / 48.8 (since,
+// with a cheaper rounding, 31.1 at 5.7 TB/s, 21.7 and 36.5).  With both, latency: two blocks of 106
+// registers a thread leave issue slots half empty.
 template <typename T, bool E5M2, bool ALIGNED, int KIND, bool BOTH>
 __global__ void __launch_bounds__(256, BOTH ? 2 : 4) quantize_tile_kernel(QuantizeArgs a) {
     __shared__ float part[8][GROUP];
@@ -431,7 +431,8 @@ __device__ __forceinline__ Chunk load_masked(const uint16_t* row, int h, int n) 
 }
 
 // A row of `blockDim.x` threads, V chunks each, strided by blockDim.x, so that
-// 16 lanes have a group.  Bound by memory.  The row stays in registers between the
+// 16 lanes have a group.  Bound by instructions (issue slots 70 % busy with 8-bit output) as much as
+// by memory.  The row stays in registers between the
 // sum and the output, and so does the weight over all the rows that a block takes
 // (every gridDim.x x blockDim.y th); AHEAD: the next row is on its way while this
 // one is summed and written, which keeps reads in flight over the barrier.  8192 rows of
